@@ -370,6 +370,80 @@ k3moe_status k3moe_cache_reset(k3moe_cache *cache, void *stream);
  * accepted. */
 void k3moe_cache_destroy(k3moe_cache *cache);
 
+/* Dense operators beside the expert layer: what the rest of a decoder needs
+ * of the same formats. They have no handle and no workspace; they run on the
+ * current HIP device, whose memory every pointer must address, allocate
+ * nothing and may be captured into a graph. Row strides are in elements and
+ * are not read for T == 1; rows may be wider than what is used of them, and
+ * nothing outside the stated rows and columns is written. Outputs must not
+ * overlap inputs or each other (h and, with K3MOE_OUT_F32_ADD, out are both).
+ * Deterministic: the same call gives the same bits. T == 0 does nothing.
+ *
+ * MXFP8 tokens: e4m3 values [T][W] and E8M0 bytes [T][ceil(W/32)], a token's
+ * value being e4m3 * 2^(byte - 127). Written so: per 32 consecutive values of
+ * a row (the last group may be shorter) the smallest power of two 2^s, s >=
+ * -127, with max|v| <= 448 * 2^s, byte s + 127, e4m3_RNE(v / 2^s). A value that
+ * is not finite is written as NaN and takes no part in the maximum. Read so:
+ * byte 255 makes its group of values zero, as in the MXFP4 weights. */
+
+/* What k3moe_add_norm adds to the stream. */
+typedef enum {
+    K3MOE_ADD_NONE = 0, /* d is NULL, h is only read */
+    K3MOE_ADD_BF16 = 1,
+    K3MOE_ADD_F32 = 2
+} k3moe_add;
+
+/* The residual addition and the norm behind it, for T tokens of width H (any
+ * H >= 1):
+ *   h[t] += d[t]                                  fp32, one rounding
+ *   v = h[t] * inv * gamma, inv = (float)(1 / sqrt(sum h^2 / H + eps))
+ *       (the numbers of k3moe_step's norm: fp64 sum, two fp32 products)
+ *   x[t] = bf16_RNE(v);  q[t], qs[t] = MXFP8(v)
+ *   h      fp32 [T][H]  in/out (only read with K3MOE_ADD_NONE)
+ *   d      bf16 or fp32 [T][H] by d_kind (k3moe_add), NULL for none
+ *   gamma  fp32 [H];  eps > 0 and finite, else K3MOE_E_INVALID_ARG
+ *   x      bf16 [T][H]           out (optional, NULL = not written)
+ *   q, qs  e4m3 [T][H] and E8M0 [T][ceil(H/32)]  out (optional, both or neither);
+ *          x, q or both must be given
+ * Bases need only their elements' alignment; 16-byte aligned bases and strides
+ * and H in multiples of 4 take wider loads. */
+k3moe_status k3moe_add_norm(float *h, int64_t h_stride, const void *d, int32_t d_kind, int64_t d_stride,
+                            int32_t T, int32_t H, const float *gamma, float eps, uint16_t *x,
+                            int64_t x_stride, uint8_t *q, int64_t q_stride, uint8_t *qs,
+                            int64_t qs_stride, void *stream);
+
+/* What a dense product does with its result y. */
+typedef enum {
+    K3MOE_OUT_BF16 = 1,    /* out bf16 [T][rows] = bf16_RNE(y)                       */
+    K3MOE_OUT_F32 = 2,     /* out fp32 [T][rows] = y                                 */
+    K3MOE_OUT_F32_ADD = 3, /* out fp32 [T][rows] += y, once (k3moe_linear only)      */
+    K3MOE_OUT_MXFP8 = 4    /* out e4m3 [T][rows], outs E8M0 [T][ceil(rows/32)]       */
+} k3moe_out;
+
+/* y[t][n] = sum_k W[n][k] x[t][k] with an MXFP4 matrix of rows x cols (packed
+ * nibbles [rows][cols/2], scales [rows][cols/32], both 16-byte aligned; the
+ * format of k3moe_mxfp4). rows >= 1; cols a multiple of 32
+ * (K3MOE_E_UNSUPPORTED_SHAPE otherwise).
+ *   x   bf16 [T][cols], or e4m3 [T][cols] with xs E8M0 [T][cols/32] (xs NULL =
+ *       bf16); 16-byte aligned rows
+ *   out, outs  as out_kind (k3moe_out) says; outs NULL unless K3MOE_OUT_MXFP8
+ * Products are exact and summed in fp32. */
+k3moe_status k3moe_linear(const uint8_t *packed, const uint8_t *scales, int32_t rows, int32_t cols,
+                          const void *x, int64_t x_stride, const uint8_t *xs, int64_t xs_stride,
+                          int32_t T, void *out, int64_t out_stride, uint8_t *outs,
+                          int64_t outs_stride, int32_t out_kind, void *stream);
+
+/* The gated first half of a dense MLP: act(W1 x, W3 x) with two matrices of
+ * rows x cols, the activation as a layer's config has it: act, and for SiTU
+ * its betas (> 0, finite). Other arguments as k3moe_linear; K3MOE_OUT_F32_ADD is
+ * refused. */
+k3moe_status k3moe_glu(const uint8_t *gate_packed, const uint8_t *gate_scales,
+                       const uint8_t *up_packed, const uint8_t *up_scales, int32_t rows,
+                       int32_t cols, const void *x, int64_t x_stride, const uint8_t *xs,
+                       int64_t xs_stride, int32_t T, int32_t act, float situ_b1, float situ_b2,
+                       void *out, int64_t out_stride, uint8_t *outs, int64_t outs_stride,
+                       int32_t out_kind, void *stream);
+
 /* Frees the handle and its error counter (synchronises the device first).
  * NULL is accepted. */
 void k3moe_layer_destroy(k3moe_layer *layer);

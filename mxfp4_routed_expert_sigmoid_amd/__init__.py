@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(PKG, "libk3moe.so")
 
 ABI_VERSION = 3
 ACT_SITU, ACT_SWIGLU = 1, 2
+ADD_NONE, ADD_BF16, ADD_F32 = 0, 1, 2
+OUT_BF16, OUT_F32, OUT_F32_ADD, OUT_MXFP8 = 1, 2, 3, 4
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "invalid or incomplete config",
           3: "unsupported shape", 4: "pointer or stride not aligned",
@@ -65,7 +67,8 @@ EXPORTS = ("k3moe_layer_create", "k3moe_workspace_size", "k3moe_route", "k3moe_f
            "k3moe_cache_create", "k3moe_cache_device_bytes", "k3moe_cache_workspace_size",
            "k3moe_cache_forward", "k3moe_cache_stats_read", "k3moe_cache_slots", "k3moe_cache_reset", "k3moe_cache_destroy",
            "k3moe_error_count", "k3moe_error_reset", "k3moe_profile_enable",
-           "k3moe_profile_read", "k3moe_layer_destroy", "k3moe_status_string")
+           "k3moe_profile_read", "k3moe_layer_destroy", "k3moe_status_string",
+           "k3moe_add_norm", "k3moe_linear", "k3moe_glu")
 STAGES = ("router", "topk", "perm", "gateup", "shared_gateup", "down", "combine",
           "latent_in", "latent_out", "prenorm", "cache_plan", "cache_fill", "gateup_tiles",
           "down_tiles")
@@ -124,6 +127,13 @@ def lib():
         L.k3moe_layer_destroy.argtypes = [P]
         L.k3moe_status_string.restype = ctypes.c_char_p
         L.k3moe_status_string.argtypes = [st]
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        L.k3moe_add_norm.restype = st
+        L.k3moe_add_norm.argtypes = [P, i64, P, i32, i64, i32, i32, P, f32, P, i64, P, i64, P, i64, P]
+        L.k3moe_linear.restype = st
+        L.k3moe_linear.argtypes = [P, P, i32, i32, P, i64, P, i64, i32, P, i64, P, i64, i32, P]
+        L.k3moe_glu.restype = st
+        L.k3moe_glu.argtypes = [P, P, P, P, i32, i32, P, i64, P, i64, i32, i32, f32, f32, P, i64, P, i64, i32, P]
         _lib = L
     return _lib
 
@@ -439,3 +449,127 @@ class Cache:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------------------
+# Dense operators (k3moe_add_norm, k3moe_linear, k3moe_glu): functions over
+# device tensors. Rows may be views of wider buffers (unit stride in a row).
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values or their bit patterns
+_F32 = (torch.float32,)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_E8M0 = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _mat(t, shape, dtypes, name, dev):
+    """Refuse anything but a [rows][width] tensor of `shape` (None: any rows)
+    and of one of `dtypes` on `dev`, unit stride within a row. Returns its
+    address and row stride (its width, for fewer than two rows)."""
+    s = t.shape
+    if len(s) != 2 or s[1] != shape[1] or (shape[0] is not None and s[0] != shape[0]):
+        raise ValueError(f"{name}: shape {tuple(s)}, expected {tuple('T' if n is None else n for n in shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    st, w = t.stride(), s[1]
+    if st[1] != 1 and w > 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    if s[0] > 1 and st[0] < w:
+        raise ValueError(f"{name}: rows overlap (stride {st[0]}, width {w})")
+    return t.data_ptr(), st[0] if s[0] > 1 else w
+
+
+def _call(fn, what, dev, stream, *args):
+    """fn(*args, stream) with `dev` current."""
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(fn(*args, s.cuda_stream), what)
+    else:
+        _check(fn(*args, s.cuda_stream), what)
+
+
+def add_norm(h, gamma, eps, d=None, x=None, q=None, qs=None, stream=None):
+    """k3moe_add_norm: h fp32 [T][H] += d (bf16 or fp32 [T][H], optional), in
+    place; the RMS norm of the new h times gamma fp32 [H] written to x (bf16
+    [T][H]) and / or to q, qs (e4m3 [T][H], E8M0 [T][ceil(H/32)])."""
+    if h.dim() != 2:
+        raise ValueError(f"h: shape {tuple(h.shape)}, expected [T][H]")
+    T, H = h.shape
+    dev = h.device
+    hp, hst = _mat(h, (T, H), _F32, "h", dev)
+    _shape(gamma, (H,), "gamma")
+    gp, _ = _mat(gamma.unsqueeze(0), (1, H), _F32, "gamma", dev)
+    dp, dst, dk = None, 0, ADD_NONE
+    if d is not None:
+        dp, dst = _mat(d, (T, H), _BF16 + _F32, "d", dev)
+        dk = ADD_F32 if d.dtype == torch.float32 else ADD_BF16
+    xp = qp = qsp = None
+    xst = qst = qsst = 0
+    if x is not None:
+        xp, xst = _mat(x, (T, H), _BF16, "x", dev)
+    if (q is None) != (qs is None):
+        raise ValueError("q and qs go together")
+    if q is not None:
+        qp, qst = _mat(q, (T, H), _E4M3, "q", dev)
+        qsp, qsst = _mat(qs, (T, (H + 31) // 32), _E8M0, "qs", dev)
+    _call(lib().k3moe_add_norm, "k3moe_add_norm", dev, stream, hp, hst, dp, dk, dst, T, H, gp, eps, xp, xst,
+          qp, qst, qsp, qsst)
+
+
+def _weight(packed, scales, name, dev):
+    """Addresses of an MXFP4 matrix: packed uint8 [N][K/2], scales [N][K/32]."""
+    _dev(packed, (1,), name + "packed")
+    if packed.dim() != 2 or packed.shape[1] % 16:
+        raise ValueError(f"{name}packed: shape {tuple(packed.shape)}, expected [rows][cols/2], cols a multiple of 32")
+    _shape(scales, (packed.shape[0], packed.shape[1] // 16), name + "scales")
+    _dev(scales, (1,), name + "scales")
+    if packed.device != dev or scales.device != dev:
+        raise ValueError(f"{name}packed and scales must be on {dev}")
+    return packed.data_ptr(), scales.data_ptr()
+
+
+def _dense(x, xs, out, outs, N, K, accumulate):
+    """Checked token and result arguments of a dense product."""
+    dev = x.device
+    xp, xst = _mat(x, (None, K), _BF16 if xs is None else _E4M3, "x", dev)
+    T = x.shape[0]
+    xsp, xsst = (None, 0) if xs is None else _mat(xs, (T, K // 32), _E8M0, "xs", dev)
+    if outs is not None:
+        op, ost = _mat(out, (T, N), _E4M3, "out", dev)
+        osp, osst = _mat(outs, (T, (N + 31) // 32), _E8M0, "outs", dev)
+        kind = OUT_MXFP8
+    else:
+        op, ost = _mat(out, (T, N), _F32 if accumulate else _BF16 + _F32, "out", dev)
+        osp, osst = None, 0
+        kind = OUT_F32_ADD if accumulate else OUT_F32 if out.dtype == torch.float32 else OUT_BF16
+    return T, (xp, xst, xsp, xsst), (op, ost, osp, osst, kind)
+
+
+def linear(packed, scales, x, out, xs=None, outs=None, accumulate=False, stream=None):
+    """k3moe_linear: out [T][N] = x W^T, W the MXFP4 matrix packed uint8
+    [N][K/2], scales [N][K/32]. x is bf16 [T][K], or e4m3 [T][K] with its E8M0
+    bytes xs [T][K/32]. out is bf16 or fp32 by its type, e4m3 with its E8M0
+    bytes outs [T][ceil(N/32)]; accumulate adds into an fp32 out."""
+    dev = x.device
+    wp, sp = _weight(packed, scales, "", dev)
+    N, K = packed.shape[0], 2 * packed.shape[1]
+    if accumulate and outs is not None:
+        raise ValueError("accumulate takes an fp32 out")
+    T, tok, res = _dense(x, xs, out, outs, N, K, accumulate)
+    _call(lib().k3moe_linear, "k3moe_linear", dev, stream, wp, sp, N, K, *tok, T, *res)
+
+
+def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=None, act=ACT_SITU,
+        situ_b1=4.0, situ_b2=25.0, stream=None):
+    """k3moe_glu: out [T][N] = act(x W1^T, x W3^T), W1 and W3 the MXFP4
+    matrices gate and up; tokens and results as in ``linear``."""
+    dev = x.device
+    gp, gs = _weight(gate_packed, gate_scales, "gate_", dev)
+    _shape(up_packed, gate_packed.shape, "up_packed")
+    up, us = _weight(up_packed, up_scales, "up_", dev)
+    N, K = gate_packed.shape[0], 2 * gate_packed.shape[1]
+    T, tok, res = _dense(x, xs, out, outs, N, K, False)
+    _call(lib().k3moe_glu, "k3moe_glu", dev, stream, gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res)
