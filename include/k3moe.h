@@ -422,8 +422,8 @@ typedef enum {
 
 /* y[t][n] = sum_k W[n][k] x[t][k] with an MXFP4 matrix of rows x cols (packed
  * nibbles [rows][cols/2], scales [rows][cols/32], both 16-byte aligned; the
- * format of k3moe_mxfp4). rows >= 1; cols a multiple of 32
- * (K3MOE_E_UNSUPPORTED_SHAPE otherwise).
+ * format of k3moe_mxfp4). rows >= 1; cols a multiple of 32, at
+ * most 2^22 (K3MOE_E_UNSUPPORTED_SHAPE otherwise).
  *   x   bf16 [T][cols], or e4m3 [T][cols] with xs E8M0 [T][cols/32] (xs NULL =
  *       bf16); 16-byte aligned rows
  *   out, outs  as out_kind (k3moe_out) says; outs NULL unless K3MOE_OUT_MXFP8

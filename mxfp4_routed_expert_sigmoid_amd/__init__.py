@@ -460,35 +460,48 @@ _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _E8M0 = (torch.float8_e8m0fnu, torch.uint8)
 
 
-def _mat(t, shape, dtypes, name, dev):
-    """Refuse anything but a [rows][width] tensor of `shape` (None: any rows)
-    and of one of `dtypes` on `dev`, unit stride within a row. Returns its
-    address and row stride (its width, for fewer than two rows)."""
-    s = t.shape
-    if len(s) != 2 or s[1] != shape[1] or (shape[0] is not None and s[0] != shape[0]):
-        raise ValueError(f"{name}: shape {tuple(s)}, expected {tuple('T' if n is None else n for n in shape)}")
+def _mat(t, rows, width, dtypes, name, dev):
+    """Refuse anything but a [rows][width] tensor of one of `dtypes` on device
+    number `dev`, unit stride within a row. Returns its address and row stride
+    (its width, for fewer than two rows). These calls take about 5 us on the
+    device for one token, so the checks use the cheapest accessors."""
+    if tuple(t.shape) != (rows, width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, width)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    st, w = t.stride(), s[1]
-    if st[1] != 1 and w > 1:
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{dev}" if dev >= 0 else "a GPU"))
+    st, unit = t.stride()
+    if unit != 1 and width > 1:
         raise ValueError(f"{name}: a row must be contiguous")
-    if s[0] > 1 and st[0] < w:
-        raise ValueError(f"{name}: rows overlap (stride {st[0]}, width {w})")
-    return t.data_ptr(), st[0] if s[0] > 1 else w
+    if rows < 2:
+        return t.data_ptr(), width
+    if st < width:
+        raise ValueError(f"{name}: rows overlap (stride {st}, width {width})")
+    return t.data_ptr(), st
+
+
+def _vec(t, n, name, dev):
+    """The address of an fp32 [n] tensor on device number `dev`."""
+    if tuple(t.shape) != (n,) or t.dtype != torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous float32 ({n},)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
 
 
 def _call(fn, what, dev, stream, *args):
-    """fn(*args, stream) with `dev` current."""
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if dev.index != torch.cuda.current_device():
+    """fn(*args, stream) with device number `dev` current, on its current
+    stream unless one is given (taken as a raw handle: making a Stream object
+    costs more than the rest of a call)."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            _check(fn(*args, s.cuda_stream), what)
+            status = fn(*args, s)
     else:
-        _check(fn(*args, s.cuda_stream), what)
+        status = fn(*args, s)
+    if status:
+        raise K3MoeError(status, what)
 
 
 def add_norm(h, gamma, eps, d=None, x=None, q=None, qs=None, stream=None):
@@ -498,54 +511,57 @@ def add_norm(h, gamma, eps, d=None, x=None, q=None, qs=None, stream=None):
     if h.dim() != 2:
         raise ValueError(f"h: shape {tuple(h.shape)}, expected [T][H]")
     T, H = h.shape
-    dev = h.device
-    hp, hst = _mat(h, (T, H), _F32, "h", dev)
-    _shape(gamma, (H,), "gamma")
-    gp, _ = _mat(gamma.unsqueeze(0), (1, H), _F32, "gamma", dev)
+    dev = h.get_device()
+    hp, hst = _mat(h, T, H, _F32, "h", dev)
+    gp = _vec(gamma, H, "gamma", dev)
     dp, dst, dk = None, 0, ADD_NONE
     if d is not None:
-        dp, dst = _mat(d, (T, H), _BF16 + _F32, "d", dev)
+        dp, dst = _mat(d, T, H, _BF16 + _F32, "d", dev)
         dk = ADD_F32 if d.dtype == torch.float32 else ADD_BF16
     xp = qp = qsp = None
     xst = qst = qsst = 0
     if x is not None:
-        xp, xst = _mat(x, (T, H), _BF16, "x", dev)
+        xp, xst = _mat(x, T, H, _BF16, "x", dev)
     if (q is None) != (qs is None):
         raise ValueError("q and qs go together")
     if q is not None:
-        qp, qst = _mat(q, (T, H), _E4M3, "q", dev)
-        qsp, qsst = _mat(qs, (T, (H + 31) // 32), _E8M0, "qs", dev)
+        qp, qst = _mat(q, T, H, _E4M3, "q", dev)
+        qsp, qsst = _mat(qs, T, (H + 31) // 32, _E8M0, "qs", dev)
     _call(lib().k3moe_add_norm, "k3moe_add_norm", dev, stream, hp, hst, dp, dk, dst, T, H, gp, eps, xp, xst,
           qp, qst, qsp, qsst)
 
 
+_U8 = (torch.uint8,)
+
+
 def _weight(packed, scales, name, dev):
     """Addresses of an MXFP4 matrix: packed uint8 [N][K/2], scales [N][K/32]."""
-    _dev(packed, (1,), name + "packed")
     if packed.dim() != 2 or packed.shape[1] % 16:
         raise ValueError(f"{name}packed: shape {tuple(packed.shape)}, expected [rows][cols/2], cols a multiple of 32")
-    _shape(scales, (packed.shape[0], packed.shape[1] // 16), name + "scales")
-    _dev(scales, (1,), name + "scales")
-    if packed.device != dev or scales.device != dev:
-        raise ValueError(f"{name}packed and scales must be on {dev}")
-    return packed.data_ptr(), scales.data_ptr()
+    N, half = packed.shape
+    pp, pst = _mat(packed, N, half, _U8, name + "packed", dev)
+    sp, sst = _mat(scales, N, half // 16, _E8M0, name + "scales", dev)
+    if pst != half or sst != half // 16:
+        raise ValueError(f"{name}packed and scales must be contiguous")
+    return pp, sp
 
 
-def _dense(x, xs, out, outs, N, K, accumulate):
+def _dense(x, xs, out, outs, N, K, accumulate, dev):
     """Checked token and result arguments of a dense product."""
-    dev = x.device
-    xp, xst = _mat(x, (None, K), _BF16 if xs is None else _E4M3, "x", dev)
     T = x.shape[0]
-    xsp, xsst = (None, 0) if xs is None else _mat(xs, (T, K // 32), _E8M0, "xs", dev)
-    if outs is not None:
-        op, ost = _mat(out, (T, N), _E4M3, "out", dev)
-        osp, osst = _mat(outs, (T, (N + 31) // 32), _E8M0, "outs", dev)
-        kind = OUT_MXFP8
+    if xs is None:
+        xp, xst = _mat(x, T, K, _BF16, "x", dev)
+        xsp, xsst = None, 0
     else:
-        op, ost = _mat(out, (T, N), _F32 if accumulate else _BF16 + _F32, "out", dev)
-        osp, osst = None, 0
-        kind = OUT_F32_ADD if accumulate else OUT_F32 if out.dtype == torch.float32 else OUT_BF16
-    return T, (xp, xst, xsp, xsst), (op, ost, osp, osst, kind)
+        xp, xst = _mat(x, T, K, _E4M3, "x", dev)
+        xsp, xsst = _mat(xs, T, K // 32, _E8M0, "xs", dev)
+    if outs is not None:
+        op, ost = _mat(out, T, N, _E4M3, "out", dev)
+        osp, osst = _mat(outs, T, (N + 31) // 32, _E8M0, "outs", dev)
+        return T, (xp, xst, xsp, xsst), (op, ost, osp, osst, OUT_MXFP8)
+    op, ost = _mat(out, T, N, _F32 if accumulate else _BF16 + _F32, "out", dev)
+    kind = OUT_F32_ADD if accumulate else OUT_F32 if out.dtype == torch.float32 else OUT_BF16
+    return T, (xp, xst, xsp, xsst), (op, ost, None, 0, kind)
 
 
 def linear(packed, scales, x, out, xs=None, outs=None, accumulate=False, stream=None):
@@ -553,12 +569,12 @@ def linear(packed, scales, x, out, xs=None, outs=None, accumulate=False, stream=
     [N][K/2], scales [N][K/32]. x is bf16 [T][K], or e4m3 [T][K] with its E8M0
     bytes xs [T][K/32]. out is bf16 or fp32 by its type, e4m3 with its E8M0
     bytes outs [T][ceil(N/32)]; accumulate adds into an fp32 out."""
-    dev = x.device
+    dev = x.get_device()
     wp, sp = _weight(packed, scales, "", dev)
     N, K = packed.shape[0], 2 * packed.shape[1]
     if accumulate and outs is not None:
         raise ValueError("accumulate takes an fp32 out")
-    T, tok, res = _dense(x, xs, out, outs, N, K, accumulate)
+    T, tok, res = _dense(x, xs, out, outs, N, K, accumulate, dev)
     _call(lib().k3moe_linear, "k3moe_linear", dev, stream, wp, sp, N, K, *tok, T, *res)
 
 
@@ -566,10 +582,10 @@ def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=No
         situ_b1=4.0, situ_b2=25.0, stream=None):
     """k3moe_glu: out [T][N] = act(x W1^T, x W3^T), W1 and W3 the MXFP4
     matrices gate and up; tokens and results as in ``linear``."""
-    dev = x.device
+    dev = x.get_device()
     gp, gs = _weight(gate_packed, gate_scales, "gate_", dev)
     _shape(up_packed, gate_packed.shape, "up_packed")
     up, us = _weight(up_packed, up_scales, "up_", dev)
     N, K = gate_packed.shape[0], 2 * gate_packed.shape[1]
-    T, tok, res = _dense(x, xs, out, outs, N, K, False)
+    T, tok, res = _dense(x, xs, out, outs, N, K, False, dev)
     _call(lib().k3moe_glu, "k3moe_glu", dev, stream, gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res)

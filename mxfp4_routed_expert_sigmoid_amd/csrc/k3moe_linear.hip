@@ -19,6 +19,10 @@
 namespace k3moe {
 namespace {
 
+// Widest matrix: a block's rows are addressed by 32-bit offsets (256 rows x
+// 2^22 / 2 bytes).
+constexpr int kMaxCols = 1 << 22;
+
 struct DenseParams {
     const uint8_t *w[2], *ws[2];   // packed rows [N][K / 2], scale rows [N][K / 32] (one or two matrices)
     const void *x;
@@ -30,7 +34,17 @@ struct DenseParams {
     int kind;                      // k3moe_out
     int act;
     float b1, b2;
+    bool vec;                      // four neighbouring results may be stored at once
 };
+
+// A dropped group (byte 255, or a block past the row's last) is cleared by
+// masks, so that no lane branches: keep is 0 for it, all ones otherwise.
+__device__ __forceinline__ uint32_t keep_mask(uint32_t s, uint32_t past) { return (s == 255u ? 0u : ~0u) & ~past; }
+__device__ __forceinline__ u4 and_u4(u4 v, uint32_t m) { return u4{v.x & m, v.y & m, v.z & m, v.w & m}; }
+
+// The converters' scale operand for byte s < 255: they read its exponent
+// field, and a field of 0 as 2^-127.
+__device__ __forceinline__ float scale_f32(uint32_t s) { return __uint_as_float(s << 23); }
 
 __device__ __forceinline__ bf8 expand8_fp8(uint32_t lo, uint32_t hi, float scale)
 {
@@ -95,21 +109,22 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_
 
     for (int c = wave; c < NC; c += kStW) {
         const int kb = 4 * c + g;
-        const bool ok = kb < KB;   // past the last block: zeros on both sides
-        const int kc = ok ? kb : KB - 1;
+        const uint32_t past = kb < KB ? 0u : ~0u;   // past the last block: zeros on both sides
+        const int kc = min(kb, KB - 1);
         bf8 b[4];
         if constexpr (X8) {
             const u4 *xp = reinterpret_cast<const u4 *>(static_cast<const uint8_t *>(p.x) + tx * p.xst + 32 * kc);
             u4 x0 = xp[0], x1 = xp[1];
             const uint32_t sx = p.xs[tx * p.xsst + kc];
-            if (!ok || sx == 255u) x0 = x1 = u4{0u, 0u, 0u, 0u};
-            const float f = e8m0_to_f32(sx);
+            const uint32_t keep = keep_mask(sx, past);
+            x0 = and_u4(x0, keep), x1 = and_u4(x1, keep);
+            const float f = scale_f32(sx & keep);
             b[0] = expand8_fp8(x0.x, x0.y, f), b[1] = expand8_fp8(x0.z, x0.w, f);
             b[2] = expand8_fp8(x1.x, x1.y, f), b[3] = expand8_fp8(x1.z, x1.w, f);
         } else {
             const u4 *xp = reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(p.x) + tx * p.xst + 32 * kc);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) b[s] = as_bf8(ok ? xp[s] : u4{0u, 0u, 0u, 0u});
+            for (int s = 0; s < 4; ++s) b[s] = as_bf8(and_u4(xp[s], ~past));
         }
 #pragma unroll
         for (int m = 0; m < NM; ++m)
@@ -117,8 +132,9 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_
             for (int r = 0; r < 2; ++r) {
                 u4 a = *reinterpret_cast<const u4 *>(wr[m][r] + 16 * kc);
                 const uint32_t sw = sr[m][r][kc];
-                if (!ok || sw == 255u) a = u4{0u, 0u, 0u, 0u};
-                const float f = e8m0_to_f32(sw);
+                const uint32_t keep = keep_mask(sw, past);
+                a = and_u4(a, keep);
+                const float f = scale_f32(sw & keep);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) acc[m][r] = mfma_bf16(dequant8_bf16(a[s], f), b[s], acc[m][r]);
             }
@@ -146,16 +162,400 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_
     }
 }
 
+// ---------------------------------------------------------------------------
+// Tiles for batches. A block of 8 waves owns 256 weight rows (256 of the one
+// matrix, or 128 of each of the two) and 128 tokens; a wave 64 rows x 64
+// tokens (gate and up rows of the same columns, so the activation stays in
+// its lanes). Tokens pass through LDS, 256 bytes of every token per K step,
+// double-buffered with one barrier per step; weights go from memory straight
+// into the registers of the two waves that share them, one step ahead.
+// Rows rather than tokens are the long side because a token's bytes are
+// four times a weight row's: LDS reads take half the cycles of the MFMAs.
+//
+// LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15), so a
+// fragment read (one slot of 16 rows) touches every bank once.
+constexpr int kTlRows = 256, kTlTok = 128, kTlWaves = 8;
+// kTkBf16: bf16 tokens. kTkExp: MXFP8 tokens expanded to bf16 on their way
+// into LDS. kTkF8: MXFP8 tokens on the block-scaled MFMA
+// v_mfma_scale_f32_16x16x128_f8f6f4 as they are.
+constexpr int kTkBf16 = 0, kTkExp = 1, kTkF8 = 2;
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+#ifdef __HIP_DEVICE_COMPILE__
+// A buffer resource over the 4 GiB behind p: the direct loads take 32-bit
+// offsets from it (and, unlike those of the global form, leave the waits for
+// loads into registers exact).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_src(const uint8_t *p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, -1, 0x00020000);
+}
+#endif
+
+// Four neighbouring results (columns n .. n + 3 of token t; the 8 lanes of an
+// octet hold one group of 32 columns). nin: how many of them exist (0: none).
+__device__ __forceinline__ void dense_store4(const DenseParams &p, int64_t t, int n, int nin, float4 y)
+{
+    const float v[4] = {y.x, y.y, y.z, y.w};
+    if (p.kind == K3MOE_OUT_MXFP8) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, i < nin ? mx8_mag(v[i]) : 0.0f);
+        m = octet_max(m);
+        const int s = mx8_exp(m);
+        const float inv = mx8_inv(s);
+        uint8_t *o = static_cast<uint8_t *>(p.out) + t * p.ost + n;
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = mx8_code(v[i], inv);
+        if (nin == 4 && p.vec) {
+            *reinterpret_cast<uint32_t *>(o) = c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < nin) o[i] = (uint8_t)c[i];
+        }
+        if (nin > 0 && n % 32 == 0) p.outs[t * p.osst + n / 32] = (uint8_t)(s + 127);
+    } else if (p.kind == K3MOE_OUT_BF16) {
+        uint16_t *o = static_cast<uint16_t *>(p.out) + t * p.ost + n;
+        if (nin == 4 && p.vec) {
+            *reinterpret_cast<uint2 *>(o) = uint2{(uint32_t)dn_bf16(v[0]) | ((uint32_t)dn_bf16(v[1]) << 16),
+                                                  (uint32_t)dn_bf16(v[2]) | ((uint32_t)dn_bf16(v[3]) << 16)};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < nin) o[i] = dn_bf16(v[i]);
+        }
+    } else {
+        float *o = static_cast<float *>(p.out) + t * p.ost + n;
+        const bool add = p.kind == K3MOE_OUT_F32_ADD;
+        if (nin == 4 && p.vec) {
+            float4 z = add ? *reinterpret_cast<const float4 *>(o) : float4{0.0f, 0.0f, 0.0f, 0.0f};
+            z.x += y.x, z.y += y.y, z.z += y.z, z.w += y.w;
+            *reinterpret_cast<float4 *>(o) = z;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < nin) o[i] = add ? o[i] + v[i] : v[i];
+        }
+    }
+}
+
+// A step is 128 columns: 64 bytes of every weight row, 256 (bf16) or 128 (kTkF8)
+// of every token, one dword of every scale row. The buffers of a block:
+template <int TK> __host__ __device__ constexpr int tl_xrow() { return TK == kTkF8 ? 128 : 256; }
+template <int TK> __host__ __device__ constexpr int tl_nbuf() { return TK == kTkF8 ? 4 : 3; }
+constexpr int kTlWBuf = kTlRows * 64, kTlSRows = 64 * kTlWaves;  // one scale dword per thread
+template <int TK> __host__ __device__ constexpr int tl_buf() { return kTlTok * tl_xrow<TK>() + kTlWBuf + 4 * kTlSRows; }
+template <int TK> __host__ __device__ constexpr int tl_lds() { return tl_nbuf<TK>() * tl_buf<TK>(); }
+
+// Waits until at most N of the wave's memory loads are in flight and its LDS
+// traffic is done, then for the block.
+template <int N>
+__device__ __forceinline__ void tile_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// LDS stores of the tile pipeline. As plain stores the compiler would first
+// wait for every direct load in flight, which may write the same LDS for all
+// it knows; tile_barrier waits for them. (The LDS address is the low half of
+// a shared pointer.)
+__device__ __forceinline__ void lds_put(const uint8_t *at, uint32_t v)
+{
+    asm volatile("ds_write_b32 %0, %1" ::"v"((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)at), "v"(v)
+                 : "memory");
+}
+__device__ __forceinline__ void lds_put16(const uint8_t *at, bf8 v)
+{
+    asm volatile("ds_write_b128 %0, %1" ::"v"((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)at), "v"(v)
+                 : "memory");
+}
+
+template <int NM, int TK>
+__global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int tok_tiles)
+{
+#ifdef __HIP_DEVICE_COMPILE__   // the buffer resource type exists on the device side only
+    constexpr int NB = tl_nbuf<TK>(), BUF = tl_buf<TK>(), XR = tl_xrow<TK>();
+    constexpr int XB = kTlTok * XR;               // a buffer: tokens, weights, scales
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
+    const int wn = wave >> 1, wt = wave & 1;
+    // Neighbouring blocks run on different XCDs (block b on b mod 8): each XCD takes one run of tiles, in an
+    // order that goes through four token tiles for every row block, so that the tiles in flight in it share
+    // weights and tokens in its L2 (2048 x 7168 x 18432 bf16: 513 us, token tiles in order 523)
+    const int nt = gridDim.x, xcd = blockIdx.x & 7, per = nt >> 3, rest = nt & 7;
+    const int tile = xcd * per + min(xcd, rest) + (int)(blockIdx.x >> 3);
+    const int group = tile / (nt / tok_tiles * 4), gt0 = 4 * group, gt = min(4, tok_tiles - gt0);
+    const int in_group = tile - nt / tok_tiles * gt0, rb = in_group / gt, tb = gt0 + in_group - rb * gt;
+    const int n0 = rb * (kTlRows / NM), t0 = tb * kTlTok;
+    const int KB = p.K / 32, NS = (KB + 3) / 4;
+
+    // Weight staging: LDS row i < 256 / NM holds row n0 + i of the first matrix, the others the second's.
+    // Four threads per row, two passes; offsets from the block's first row fit 32 bits.
+    auto lrow = [&](int i) { return NM == 1 ? i : i & (kTlRows / 2 - 1); };
+    uint32_t wo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) wo[i] = (uint32_t)min(lrow((tid >> 2) + 128 * i), p.N - 1 - n0) * (uint32_t)(p.K / 2);
+    __amdgpu_buffer_rsrc_t wsrc[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) wsrc[m] = tile_src(p.w[m] + (size_t)n0 * (p.K / 2));
+    const int wj = (tid & 3) ^ ((tid >> 4) & 3);  // slot j of row r lies at j ^ (r / 4 mod 4)
+    auto wdirect = [&](int k, int buf) {
+        const uint32_t kc = 16u * (uint32_t)min(4 * k + wj, KB - 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc[NM == 1 ? 0 : i],
+                                                     (lds_void *)(lds + buf * BUF + XB + (512 * i + 64 * wave) * 16), 16,
+                                                     (int)(wo[i] + kc), 0, 0, 0);
+    };
+    // Scales: thread i < 256 holds the dword (four blocks) of LDS weight row i, thread 256 + t (kTkF8, t < 128)
+    // that of token t, in a register for a step before it goes to its buffer; blocks past the row's last read
+    // as 255. K >= 128: the last dword of a row is loaded and shifted.
+    const uint8_t *sp = p.ws[NM == 1 ? 0 : (tid & 255) >> 7] + (size_t)min(n0 + lrow(tid & 255), p.N - 1) * KB;
+    if (TK == kTkF8 && tid >= 256) sp = p.xs + (int64_t)min(t0 + (tid & 127), p.T - 1) * p.xsst;
+    uint32_t sreg = 0;
+    auto sload = [&](int k) { __builtin_memcpy(&sreg, sp + min(4 * k, KB - 4), 4); };
+    auto sstore = [&](int k, int buf) {
+        const int sh = 8 * max(0, 4 * k + 4 - KB);   // blocks past the last: 0, or 8 to 24 bits
+        lds_put(lds + buf * BUF + XB + kTlWBuf + 4 * tid, (sreg >> sh) | ~(~0u >> sh));
+    };
+
+    // Token staging. Direct (kTkBf16, kTkF8): slots of 16 bytes, XP per thread. kTkExp: two slots of 16 values
+    // per thread, held in registers for a step and expanded on their way into LDS.
+    constexpr int ES = TK == kTkBf16 ? 2 : 1;     // bytes per token element in memory
+    constexpr int SL = XR / 16, XP = XB / 8192;   // slots per row, passes
+    constexpr int EP = 2;
+    const uint8_t *xb = static_cast<const uint8_t *>(p.x);
+    const uint8_t *xr[EP], *xsr[EP];
+    uint32_t xo[XP];
+    const __amdgpu_buffer_rsrc_t xsrc = tile_src(xb + (int64_t)t0 * p.xst * ES);
+    if constexpr (TK == kTkExp) {
+#pragma unroll
+        for (int i = 0; i < EP; ++i) {
+            const int64_t t = min(t0 + (tid >> 3) + 64 * i, p.T - 1);
+            xr[i] = xb + t * p.xst;
+            xsr[i] = p.xs + t * p.xsst;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < XP; ++i)
+            xo[i] = (uint32_t)min((tid + 512 * i) / SL, p.T - 1 - t0) * (uint32_t)(p.xst * ES);
+    }
+    const int last = p.K * ES / 16 - 1;           // last slot of a token row
+    // slot j of token r lies at j ^ (r mod 16) of 16, or j ^ (r / 2 mod 8) of 8 (the passes keep r mod 16)
+    const int xsw = SL == 16 ? (tid >> 4) & 15 : (tid >> 4) & 7;
+    auto xdirect = [&](int k, int buf) {
+        const uint32_t o = 16u * (uint32_t)min(SL * k + ((tid & (SL - 1)) ^ xsw), last);
+#pragma unroll
+        for (int i = 0; i < XP; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xsrc, (lds_void *)(lds + buf * BUF + (512 * i + 64 * wave) * 16), 16,
+                                                     (int)(xo[i] + o), 0, 0, 0);
+    };
+    u4 xe[EP];
+    uint32_t xes[EP];
+    auto eload = [&](int k) {
+        const int slot = min(8 * k + (tid & 7), last);
+#pragma unroll
+        for (int i = 0; i < EP; ++i) {
+            xe[i] = *reinterpret_cast<const u4 *>(xr[i] + 16 * (int64_t)slot);
+            xes[i] = xsr[i][slot >> 1];
+        }
+    };
+    auto estore = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < EP; ++i) {
+            const int row = (tid >> 3) + 64 * i, j = 2 * (tid & 7);
+            const uint32_t keep = keep_mask(xes[i], 0u);
+            const float f = scale_f32(xes[i] & keep);
+            const u4 v = and_u4(xe[i], keep);
+            uint8_t *d = lds + buf * BUF + row * 256;
+            lds_put16(d + 16 * (j ^ (row & 15)), expand8_fp8(v.x, v.y, f));
+            lds_put16(d + 16 * ((j + 1) ^ (row & 15)), expand8_fp8(v.z, v.w, f));
+        }
+    };
+
+    v4f acc[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // this wave's four row tiles: LDS rows 64 wn + 16 r, or 32 wn + 16 (r mod 2) of either matrix's half
+    int arow[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        arow[r] = (NM == 1 ? 64 * wn + 16 * r : 128 * (r >> 1) + 32 * wn + 16 * (r & 1)) + l16;
+    const int asl = 16 * (g ^ (l16 >> 2));        // this lane's slot of them
+
+    auto compute = [&](int buf) {
+        const uint8_t *B = lds + buf * BUF + (64 * wt + l16) * XR;
+        const uint8_t *A = lds + buf * BUF + XB, *S = A + kTlWBuf;
+        u4 a[4];
+        uint32_t s4[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            a[r] = *reinterpret_cast<const u4 *>(A + arow[r] * 64 + asl);
+            s4[r] = *reinterpret_cast<const uint32_t *>(S + 4 * arow[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t sv = (s4[r] >> (8 * g)) & 0xffu, keep = keep_mask(sv, 0u);
+            a[r] = and_u4(a[r], keep);
+            s4[r] = sv & keep;
+        }
+        if constexpr (TK == kTkF8) {
+            // the fp8 operand of lane group g: columns [16g, 16g + 16) and [64 + 16g, 80 + 16g) of
+            // the step; its scale: block g
+            u4 lo[4], hi[4];
+            int sx[4];
+            bool any = false;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                lo[t] = *reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * (g ^ (l16 >> 1)));
+                hi[t] = *reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * ((4 + g) ^ (l16 >> 1)));
+                sx[t] = (int)((*reinterpret_cast<const uint32_t *>(S + 4 * (kTlRows + 64 * wt + 16 * t + l16)) >> (8 * g)) & 0xffu);
+                any |= sx[t] == 255;
+            }
+            if (__any(any)) {  // dropped groups: the values of blocks g / 2 and 2 + g / 2 are held here
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if (__shfl(sx[t], 16 * (g >> 1) + l16) == 255) lo[t] = u4{0u, 0u, 0u, 0u};
+                    if (__shfl(sx[t], 32 + 16 * (g >> 1) + l16) == 255) hi[t] = u4{0u, 0u, 0u, 0u};
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (sx[t] == 255) sx[t] = 127;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const v8i b = b_operand(lo[t], hi[t]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[r][t] = mfma_fp4_fp8(a_operand(a[r]), b, acc[r][t], (int)s4[r], sx[t]);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                bf8 b[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    b[t] = as_bf8(*reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * ((4 * g + s) ^ l16)));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bf8 av = dequant8_bf16(a[r][s], scale_f32(s4[r]));
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) acc[r][t] = mfma_bf16(av, b[t], acc[r][t]);
+                }
+            }
+        }
+    };
+
+    // Pipeline. The loads of step k are issued in step k - NB + 1: first those
+    // through registers (stored to their buffer one step later), then the
+    // direct ones. Step k waits until only the loads of the NB - 2 steps
+    // behind it are in flight, and for the block; its buffer is then whole,
+    // and the buffer of step k - 1 is read and free for step k + NB - 1. Steps
+    // past the last load the last one's operands again, so that every step
+    // issues LPS loads.
+    constexpr int LPS = 1 + (TK == kTkExp ? 2 * EP : XP) + 2;
+    constexpr int D = NB - 1;
+    auto issue = [&](int k, int buf) {
+        const int kc = min(k, NS - 1);
+        sload(kc);
+        if constexpr (TK == kTkExp) eload(kc);
+        wdirect(kc, buf);
+        if constexpr (TK != kTkExp) xdirect(kc, buf);
+        asm volatile("" ::: "memory");            // no load moves behind the products
+    };
+    auto settle = [&](int k, int buf) {
+        sstore(min(k, NS - 1), buf);
+        if constexpr (TK == kTkExp) estore(buf);
+    };
+#pragma unroll
+    for (int k = 0; k < D; ++k) {
+        issue(k, k);
+        if (k < D - 1) settle(k, k);
+    }
+    int cur = 0, in = D;                          // buffers of step k and of step k + D
+    for (int k = 0; k < NS; ++k) {
+        // the newest loads in registers (step k + D - 1) go to their buffer, then step k's operands are awaited
+        const int prev = in == 0 ? NB - 1 : in - 1;
+        settle(k + D - 1, prev);
+        tile_barrier<LPS *(D - 1)>();
+        issue(k + D, in);
+        compute(cur);
+        cur = cur == NB - 1 ? 0 : cur + 1;
+        in = in == NB - 1 ? 0 : in + 1;
+    }
+    tile_barrier<0>();  // the buffers become the waves' transpose areas
+
+    // Epilogue, 16 tokens at a time: [token][row] through the wave's own LDS, then four
+    // neighbouring columns per lane (16 lanes: 64 rows of one matrix, or the first 8 of them
+    // 32 activations).
+    float *tr = reinterpret_cast<float *>(lds) + wave * (16 * 68);
+    constexpr int CT = 64 / NM;                    // columns per wave
+    constexpr int LPT = CT / 4, TPP = 64 / LPT;    // lanes per token, tokens per pass
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4 / NM; ++r) {
+            float4 v;
+            if constexpr (NM == 1) {
+                v = float4{acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]};
+            } else {
+                v = float4{act_fn(acc[r][t][0], acc[r + 2][t][0], p.act, p.b1, p.b2),
+                           act_fn(acc[r][t][1], acc[r + 2][t][1], p.act, p.b1, p.b2),
+                           act_fn(acc[r][t][2], acc[r + 2][t][2], p.act, p.b1, p.b2),
+                           act_fn(acc[r][t][3], acc[r + 2][t][3], p.act, p.b1, p.b2)};
+            }
+            *reinterpret_cast<float4 *>(tr + 68 * l16 + 16 * r + 4 * g) = v;
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int q = 0; q < 16 / TPP; ++q) {
+            const int tok = q * TPP + lane / LPT, col = 4 * (lane % LPT);
+            const float4 v = *reinterpret_cast<const float4 *>(tr + 68 * tok + col);
+            const int tt = t0 + 64 * wt + 16 * t + tok, n = n0 + CT * wn + col;
+            dense_store4(p, tt, n, tt < p.T ? max(0, min(4, p.N - n)) : 0, v);
+        }
+        wave_lds_sync();
+    }
+#endif
+}
+
 // work-items of a launch are counted in 32 bits
 constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;
+
+template <int NM, int TK>
+void launch_tile(const DenseParams &p, int64_t blocks, int tok_tiles, hipStream_t s)
+{
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_tile<NM, TK>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, tl_lds<TK>());
+    k_mx_tile<NM, TK><<<(unsigned)blocks, 64 * kTlWaves, tl_lds<TK>(), s>>>(p, tok_tiles);
+}
+
+// Batches of more tokens than this run on tiles.
+constexpr int kStreamMaxT = 64;
 
 template <int NM>
 k3moe_status launch_dense(const DenseParams &p, hipStream_t s)
 {
-    const int64_t rb = ((int64_t)p.N + 31) / 32, tb = ((int64_t)p.T + 15) / 16;
-    if (rb * tb > kMaxItems / (64 * kStW)) return K3MOE_E_UNSUPPORTED_SHAPE;
-    if (p.xs) k_mx_stream<NM, true><<<(unsigned)(rb * tb), 64 * kStW, 0, s>>>(p, (int)rb);
-    else k_mx_stream<NM, false><<<(unsigned)(rb * tb), 64 * kStW, 0, s>>>(p, (int)rb);
+    const int64_t xes = p.xs ? 1 : 2;
+    const bool tile_ok = p.K >= 128 && (kTlTok - 1) * p.xst * xes + p.K * xes < ((int64_t)1 << 32);
+    if (p.T > kStreamMaxT && tile_ok) {
+        const int64_t rb = ((int64_t)p.N * NM + kTlRows - 1) / kTlRows, tb = ((int64_t)p.T + kTlTok - 1) / kTlTok;
+        if (rb * tb > kMaxItems / (64 * kTlWaves)) return K3MOE_E_UNSUPPORTED_SHAPE;
+        if (!p.xs) launch_tile<NM, kTkBf16>(p, rb * tb, (int)tb, s);
+        else if (p.kind == K3MOE_OUT_BF16) launch_tile<NM, kTkF8>(p, rb * tb, (int)tb, s);
+        else launch_tile<NM, kTkExp>(p, rb * tb, (int)tb, s);
+    } else {
+        const int64_t rb = ((int64_t)p.N + 31) / 32, tb = ((int64_t)p.T + 15) / 16;
+        if (rb * tb > kMaxItems / (64 * kStW)) return K3MOE_E_UNSUPPORTED_SHAPE;
+        if (p.xs) k_mx_stream<NM, true><<<(unsigned)(rb * tb), 64 * kStW, 0, s>>>(p, (int)rb);
+        else k_mx_stream<NM, false><<<(unsigned)(rb * tb), 64 * kStW, 0, s>>>(p, (int)rb);
+    }
     return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
 }
 
@@ -170,7 +570,7 @@ k3moe_status check_dense(DenseParams &p, const uint8_t *const *w, const uint8_t 
     *nothing = false;
     if (T < 0 || rows <= 0 || cols <= 0) return K3MOE_E_INVALID_ARG;
     if (kind < K3MOE_OUT_BF16 || kind > K3MOE_OUT_MXFP8) return K3MOE_E_INVALID_ARG;
-    if (cols % 32) return K3MOE_E_UNSUPPORTED_SHAPE;
+    if (cols % 32 || cols > kMaxCols) return K3MOE_E_UNSUPPORTED_SHAPE;
     if (T == 0) {
         *nothing = true;
         return K3MOE_OK;
@@ -185,7 +585,9 @@ k3moe_status check_dense(DenseParams &p, const uint8_t *const *w, const uint8_t 
     for (int m = 0; m < nm; ++m)
         if (!at(w[m], 16) || !at(ws[m], 16)) return K3MOE_E_ALIGNMENT;
     if (!at(x, 16) || x_stride % (xs ? 16 : 8)) return K3MOE_E_ALIGNMENT;
-    if (!at(out, kind == K3MOE_OUT_MXFP8 ? 1 : kind == K3MOE_OUT_BF16 ? 2 : 4)) return K3MOE_E_ALIGNMENT;
+    const size_t oe = kind == K3MOE_OUT_MXFP8 ? 1 : kind == K3MOE_OUT_BF16 ? 2 : 4;
+    if (!at(out, oe)) return K3MOE_E_ALIGNMENT;
+    p.vec = at(out, 4 * oe) && out_stride % 4 == 0;
     for (int m = 0; m < nm; ++m) p.w[m] = w[m], p.ws[m] = ws[m];
     p.x = x, p.xs = xs, p.out = out, p.outs = outs;
     p.xst = x_stride, p.xsst = xs_stride, p.ost = out_stride, p.osst = outs_stride;
