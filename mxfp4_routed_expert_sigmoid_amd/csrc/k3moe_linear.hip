@@ -79,19 +79,210 @@ __device__ __forceinline__ void dense_store(const DenseParams &p, int64_t t, int
     }
 }
 
-// A block owns 32 rows of each matrix and 16 tokens; its waves take the chunks
-// of 128 columns in turn, and their fp32 sums are added in wave order.
-constexpr int kStW = 4;
+// ---------------------------------------------------------------------------
+// A few tokens: the product is a stream of weights. A block owns 16 RT rows
+// of each matrix; its waves split the columns, so that a narrow matrix still
+// fills the card, and their fp32 sums are added in wave order. A wave reads
+// 16 rows x 256 bytes per unit (512 columns) and matrix tile, the next unit in
+// flight while one is multiplied; its share of the tokens goes into LDS first
+// (behind the first weight loads), so that the loads in flight are all weights.
+constexpr int kGvTok = 4, kGvMaxWaves = 8;
+constexpr int kGvMaxLds = 65536;   // token bytes of a block
+// A matrix of fewer tiles has a block for each, which the card schedules as
+// they end (18432 rows x 2 matrices x 7168: 33 us, 39 us with two or three
+// tiles per block); a longer one two blocks per CU, each with many tiles,
+// which keeps the tokens in LDS and the loads in flight between them
+// (4 tokens x 163840 rows x 7168: 124 us, a block per tile 161 us).
+constexpr int kGvLong = 4096, kGvBlocks = 512;
 
-template <int NM, bool X8>
+// Weights of one unit (U chunks of 128 columns) of a 16-row tile: its chunks of
+// this lane's row, and the row's scale bytes of them (chunk j in dword j).
+template <int U>
+struct GvUnit {
+    u4 a[U];
+    uint32_t s[U];
+};
+
+template <int U>
+__device__ __forceinline__ void gv_load(GvUnit<U> &u, const uint8_t *w, const uint8_t *s, int unit, int KB, int g)
+{
+    const int b0 = 4 * U * unit;
+    if (b0 + 4 * U <= KB) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) u.a[j] = *reinterpret_cast<const u4 *>(w + 16 * (b0 + 4 * j + g));
+        __builtin_memcpy(u.s, s + b0, 4 * U);
+    } else {  // the row's last, partial unit
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int b = b0 + 4 * j + g, bc = min(b, KB - 1);
+            u.a[j] = *reinterpret_cast<const u4 *>(w + 16 * bc);
+            u.s[j] = (b < KB ? (uint32_t)s[bc] : 255u) << (8 * g);
+        }
+    }
+}
+
+// Waits for the wave's LDS traffic, then for the block; loads into registers
+// stay in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int NM, bool X8, int RT, int U>
+__global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int tiles)
+{
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
+    const int g = lane >> 4, l16 = lane & 15;
+    const int KB = p.K / 32, NU = (KB + 4 * U - 1) / (4 * U);
+    const int u0 = NU * wave / nw, u1 = NU * (wave + 1) / nw;  // at least one unit each
+    // this block's row tiles (16 RT rows)
+    const int tile0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), tile1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+    const int xrow = 2 * p.K;                                  // LDS bytes of a token: bf16
+    uint8_t *xl = lds;
+    float *red0 = reinterpret_cast<float *>(lds + p.T * xrow); // two of [wave][NM][RT][token][16]
+    const int rsize = nw * NM * RT * kGvTok * 16;
+
+    const uint8_t *wr[NM][RT], *sr[NM][RT];
+    auto rows = [&](int tile) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int64_t n = min(16 * (RT * tile + r) + l16, p.N - 1);
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                wr[m][r] = p.w[m] + n * (p.K / 2);
+                sr[m][r] = p.ws[m] + n * KB;
+            }
+        }
+    };
+    GvUnit<U> ua[NM][RT], ub[NM][RT];
+    int lt = tile0, lu = u0;                                   // the next unit to load
+    auto load = [&](GvUnit<U> (&q)[NM][RT]) {
+        if (lt >= tile1) return;
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) gv_load(q[m][r], wr[m][r], sr[m][r], lu, KB, g);
+        if (++lu == u1) {
+            lu = u0;
+            rows(++lt);
+        }
+    };
+    v4f acc[NM][RT];
+    auto clear = [&]() {
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[m][r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    const uint8_t *bx = xl + min(l16, p.T - 1) * xrow;
+    auto mul = [&](int u, const GvUnit<U> (&q)[NM][RT]) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int kc = min(4 * (U * u + j) + g, KB - 1);    // past the row's last block the weights are zeros
+            bf8 b[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) b[s] = as_bf8(*reinterpret_cast<const u4 *>(bx + 64 * kc + 16 * s));
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const uint32_t sw = (q[m][r].s[j] >> (8 * g)) & 0xffu, keep = keep_mask(sw, 0u);
+                    const u4 a = and_u4(q[m][r].a[j], keep);
+                    const float f = scale_f32(sw & keep);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) acc[m][r] = mfma_bf16(dequant8_bf16(a[s], f), b[s], acc[m][r]);
+                }
+        }
+    };
+    // a tile's sums: added in wave order, one value per thread of the first waves (32 rows, or 16, of a token)
+    auto finish = [&](int tile) {
+        float *red = red0 + ((tile - tile0) & 1 ? rsize : 0);
+        if (l16 < p.T) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    *reinterpret_cast<float4 *>(red + (((wave * NM + m) * RT + r) * kGvTok + l16) * 16 + 4 * g) =
+                        float4{acc[m][r][0], acc[m][r][1], acc[m][r][2], acc[m][r][3]};
+        }
+        lds_barrier();
+        for (int i = tid; i < 16 * RT * ((p.T + 1) & ~1); i += 64 * nw) {
+            const int row = i % (16 * RT), tok = i / (16 * RT), tc = min(tok, p.T - 1), n = 16 * RT * tile + row;
+            float v[NM];
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                v[m] = 0.0f;
+                for (int w = 0; w < nw; ++w) v[m] += red[(((w * NM + m) * RT + (row >> 4)) * kGvTok + tc) * 16 + (row & 15)];
+            }
+            float y = v[0];
+            if constexpr (NM == 2) y = act_fn(v[0], v[1], p.act, p.b1, p.b2);
+            dense_store(p, tok, n, tok < p.T && n < p.N, y);
+        }
+        clear();
+    };
+
+    rows(tile0);
+    load(ua);
+    clear();
+    {
+        // the wave's columns of every token, as bf16
+        const int c0 = 128 * U * u0, per = (min(128 * U * u1, p.K) - c0) / (X8 ? 16 : 8);   // 16-byte pieces of a token
+        for (int i = lane; i < p.T * per; i += 64) {
+            const int t = i / per, q = i - t * per;
+            if constexpr (X8) {
+                const int c = c0 + 16 * q;
+                const u4 x = *reinterpret_cast<const u4 *>(static_cast<const uint8_t *>(p.x) + t * p.xst + c);
+                const uint32_t sx = p.xs[t * p.xsst + c / 32], keep = keep_mask(sx, 0u);
+                const u4 v = and_u4(x, keep);
+                const float f = scale_f32(sx & keep);
+                bf8 *d = reinterpret_cast<bf8 *>(xl + t * xrow + 2 * c);
+                d[0] = expand8_fp8(v.x, v.y, f), d[1] = expand8_fp8(v.z, v.w, f);
+            } else {
+                const int c = c0 + 8 * q;
+                *reinterpret_cast<u4 *>(xl + t * xrow + 2 * c) =
+                    *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(p.x) + t * p.xst + c);
+            }
+        }
+        wave_lds_sync();
+    }
+    // two units at a time: while one is multiplied the other is in flight, across the tiles' borders
+    int t = tile0, u = u0;
+    auto next = [&]() {
+        if (++u == u1) {
+            finish(t);
+            u = u0;
+            ++t;
+        }
+    };
+    while (t < tile1) {
+        load(ub);
+        mul(u, ua);
+        next();
+        if (t < tile1) {
+            load(ua);
+            mul(u, ub);
+            next();
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 64 tokens. As above with NT tiles of 16 tokens and 32 rows of each
+// matrix per block; tokens come from memory (the L2) with the weights, a chunk
+// ahead.
+constexpr int kStW = 8;
+
+template <int NM, bool X8, int NT>
 __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_blocks)
 {
-    __shared__ float4 red[kStW][NM][2][64];
+    __shared__ float4 red[kStW / 2][NM][2][NT][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
     const int rb = blockIdx.x % row_blocks, tb = blockIdx.x / row_blocks;
-    const int n0 = 32 * rb, t0 = 16 * tb;
+    const int n0 = 32 * rb, t0 = 16 * NT * tb;
     const int KB = p.K / 32, NC = (KB + 3) / 4;
-    const int64_t tx = min(t0 + l16, p.T - 1);
     const uint8_t *wr[NM][2], *sr[NM][2];
 #pragma unroll
     for (int m = 0; m < NM; ++m)
@@ -101,64 +292,133 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_
             wr[m][r] = p.w[m] + n * (p.K / 2);
             sr[m][r] = p.ws[m] + n * KB;
         }
-    v4f acc[NM][2];
+    constexpr int ES = X8 ? 1 : 2;
+    const uint8_t *xr[NT], *xsr[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int64_t tx = min(t0 + 16 * t + l16, p.T - 1);
+        xr[t] = static_cast<const uint8_t *>(p.x) + tx * p.xst * ES;
+        xsr[t] = p.xs + tx * p.xsst;
+    }
+    v4f acc[NM][2][NT];
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) acc[m][r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-    for (int c = wave; c < NC; c += kStW) {
-        const int kb = 4 * c + g;
-        const uint32_t past = kb < KB ? 0u : ~0u;   // past the last block: zeros on both sides
-        const int kc = min(kb, KB - 1);
-        bf8 b[4];
-        if constexpr (X8) {
-            const u4 *xp = reinterpret_cast<const u4 *>(static_cast<const uint8_t *>(p.x) + tx * p.xst + 32 * kc);
-            u4 x0 = xp[0], x1 = xp[1];
-            const uint32_t sx = p.xs[tx * p.xsst + kc];
-            const uint32_t keep = keep_mask(sx, past);
-            x0 = and_u4(x0, keep), x1 = and_u4(x1, keep);
-            const float f = scale_f32(sx & keep);
-            b[0] = expand8_fp8(x0.x, x0.y, f), b[1] = expand8_fp8(x0.z, x0.w, f);
-            b[2] = expand8_fp8(x1.x, x1.y, f), b[3] = expand8_fp8(x1.z, x1.w, f);
-        } else {
-            const u4 *xp = reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(p.x) + tx * p.xst + 32 * kc);
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) b[s] = as_bf8(and_u4(xp[s], ~past));
+            for (int t = 0; t < NT; ++t) acc[m][r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+    struct Chunk {
+        u4 a[NM][2], x[NT][X8 ? 2 : 4];
+        uint32_t s[NM][2], xs[NT];
+    };
+    auto load = [&](int c, Chunk &q) {
+        const int kc = min(4 * c + g, KB - 1);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int i = 0; i < 2 * ES; ++i) q.x[t][i] = *reinterpret_cast<const u4 *>(xr[t] + (32 * ES) * (int64_t)kc + 16 * i);
+            if constexpr (X8) q.xs[t] = xsr[t][kc];
         }
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                u4 a = *reinterpret_cast<const u4 *>(wr[m][r] + 16 * kc);
-                const uint32_t sw = sr[m][r][kc];
-                const uint32_t keep = keep_mask(sw, past);
-                a = and_u4(a, keep);
-                const float f = scale_f32(sw & keep);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) acc[m][r] = mfma_bf16(dequant8_bf16(a[s], f), b[s], acc[m][r]);
+                q.a[m][r] = *reinterpret_cast<const u4 *>(wr[m][r] + 16 * (int64_t)kc);
+                q.s[m][r] = sr[m][r][kc];
             }
+    };
+    auto mul = [&](int c, const Chunk &q) {
+        const uint32_t past = 4 * c + g < KB ? 0u : ~0u;   // past the last block: zero weights
+        u4 a[NM][2];
+        float f[NM][2];
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t keep = keep_mask(q.s[m][r], past);
+                a[m][r] = and_u4(q.a[m][r], keep);
+                f[m][r] = scale_f32(q.s[m][r] & keep);
+            }
+        uint32_t xk[NT];
+        float xf[NT];
+        if constexpr (X8) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                xk[t] = keep_mask(q.xs[t], 0u);
+                xf[t] = scale_f32(q.xs[t] & xk[t]);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            bf8 w[NM][2];
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) w[m][r] = dequant8_bf16(a[m][r][s], f[m][r]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                bf8 b;
+                if constexpr (X8) b = expand8_fp8(q.x[t][s >> 1][2 * (s & 1)] & xk[t], q.x[t][s >> 1][2 * (s & 1) + 1] & xk[t], xf[t]);
+                else b = as_bf8(q.x[t][s]);
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) acc[m][r][t] = mfma_bf16(w[m][r], b, acc[m][r][t]);
+            }
+        }
+    };
+    const int c0 = NC * wave / kStW, c1 = NC * (wave + 1) / kStW;
+    Chunk qa, qb;
+    if (c0 < c1) load(c0, qa);
+    for (int c = c0; c < c1; c += 2) {
+        if (c + 1 < c1) load(c + 1, qb);
+        mul(c, qa);
+        if (c + 1 < c1) {
+            if (c + 2 < c1) load(c + 2, qa);
+            mul(c + 1, qb);
+        }
     }
+    // the upper half of the waves hands its sums to the lower half, which keeps wave order: (w) + (w + 4)
+    auto put = [&](int w) {
 #pragma unroll
-    for (int m = 0; m < NM; ++m)
+        for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)  // [token][row]: lane l16 holds rows 4g + i of token l16
-            red[wave][m][r][4 * l16 + g] = float4{acc[m][r][0], acc[m][r][1], acc[m][r][2], acc[m][r][3]};
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)   // [token][row]: lane l16 holds rows 4g + i of token l16
+                    red[w][m][r][t][4 * l16 + g] = float4{acc[m][r][t][0], acc[m][r][t][1], acc[m][r][t][2], acc[m][r][t][3]};
+    };
+    if (wave >= kStW / 2) put(wave - kStW / 2);
+    __syncthreads();
+    if (wave < kStW / 2) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float4 z = red[wave][m][r][t][4 * l16 + g];
+                    acc[m][r][t] += v4f{z.x, z.y, z.z, z.w};
+                }
+        put(wave);
+    }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int tok = (tid >> 5) + 8 * q, row = tid & 31;
+    for (int q = 0; q < NT; ++q) {
+        const int tok = (tid >> 5), row = tid & 31;
         float v[NM];
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             v[m] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kStW; ++w)
-                v[m] += reinterpret_cast<const float *>(&red[w][m][row >> 4][0])[16 * tok + (row & 15)];
+            for (int w = 0; w < kStW / 2; ++w)
+                v[m] += reinterpret_cast<const float *>(&red[w][m][row >> 4][q][0])[16 * tok + (row & 15)];
         }
         float y = v[0];
         if constexpr (NM == 2) y = act_fn(v[0], v[1], p.act, p.b1, p.b2);
-        dense_store(p, t0 + tok, n0 + row, t0 + tok < p.T && n0 + row < p.N, y);
+        const int t = t0 + 16 * q + tok;
+        dense_store(p, t, n0 + row, t < p.T && n0 + row < p.N, y);
     }
 }
 
@@ -536,6 +796,44 @@ void launch_tile(const DenseParams &p, int64_t blocks, int tok_tiles, hipStream_
     k_mx_tile<NM, TK><<<(unsigned)blocks, 64 * kTlWaves, tl_lds<TK>(), s>>>(p, tok_tiles);
 }
 
+template <int NM, bool X8, int RT, int U>
+void launch_gemv(const DenseParams &p, int tiles, int blocks, hipStream_t s)
+{
+    const int NU = (p.K / 32 + 4 * U - 1) / (4 * U);
+    // waves per block: the fewest that give the same longest share as the most
+    const int share = (NU + kGvMaxWaves - 1) / kGvMaxWaves, nw = (NU + share - 1) / share;
+    const int lds = p.T * 2 * p.K + 2 * nw * NM * RT * kGvTok * 64;
+    if (lds > 65536)
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_gemv<NM, X8, RT, U>),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, kGvMaxLds + 65536);
+    k_mx_gemv<NM, X8, RT, U><<<(unsigned)blocks, 64 * nw, lds, s>>>(p, tiles);
+}
+
+template <int NM, bool X8, int NT>
+void launch_stream(const DenseParams &p, int64_t rb, int64_t tb, hipStream_t s)
+{
+    k_mx_stream<NM, X8, NT><<<(unsigned)(rb * tb), 64 * kStW, 0, s>>>(p, (int)rb);
+}
+
+template <int NM, bool X8>
+k3moe_status launch_few(const DenseParams &p, hipStream_t s)
+{
+    if (p.T <= kGvTok && (int64_t)p.T * 2 * p.K <= kGvMaxLds) {
+        const int t1 = (int)(((int64_t)p.N + 15) / 16), t2 = (t1 + 1) / 2;
+        if (p.kind == K3MOE_OUT_MXFP8) launch_gemv<NM, X8, 2, 2>(p, t2, t2 < kGvBlocks ? t2 : kGvBlocks, s);  // 32 rows share a scale
+        else if (t1 < kGvLong) launch_gemv<NM, X8, 1, 2>(p, t1, t1, s);
+        else launch_gemv<NM, X8, 1, 4>(p, t1, kGvBlocks, s);
+        return K3MOE_OK;
+    }
+    const int nt = p.T > 32 ? 4 : p.T > 16 ? 2 : 1;
+    const int64_t rb = ((int64_t)p.N + 31) / 32, tb = ((int64_t)p.T + 16 * nt - 1) / (16 * nt);
+    if (rb * tb > kMaxItems / (64 * kStW)) return K3MOE_E_UNSUPPORTED_SHAPE;
+    if (nt == 4) launch_stream<NM, X8, NM == 2 ? 2 : 4>(p, rb, NM == 2 ? ((int64_t)p.T + 31) / 32 : tb, s);
+    else if (nt == 2) launch_stream<NM, X8, 2>(p, rb, tb, s);
+    else launch_stream<NM, X8, 1>(p, rb, tb, s);
+    return K3MOE_OK;
+}
+
 // Batches of more tokens than this run on tiles.
 constexpr int kStreamMaxT = 64;
 
@@ -544,6 +842,7 @@ k3moe_status launch_dense(const DenseParams &p, hipStream_t s)
 {
     const int64_t xes = p.xs ? 1 : 2;
     const bool tile_ok = p.K >= 128 && (kTlTok - 1) * p.xst * xes + p.K * xes < ((int64_t)1 << 32);
+    k3moe_status st = K3MOE_OK;
     if (p.T > kStreamMaxT && tile_ok) {
         const int64_t rb = ((int64_t)p.N * NM + kTlRows - 1) / kTlRows, tb = ((int64_t)p.T + kTlTok - 1) / kTlTok;
         if (rb * tb > kMaxItems / (64 * kTlWaves)) return K3MOE_E_UNSUPPORTED_SHAPE;
@@ -551,11 +850,9 @@ k3moe_status launch_dense(const DenseParams &p, hipStream_t s)
         else if (p.kind == K3MOE_OUT_BF16) launch_tile<NM, kTkF8>(p, rb * tb, (int)tb, s);
         else launch_tile<NM, kTkExp>(p, rb * tb, (int)tb, s);
     } else {
-        const int64_t rb = ((int64_t)p.N + 31) / 32, tb = ((int64_t)p.T + 15) / 16;
-        if (rb * tb > kMaxItems / (64 * kStW)) return K3MOE_E_UNSUPPORTED_SHAPE;
-        if (p.xs) k_mx_stream<NM, true><<<(unsigned)(rb * tb), 64 * kStW, 0, s>>>(p, (int)rb);
-        else k_mx_stream<NM, false><<<(unsigned)(rb * tb), 64 * kStW, 0, s>>>(p, (int)rb);
+        st = p.xs ? launch_few<NM, true>(p, s) : launch_few<NM, false>(p, s);
     }
+    if (st != K3MOE_OK) return st;
     return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
 }
 
