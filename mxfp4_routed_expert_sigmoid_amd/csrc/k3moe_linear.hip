@@ -46,6 +46,32 @@ __device__ __forceinline__ u4 and_u4(u4 v, uint32_t m) { return u4{v.x & m, v.y 
 // field, and a field of 0 as 2^-127.
 __device__ __forceinline__ float scale_f32(uint32_t s) { return __uint_as_float(s << 23); }
 
+// Scale bytes of a run of chunks. A load that touches 16 rows costs the address
+// unit as much for four bytes of each as for 64, so the bytes of 16 chunks
+// (64 of every row) are loaded at once: lane 16g + r takes bytes [16g, 16g + 16)
+// of row r's run, and chunk j's dword is fetched from lane 16 (j / 4) + r when it
+// is used. A run may pass the row's end (those chunks' weights are dropped),
+// but not the tensor's: there the load is moved back and its bytes shifted.
+// left: bytes from the run's start to the tensor's end (>= 1); total: the
+// tensor's bytes.
+__device__ __forceinline__ u4 run_load(const uint8_t *s, int64_t left, int64_t total, int g)
+{
+    u4 v = u4{0u, 0u, 0u, 0u};
+    if (total < 16) {   // (a matrix or batch of fewer than 16 blocks)
+        for (int i = 0; i < 16; ++i)
+            if (16 * g + i < left) v[i >> 2] |= (uint32_t)s[16 * g + i] << (8 * (i & 3));
+        return v;
+    }
+    const int64_t at = min((int64_t)(16 * g), left - 16);
+    __builtin_memcpy(&v, s + at, 16);
+    const int back = (int)(16 * g - at);          // bytes in front of the wanted ones; past 15: none is wanted
+    if (back & 8) v = u4{v.z, v.w, 0u, 0u};
+    if (back & 4) v = u4{v.y, v.z, v.w, 0u};
+    const uint32_t b = 8 * (back & 3);
+    return u4{__builtin_amdgcn_alignbit(v.y, v.x, b), __builtin_amdgcn_alignbit(v.z, v.y, b),
+              __builtin_amdgcn_alignbit(v.w, v.z, b), v.w >> b};
+}
+
 __device__ __forceinline__ bf8 expand8_fp8(uint32_t lo, uint32_t hi, float scale)
 {
     const bf2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
@@ -179,12 +205,16 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
     };
     const uint8_t *bx = xl + min(l16, p.T - 1) * xrow;
     auto mul = [&](int u, const GvUnit<U> (&q)[NM][RT]) {
+        bf8 b[U][4];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int kc = min(4 * (U * u + j) + g, KB - 1);    // past the row's last block the weights are zeros
-            bf8 b[4];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) b[s] = as_bf8(*reinterpret_cast<const u4 *>(bx + 64 * kc + 16 * s));
+            for (int s = 0; s < 4; ++s) b[j][s] = as_bf8(*reinterpret_cast<const u4 *>(bx + 64 * kc + 16 * s));
+        }
+        if constexpr (U == 2) __builtin_amdgcn_sched_barrier(0);   // every fragment is read before the first product
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
 #pragma unroll
             for (int m = 0; m < NM; ++m)
 #pragma unroll
@@ -193,7 +223,7 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
                     const u4 a = and_u4(q[m][r].a[j], keep);
                     const float f = scale_f32(sw & keep);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) acc[m][r] = mfma_bf16(dequant8_bf16(a[s], f), b[s], acc[m][r]);
+                    for (int s = 0; s < 4; ++s) acc[m][r] = mfma_bf16(dequant8_bf16(a[s], f), b[j][s], acc[m][r]);
                 }
         }
     };
@@ -257,49 +287,168 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
             ++t;
         }
     };
-    while (t < tile1) {
+    for (;;) {
         load(ub);
         mul(u, ua);
         next();
-        if (t < tile1) {
-            load(ua);
-            mul(u, ub);
-            next();
-        }
+        if (t == tile1) break;
+        load(ua);
+        mul(u, ub);
+        next();
+        if (t == tile1) break;
     }
 }
 
 // ---------------------------------------------------------------------------
-// Up to 64 tokens. As above with NT tiles of 16 tokens and 32 rows of each
-// matrix per block; tokens come from memory (the L2) with the weights, a chunk
-// ahead.
-constexpr int kStW = 8;
+// Token kinds of the batch kernels. kTkBf16: bf16 tokens. kTkExp: MXFP8 tokens
+// expanded to bf16. kTkF8: MXFP8 tokens as they are on the block-scaled MFMA
+// v_mfma_scale_f32_16x16x128_f8f6f4.
+constexpr int kTkBf16 = 0, kTkExp = 1, kTkF8 = 2;
 
-template <int NM, bool X8, int NT>
-__global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_blocks)
+typedef __attribute__((address_space(3))) void lds_void;
+
+#ifdef __HIP_DEVICE_COMPILE__
+// A buffer resource over the 4 GiB behind p: the direct loads take 32-bit
+// offsets from it (and, unlike those of the global form, leave the waits for
+// loads into registers exact).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_src(const uint8_t *p, int bytes = -1)
 {
-    __shared__ float4 red[kStW / 2][NM][2][NT][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
-    const int rb = blockIdx.x % row_blocks, tb = blockIdx.x / row_blocks;
-    const int n0 = 32 * rb, t0 = 16 * NT * tb;
-    const int KB = p.K / 32, NC = (KB + 3) / 4;
-    const uint8_t *wr[NM][2], *sr[NM][2];
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int64_t n = min(n0 + 16 * r + l16, p.N - 1);
-            wr[m][r] = p.w[m] + n * (p.K / 2);
-            sr[m][r] = p.ws[m] + n * KB;
-        }
-    constexpr int ES = X8 ? 1 : 2;
-    const uint8_t *xr[NT], *xsr[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int64_t tx = min(t0 + 16 * t + l16, p.T - 1);
-        xr[t] = static_cast<const uint8_t *>(p.x) + tx * p.xst * ES;
-        xsr[t] = p.xs + tx * p.xsst;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, bytes, 0x00020000);
+}
+#endif
+
+// Waits until at most N of the wave's memory loads are in flight and its LDS
+// traffic is done, then for the block.
+template <int N>
+__device__ __forceinline__ void tile_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The scaled MFMA's fp8 operand of 16 tokens (lane group g: columns
+// [16g, 16g + 16) in lo, [64 + 16g, 80 + 16g) in hi of 128) with its scale byte
+// s (block g). A dropped group's values lie in lanes of two groups: found on the
+// wave's ballot, which is almost always empty.
+__device__ __forceinline__ v8i f8_operand(u4 lo, u4 hi, int &s)
+{
+    if (__any(s == 255)) {
+        const int l16 = threadIdx.x & 15, h = (threadIdx.x & 63) >> 5;   // blocks h and 2 + h are held here
+        if (__shfl(s, 16 * h + l16) == 255) lo = u4{0u, 0u, 0u, 0u};
+        if (__shfl(s, 32 + 16 * h + l16) == 255) hi = u4{0u, 0u, 0u, 0u};
+        if (s == 255) s = 127;
     }
+    return b_operand(lo, hi);
+}
+
+// ---------------------------------------------------------------------------
+// More tokens on a card that tiles would not fill. A block owns 32 rows of
+// each matrix and 16 NT tokens; its eight waves take the chunks of 128
+// columns in turn, eight chunks (a phase) at a time, and add their sums at the
+// end in wave order. The tokens of a phase go into LDS by direct loads of
+// whole rows (read from memory in operand order, a fragment would touch 64
+// lines per load: 48 tokens x 7168 x 7168 took 26 us so); weights go straight
+// to the registers of the one wave that needs them.
+//
+// LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15).
+constexpr int kStW = 8;
+template <int TK> __host__ __device__ constexpr int st_es() { return TK == kTkBf16 ? 2 : 1; }  // bytes per token element
+constexpr int kMaxLds = 163840;
+template <int NM, int TK, int NT> __host__ __device__ constexpr int st_x() { return 16 * NT * 1024 * st_es<TK>(); }   // tokens of a phase
+template <int NM, int TK, int NT> __host__ __device__ constexpr int st_buf() { return st_x<NM, TK, NT>() + kStW * NM * 2048; }
+template <int NM, int TK, int NT> __host__ __device__ constexpr int st_nbuf() { return 3 * st_buf<NM, TK, NT>() <= kMaxLds ? 3 : 2; }
+template <int NM, int TK, int NT> __host__ __device__ constexpr int st_lds()
+{
+    constexpr int x = st_nbuf<NM, TK, NT>() * st_buf<NM, TK, NT>(), red = kStW / 2 * NM * 2 * NT * 1024;
+    static_assert(x <= kMaxLds && red <= kMaxLds, "a block's LDS");
+    return x > red ? x : red;
+}
+
+template <int NM, int TK, int NT>
+__global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_blocks)
+{
+#ifdef __HIP_DEVICE_COMPILE__   // the buffer resource type exists on the device side only
+    constexpr int ES = st_es<TK>(), XBUF = st_x<NM, TK, NT>(), BUF = st_buf<NM, TK, NT>(), NB = st_nbuf<NM, TK, NT>(), D = NB - 1;
+    constexpr int XL = 2 * NT * ES;               // direct loads per wave and phase
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
+    const int uw = __builtin_amdgcn_readfirstlane(wave);
+    // block b runs on XCD b mod 8: each XCD takes one run of blocks, those of the same rows next to each other
+    const int nt = gridDim.x, xcd = blockIdx.x & 7, per = nt >> 3, rest = nt & 7;
+    const int at = xcd * per + min(xcd, rest) + (int)(blockIdx.x >> 3);
+    const int rb = at / tok_blocks, tb = at - rb * tok_blocks;
+    const int n0 = 32 * rb, t0 = 16 * NT * tb;
+    const int KB = p.K / 32, NC = (KB + 3) / 4, NP = (NC + kStW - 1) / kStW;   // chunks, phases
+    // wave w multiplies the chunks [c0(w), c0(w + 1)) of 128 columns, one per phase
+    auto c0 = [&](int w) { return NC * w / kStW; };
+    const int cw = c0(wave), cn = c0(wave + 1) - cw;
+    // Weights, four lanes per row (a lane of the MFMA's order per row would cost the address unit a cycle per
+    // lane): load i brings 16 bytes x 4 of rows 16 i .. 16 i + 15, slot j of row r at j ^ (r / 4 mod 4).
+    const uint8_t *sr[NM][2];
+    __amdgpu_buffer_rsrc_t wsrc[NM];
+    uint32_t wo[2];
+    int64_t sleft[2], xleft[NT];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) wsrc[m] = buf_src(p.w[m] + (size_t)n0 * (p.K / 2));
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int64_t ns = min(n0 + 16 * r + l16, p.N - 1);
+        wo[r] = (uint32_t)min(16 * r + (lane >> 2), p.N - 1 - n0) * (uint32_t)(p.K / 2);
+        sleft[r] = (p.N - ns) * KB;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) sr[m][r] = p.ws[m] + ns * KB;
+    }
+    const int wj = (lane & 3) ^ (lane >> 4);      // this lane's block of a chunk
+    const uint8_t *xsr[NT];
+    if constexpr (TK != kTkBf16) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int64_t tt = min(t0 + 16 * t + l16, p.T - 1);
+            xsr[t] = p.xs + tt * p.xsst;
+            xleft[t] = (p.T - 1 - tt) * p.xsst + KB;
+        }
+    }
+    auto wload = [&](int ph, int buf) {
+        const int kc = min(4 * (cw + max(min(ph, cn - 1), 0)) + wj, KB - 1);   // (a wave may have no chunk)
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc[m], (lds_void *)(lds + buf * BUF + XBUF + ((uw * NM + m) * 2 + r) * 1024),
+                                                         16, (int)(wo[r] + 16u * (uint32_t)kc), 0, 0, 0);
+        asm volatile("" ::: "memory");            // no load moves behind the products
+    };
+    struct Scales {                               // of 16 phases
+        u4 w[NM][2], x[TK == kTkBf16 ? 1 : NT];
+    };
+    auto sload = [&](int seg, Scales &q) {
+        const int o = 4 * min(cw + 16 * seg, (KB - 1) / 4);
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) q.w[m][r] = run_load(sr[m][r] + o, sleft[r] - o, (int64_t)p.N * KB, g);
+        if constexpr (TK != kTkBf16) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) q.x[t] = run_load(xsr[t] + o, xleft[t] - o, (p.T - 1) * p.xsst + KB, g);
+        }
+    };
+    // direct loads: 64 slots of one row per wave and load, those of all eight waves' chunks
+    const int last = p.K * ES / 16 - 1;           // last slot of a token row
+    auto xload = [&](int ph, int buf) {
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const int q = kStW * i + uw, row = q / ES, half = q - row * ES;
+            const __amdgpu_buffer_rsrc_t src =
+                buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)min(t0 + row, p.T - 1) * p.xst * ES, 0x7fffffff);
+            const uint32_t none = t0 + row < p.T ? 0u : 0x80000000u;   // rows past the last token: outside, read as zeros
+            const int j = (64 * half + lane) ^ (row & 15), w = j / (8 * ES);   // the slot this lane brings, its wave
+            const int slot = min(8 * ES * (c0(w) + ph) + (j & (8 * ES - 1)), last);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void *)(lds + buf * BUF + 1024 * q), 16,
+                                                     (int)(16u * (uint32_t)slot | none), 0, 0, 0);
+        }
+        asm volatile("" ::: "memory");            // no load moves behind the products
+    };
     v4f acc[NM][2][NT];
 #pragma unroll
     for (int m = 0; m < NM; ++m)
@@ -308,78 +457,112 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[m][r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    struct Chunk {
-        u4 a[NM][2], x[NT][X8 ? 2 : 4];
-        uint32_t s[NM][2], xs[NT];
-    };
-    auto load = [&](int c, Chunk &q) {
-        const int kc = min(4 * c + g, KB - 1);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int i = 0; i < 2 * ES; ++i) q.x[t][i] = *reinterpret_cast<const u4 *>(xr[t] + (32 * ES) * (int64_t)kc + 16 * i);
-            if constexpr (X8) q.xs[t] = xsr[t][kc];
-        }
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                q.a[m][r] = *reinterpret_cast<const u4 *>(wr[m][r] + 16 * (int64_t)kc);
-                q.s[m][r] = sr[m][r][kc];
-            }
-    };
-    auto mul = [&](int c, const Chunk &q) {
-        const uint32_t past = 4 * c + g < KB ? 0u : ~0u;   // past the last block: zero weights
+    // phase ph = 16 seg + 4 quarter + k with the scales of its segment
+    auto mul = [&](int ph, int quarter, int k, const Scales &sc, int buf) {
+        const uint32_t past = 4 * (cw + ph) + g < KB && ph < cn ? 0u : ~0u;   // no block of this wave: zero weights
+        const uint8_t *B = lds + buf * BUF + l16 * 1024 * ES;
+        const uint8_t *A = lds + buf * BUF + XBUF + wave * NM * 2048 + 64 * l16 + 16 * (g ^ (l16 >> 2));
+        const int from = 16 * quarter + l16;      // the lane that holds the phase's scales
         u4 a[NM][2];
-        float f[NM][2];
+        uint32_t sw[NM][2], xsb[NT];
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const uint32_t keep = keep_mask(q.s[m][r], past);
-                a[m][r] = and_u4(q.a[m][r], keep);
-                f[m][r] = scale_f32(q.s[m][r] & keep);
+                const uint32_t sv = ((uint32_t)__shfl((int)sc.w[m][r][k], from) >> (8 * g)) & 0xffu, keep = keep_mask(sv, past);
+                a[m][r] = and_u4(*reinterpret_cast<const u4 *>(A + (2 * m + r) * 1024), keep);
+                sw[m][r] = sv & keep;
             }
-        uint32_t xk[NT];
-        float xf[NT];
-        if constexpr (X8) {
+        if constexpr (TK != kTkBf16) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                xk[t] = keep_mask(q.xs[t], 0u);
-                xf[t] = scale_f32(q.xs[t] & xk[t]);
-            }
+            for (int t = 0; t < NT; ++t) xsb[t] = ((uint32_t)__shfl((int)sc.x[t][k], from) >> (8 * g)) & 0xffu;
         }
+        // every fragment of the chunk is read before the first product (the compiler would read each where it
+        // is used, a wait of the LDS's latency every few MFMAs)
+        constexpr int XF = TK == kTkBf16 ? 4 : 2;
+        u4 x[NT][XF];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            bf8 w[NM][2];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) w[m][r] = dequant8_bf16(a[m][r][s], f[m][r]);
+            for (int i = 0; i < XF; ++i) {
+                const int slot = TK == kTkBf16 ? 16 * wave + 4 * g + i : TK == kTkExp ? 8 * wave + 2 * g + i : 8 * wave + 4 * i + g;
+                x[t][i] = *reinterpret_cast<const u4 *>(B + 16384 * ES * t + 16 * (slot ^ l16));
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (TK == kTkF8) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                bf8 b;
-                if constexpr (X8) b = expand8_fp8(q.x[t][s >> 1][2 * (s & 1)] & xk[t], q.x[t][s >> 1][2 * (s & 1) + 1] & xk[t], xf[t]);
-                else b = as_bf8(q.x[t][s]);
+                int sx = (int)xsb[t];
+                const v8i b = f8_operand(x[t][0], x[t][1], sx);
 #pragma unroll
                 for (int m = 0; m < NM; ++m)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) acc[m][r][t] = mfma_bf16(w[m][r], b, acc[m][r][t]);
+                    for (int r = 0; r < 2; ++r)
+                        acc[m][r][t] = mfma_fp4_fp8(a_operand(a[m][r]), b, acc[m][r][t], (int)sw[m][r], sx);
+            }
+        } else {
+            float xf[NT];
+            if constexpr (TK == kTkExp) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t keep = keep_mask(xsb[t], 0u);
+                    x[t][0] = and_u4(x[t][0], keep), x[t][1] = and_u4(x[t][1], keep);
+                    xf[t] = scale_f32(xsb[t] & keep);
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                bf8 w[NM][2];
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) w[m][r] = dequant8_bf16(a[m][r][s], scale_f32(sw[m][r]));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    bf8 b;
+                    if constexpr (TK == kTkExp) b = expand8_fp8(x[t][s >> 1][2 * (s & 1)], x[t][s >> 1][2 * (s & 1) + 1], xf[t]);
+                    else b = as_bf8(x[t][s]);
+#pragma unroll
+                    for (int m = 0; m < NM; ++m)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) acc[m][r][t] = mfma_bf16(w[m][r], b, acc[m][r][t]);
+                }
             }
         }
     };
-    const int c0 = NC * wave / kStW, c1 = NC * (wave + 1) / kStW;
-    Chunk qa, qb;
-    if (c0 < c1) load(c0, qa);
-    for (int c = c0; c < c1; c += 2) {
-        if (c + 1 < c1) load(c + 1, qb);
-        mul(c, qa);
-        if (c + 1 < c1) {
-            if (c + 2 < c1) load(c + 2, qa);
-            mul(c + 1, qb);
-        }
+
+    // Pipeline. A phase's tokens and weights are loaded D phases ahead; phase ph
+    // waits until only the loads of the D - 1 phases behind it are in flight,
+    // and for the block. A buffer is loaded again behind the barrier that
+    // follows the phase which read it. Phases past a wave's last load it again
+    // and are not multiplied.
+    constexpr int LPP = XL + 2 * NM;              // loads per phase
+    Scales sc;
+    sload(0, sc);
+#pragma unroll
+    for (int k = 0; k < D; ++k) {
+        wload(k, k);
+        xload(min(k, NP - 1), k);
     }
-    // the upper half of the waves hands its sums to the lower half, which keeps wave order: (w) + (w + 4)
+    int cur = 0, in = D;
+    for (int ph = 0; ph < NP; ph += 4) {
+        if (ph > 0 && ph % 16 == 0) sload(ph / 16, sc);
+        static_for<0, 4>([&](auto kk) {
+            constexpr int k = decltype(kk)::value;
+            if (ph + k < NP) {
+                tile_barrier<LPP *(D - 1)>();
+                wload(ph + k + D, in);
+                xload(min(ph + k + D, NP - 1), in);
+                mul(ph + k, (ph >> 2) & 3, k, sc, cur);
+                cur = cur == NB - 1 ? 0 : cur + 1;
+                in = in == NB - 1 ? 0 : in + 1;
+            }
+        });
+    }
+    tile_barrier<0>();   // the buffers become the sums' area
+
+    // the upper half of the waves hands its sums to the lower half: (w) + (w + 4), then in wave order
+    float4 *red = reinterpret_cast<float4 *>(lds);
     auto put = [&](int w) {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
@@ -387,10 +570,11 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)   // [token][row]: lane l16 holds rows 4g + i of token l16
-                    red[w][m][r][t][4 * l16 + g] = float4{acc[m][r][t][0], acc[m][r][t][1], acc[m][r][t][2], acc[m][r][t][3]};
+                    red[(((w * NM + m) * 2 + r) * NT + t) * 64 + 4 * l16 + g] =
+                        float4{acc[m][r][t][0], acc[m][r][t][1], acc[m][r][t][2], acc[m][r][t][3]};
     };
     if (wave >= kStW / 2) put(wave - kStW / 2);
-    __syncthreads();
+    tile_barrier<0>();
     if (wave < kStW / 2) {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
@@ -398,28 +582,28 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const float4 z = red[wave][m][r][t][4 * l16 + g];
+                    const float4 z = red[(((wave * NM + m) * 2 + r) * NT + t) * 64 + 4 * l16 + g];
                     acc[m][r][t] += v4f{z.x, z.y, z.z, z.w};
                 }
         put(wave);
     }
-    __syncthreads();
+    tile_barrier<0>();
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-        const int tok = (tid >> 5), row = tid & 31;
+        const int tok = tid >> 5, row = tid & 31, t = t0 + 16 * q + tok;
         float v[NM];
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             v[m] = 0.0f;
 #pragma unroll
             for (int w = 0; w < kStW / 2; ++w)
-                v[m] += reinterpret_cast<const float *>(&red[w][m][row >> 4][q][0])[16 * tok + (row & 15)];
+                v[m] += reinterpret_cast<const float *>(red + (((w * NM + m) * 2 + (row >> 4)) * NT + q) * 64)[16 * tok + (row & 15)];
         }
         float y = v[0];
         if constexpr (NM == 2) y = act_fn(v[0], v[1], p.act, p.b1, p.b2);
-        const int t = t0 + 16 * q + tok;
         dense_store(p, t, n0 + row, t < p.T && n0 + row < p.N, y);
     }
+#endif
 }
 
 // ---------------------------------------------------------------------------
@@ -435,23 +619,6 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int row_
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15), so a
 // fragment read (one slot of 16 rows) touches every bank once.
 constexpr int kTlRows = 256, kTlTok = 128, kTlWaves = 8;
-// kTkBf16: bf16 tokens. kTkExp: MXFP8 tokens expanded to bf16 on their way
-// into LDS. kTkF8: MXFP8 tokens on the block-scaled MFMA
-// v_mfma_scale_f32_16x16x128_f8f6f4 as they are.
-constexpr int kTkBf16 = 0, kTkExp = 1, kTkF8 = 2;
-
-typedef __attribute__((address_space(3))) void lds_void;
-
-#ifdef __HIP_DEVICE_COMPILE__
-// A buffer resource over the 4 GiB behind p: the direct loads take 32-bit
-// offsets from it (and, unlike those of the global form, leave the waits for
-// loads into registers exact).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_src(const uint8_t *p)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, -1, 0x00020000);
-}
-#endif
-
 // Four neighbouring results (columns n .. n + 3 of token t; the 8 lanes of an
 // octet hold one group of 32 columns). nin: how many of them exist (0: none).
 __device__ __forceinline__ void dense_store4(const DenseParams &p, int64_t t, int n, int nin, float4 y)
@@ -509,16 +676,6 @@ constexpr int kTlWBuf = kTlRows * 64, kTlSRows = 64 * kTlWaves;  // one scale dw
 template <int TK> __host__ __device__ constexpr int tl_buf() { return kTlTok * tl_xrow<TK>() + kTlWBuf + 4 * kTlSRows; }
 template <int TK> __host__ __device__ constexpr int tl_lds() { return tl_nbuf<TK>() * tl_buf<TK>(); }
 
-// Waits until at most N of the wave's memory loads are in flight and its LDS
-// traffic is done, then for the block.
-template <int N>
-__device__ __forceinline__ void tile_barrier()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 // LDS stores of the tile pipeline. As plain stores the compiler would first
 // wait for every direct load in flight, which may write the same LDS for all
 // it knows; tile_barrier waits for them. (The LDS address is the low half of
@@ -561,7 +718,7 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     for (int i = 0; i < 2; ++i) wo[i] = (uint32_t)min(lrow((tid >> 2) + 128 * i), p.N - 1 - n0) * (uint32_t)(p.K / 2);
     __amdgpu_buffer_rsrc_t wsrc[NM];
 #pragma unroll
-    for (int m = 0; m < NM; ++m) wsrc[m] = tile_src(p.w[m] + (size_t)n0 * (p.K / 2));
+    for (int m = 0; m < NM; ++m) wsrc[m] = buf_src(p.w[m] + (size_t)n0 * (p.K / 2));
     const int wj = (tid & 3) ^ ((tid >> 4) & 3);  // slot j of row r lies at j ^ (r / 4 mod 4)
     auto wdirect = [&](int k, int buf) {
         const uint32_t kc = 16u * (uint32_t)min(4 * k + wj, KB - 1);
@@ -591,7 +748,7 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     const uint8_t *xb = static_cast<const uint8_t *>(p.x);
     const uint8_t *xr[EP], *xsr[EP];
     uint32_t xo[XP];
-    const __amdgpu_buffer_rsrc_t xsrc = tile_src(xb + (int64_t)t0 * p.xst * ES);
+    const __amdgpu_buffer_rsrc_t xsrc = buf_src(xb + (int64_t)t0 * p.xst * ES);
     if constexpr (TK == kTkExp) {
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
@@ -667,33 +824,13 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
             s4[r] = sv & keep;
         }
         if constexpr (TK == kTkF8) {
-            // the fp8 operand of lane group g: columns [16g, 16g + 16) and [64 + 16g, 80 + 16g) of
-            // the step; its scale: block g
-            u4 lo[4], hi[4];
-            int sx[4];
-            bool any = false;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                lo[t] = *reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * (g ^ (l16 >> 1)));
-                hi[t] = *reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * ((4 + g) ^ (l16 >> 1)));
-                sx[t] = (int)((*reinterpret_cast<const uint32_t *>(S + 4 * (kTlRows + 64 * wt + 16 * t + l16)) >> (8 * g)) & 0xffu);
-                any |= sx[t] == 255;
-            }
-            if (__any(any)) {  // dropped groups: the values of blocks g / 2 and 2 + g / 2 are held here
+                int sx = (int)((*reinterpret_cast<const uint32_t *>(S + 4 * (kTlRows + 64 * wt + 16 * t + l16)) >> (8 * g)) & 0xffu);
+                const v8i b = f8_operand(*reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * (g ^ (l16 >> 1))),
+                                         *reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * ((4 + g) ^ (l16 >> 1))), sx);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if (__shfl(sx[t], 16 * (g >> 1) + l16) == 255) lo[t] = u4{0u, 0u, 0u, 0u};
-                    if (__shfl(sx[t], 32 + 16 * (g >> 1) + l16) == 255) hi[t] = u4{0u, 0u, 0u, 0u};
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (sx[t] == 255) sx[t] = 127;
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const v8i b = b_operand(lo[t], hi[t]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r][t] = mfma_fp4_fp8(a_operand(a[r]), b, acc[r][t], (int)s4[r], sx[t]);
+                for (int r = 0; r < 4; ++r) acc[r][t] = mfma_fp4_fp8(a_operand(a[r]), b, acc[r][t], (int)s4[r], sx);
             }
         } else {
 #pragma unroll
@@ -809,10 +946,16 @@ void launch_gemv(const DenseParams &p, int tiles, int blocks, hipStream_t s)
     k_mx_gemv<NM, X8, RT, U><<<(unsigned)blocks, 64 * nw, lds, s>>>(p, tiles);
 }
 
-template <int NM, bool X8, int NT>
-void launch_stream(const DenseParams &p, int64_t rb, int64_t tb, hipStream_t s)
+template <int NM, int TK, int NT>
+k3moe_status launch_stream(const DenseParams &p, hipStream_t s)
 {
-    k_mx_stream<NM, X8, NT><<<(unsigned)(rb * tb), 64 * kStW, 0, s>>>(p, (int)rb);
+    const int64_t rb = ((int64_t)p.N + 31) / 32, tb = ((int64_t)p.T + 16 * NT - 1) / (16 * NT);
+    if (rb * tb > kMaxItems / (64 * kStW)) return K3MOE_E_UNSUPPORTED_SHAPE;
+    if (st_lds<NM, TK, NT>() > 65536)
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_stream<NM, TK, NT>),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, st_lds<NM, TK, NT>());
+    k_mx_stream<NM, TK, NT><<<(unsigned)(rb * tb), 64 * kStW, st_lds<NM, TK, NT>(), s>>>(p, (int)tb);
+    return K3MOE_OK;
 }
 
 template <int NM, bool X8>
@@ -825,13 +968,22 @@ k3moe_status launch_few(const DenseParams &p, hipStream_t s)
         else launch_gemv<NM, X8, 1, 4>(p, t1, kGvBlocks, s);
         return K3MOE_OK;
     }
-    const int nt = p.T > 32 ? 4 : p.T > 16 ? 2 : 1;
-    const int64_t rb = ((int64_t)p.N + 31) / 32, tb = ((int64_t)p.T + 16 * nt - 1) / (16 * nt);
-    if (rb * tb > kMaxItems / (64 * kStW)) return K3MOE_E_UNSUPPORTED_SHAPE;
-    if (nt == 4) launch_stream<NM, X8, NM == 2 ? 2 : 4>(p, rb, NM == 2 ? ((int64_t)p.T + 31) / 32 : tb, s);
-    else if (nt == 2) launch_stream<NM, X8, 2>(p, rb, tb, s);
-    else launch_stream<NM, X8, 1>(p, rb, tb, s);
-    return K3MOE_OK;
+    // token tiles per block: as many as the batch has, if the LDS holds them (bf16: two, or one of two
+    // matrices; MXFP8: four or three)
+    constexpr int most = !X8 ? 3 - NM : NM == 2 ? 3 : 4;
+    const int nt = (int)((p.T + 15) / 16), blocks = (nt + most - 1) / most, per = (nt + blocks - 1) / blocks;
+    auto go = [&](auto tk) {
+        constexpr int TK = decltype(tk)::value;
+        if (per == 1) return launch_stream<NM, TK, 1>(p, s);
+        if constexpr (most >= 2)
+            if (per == 2) return launch_stream<NM, TK, 2>(p, s);
+        if constexpr (most >= 3)
+            if (per == 3) return launch_stream<NM, TK, 3>(p, s);
+        return launch_stream<NM, TK, most>(p, s);
+    };
+    if constexpr (!X8) return go(std::integral_constant<int, kTkBf16>{});
+    else if (p.kind == K3MOE_OUT_BF16) return go(std::integral_constant<int, kTkF8>{});
+    else return go(std::integral_constant<int, kTkExp>{});
 }
 
 // Batches of more tokens than this run on tiles.
