@@ -257,6 +257,33 @@ def test_linear_sizes(T, N, K, x8):
         _linear(T, N, K, x8, out)
 
 
+# wide matrices: many row tiles per block for a few tokens (from 65521 rows, and
+# from 16385 to MXFP8), the tile kernel for batches (ragged in every direction)
+@pytest.mark.parametrize("T,N,K,out", [
+    (1, 65521, 96, "f32"), (4, 66001, 288, "bf16"), (2, 70000, 1056, "add"), (3, 16500, 160, "mxfp8"),
+    (130, 20001, 160, "f32"), (257, 9000, 352, "bf16"), (300, 9001, 1056, "add"), (1000, 4129, 640, "mxfp8"),
+    (129, 16640, 2048, "bf16"), (70, 33000, 128, "f32"), (2100, 2090, 416, "f32"), (385, 16001, 96, "bf16")])
+@pytest.mark.parametrize("x8", [False, True])
+def test_linear_wide(T, N, K, out, x8):
+    _linear(T, N, K, x8, out, pad=3 if N % 2 else 0)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 66000, 96), (4, 16500, 288), (130, 20001, 160), (600, 5000, 352)])
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("out", ["bf16", "mxfp8"])
+def test_glu_wide(T, N, K, x8, out):
+    _glu_scaled(T, N, K, x8, out, 1)
+
+
+# every number of 16-token tiles, every last phase and scale run of the streaming kernel
+@pytest.mark.parametrize("T", [5, 16, 17, 32, 33, 48, 49, 64, 66])
+@pytest.mark.parametrize("K", [32, 96, 128, 1024, 1152, 4128, 16416, 18432])
+@pytest.mark.parametrize("x8", [False, True])
+def test_linear_streamed(T, K, x8):
+    for out in ("f32", "bf16"):
+        _linear(T, 45, K, x8, out)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 100, 7168), (5, 130, 2080), (48, 257, 1536), (300, 160, 1056), (2048, 256, 512)])
 @pytest.mark.parametrize("x8", [False, True])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
