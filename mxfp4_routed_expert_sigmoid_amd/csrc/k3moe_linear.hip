@@ -475,7 +475,10 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
             }
         if constexpr (TK != kTkBf16) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) xsb[t] = ((uint32_t)__shfl((int)sc.x[t][k], from) >> (8 * g)) & 0xffu;
+            for (int t = 0; t < NT; ++t) {   // (every lane takes part in the exchange)
+                const uint32_t sx = ((uint32_t)__shfl((int)sc.x[t][k], from) >> (8 * g)) & 0xffu;
+                xsb[t] = (sx & ~past) | (127u & past);   // past the last block: any finite scale, the weights are zeros
+            }
         }
         // every fragment of the chunk is read before the first product (the compiler would read each where it
         // is used, a wait of the LDS's latency every few MFMAs)

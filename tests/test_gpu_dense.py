@@ -386,6 +386,32 @@ def test_a_token_that_is_not_finite_stays_alone(T, x8):
     assert np.array_equal(got[keep], (xv @ R.dense(p, s).T)[keep])
 
 
+@pytest.mark.parametrize("T", [2, 6, 20, 200])
+@pytest.mark.parametrize("K", [96, 1056, 2080])
+def test_what_lies_behind_a_row_is_not_used(T, K):
+    # scale bytes behind a row's last block (the next token's first, or padding) are far out of the row's
+    # range: read by the kernels in wide loads, they must not reach a result
+    _need()
+    N = 40
+    r = np.random.default_rng([T, K])
+    p, s = _weights(N, K, r, "exact")
+    q = R.e4m3_rne(r.integers(-15, 16, (T, K)).astype(np.float64))
+    q[:, K - 32:] |= 0x78                            # large last blocks: not zeros
+    q[:, K - 32:] &= 0xfd
+    q[:, :32] = R.e4m3_rne(r.integers(-1, 2, (T, 32)).astype(np.float64))   # (15 * 2^127 would be infinite)
+    xsb = np.full((T, K // 32), 127, np.uint8)
+    xsb[:, 0] = 254                                  # every row's first block 2^127, its weights dropped
+    s[:, 0] = 255
+    wide = np.full((T, K // 32 + 16), 254, np.uint8)
+    wide[:, :K // 32] = xsb
+    want = R.tokens8(q[:, 32:], xsb[:, 1:]) @ R.dense(p, s)[:, 32:].T
+    for xs in (_t(xsb), _t(wide)[:, :K // 32]):
+        out = torch.empty((T, N), device=DEV)
+        k3.linear(_t(p), _t(s), _t(q), out, xs=xs)
+        got = out.double().cpu().numpy()
+        assert np.array_equal(got, want)
+
+
 def test_no_tokens():
     _need()
     p, s = (torch.zeros((8, w), dtype=torch.uint8, device=DEV) for w in (16, 1))
