@@ -393,8 +393,8 @@ typedef enum {
     K3MOE_ADD_F32 = 2
 } k3moe_add;
 
-/* The residual addition and the norm behind it, for T tokens of width H (any
- * H >= 1):
+/* The residual addition and the norm behind it, for T tokens of width H (1 to
+ * 2^30, K3MOE_E_UNSUPPORTED_SHAPE above):
  *   h[t] += d[t]                                  fp32, one rounding
  *   v = h[t] * inv * gamma, inv = (float)(1 / sqrt(sum h^2 / H + eps))
  *       (the numbers of k3moe_step's norm: fp64 sum, two fp32 products)

@@ -465,12 +465,16 @@ def _mat(t, rows, width, dtypes, name, dev):
     number `dev`, unit stride within a row. Returns its address and row stride
     (its width, for fewer than two rows). These calls take about 5 us on the
     device for one token, so the checks use the cheapest accessors."""
-    if tuple(t.shape) != (rows, width):
+    if t.shape != (rows, width):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, width)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if rows >> 31 or width >> 31:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, rows and columns are counted in 32 bits")
     if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{dev}" if dev >= 0 else "a GPU"))
+    if t.is_contiguous():
+        return t.data_ptr(), width
     st, unit = t.stride()
     if unit != 1 and width > 1:
         raise ValueError(f"{name}: a row must be contiguous")
@@ -490,18 +494,20 @@ def _vec(t, n, name, dev):
     return t.data_ptr()
 
 
-def _call(fn, what, dev, stream, *args):
-    """fn(*args, stream) with device number `dev` current, on its current
-    stream unless one is given (taken as a raw handle: making a Stream object
-    costs more than the rest of a call)."""
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
-            status = fn(*args, s)
-    else:
-        status = fn(*args, s)
+def _queue(dev, stream):
+    """The stream's raw handle (the current one of device number `dev` by
+    default; making a Stream object costs more than the rest of a call)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _done(status, what):
     if status:
         raise K3MoeError(status, what)
+
+
+def _elsewhere(dev):
+    """Whether `dev` is not the current device (the call is then made with it current)."""
+    return dev != torch._C._cuda_getDevice()
 
 
 def add_norm(h, gamma, eps, d=None, x=None, q=None, qs=None, stream=None):
@@ -527,8 +533,11 @@ def add_norm(h, gamma, eps, d=None, x=None, q=None, qs=None, stream=None):
     if q is not None:
         qp, qst = _mat(q, T, H, _E4M3, "q", dev)
         qsp, qsst = _mat(qs, T, (H + 31) // 32, _E8M0, "qs", dev)
-    _call(lib().k3moe_add_norm, "k3moe_add_norm", dev, stream, hp, hst, dp, dk, dst, T, H, gp, eps, xp, xst,
-          qp, qst, qsp, qsst)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return add_norm(h, gamma, eps, d, x, q, qs, stream)
+    _done(lib().k3moe_add_norm(hp, hst, dp, dk, dst, T, H, gp, eps, xp, xst, qp, qst, qsp, qsst, _queue(dev, stream)),
+          "k3moe_add_norm")
 
 
 _U8 = (torch.uint8,)
@@ -575,7 +584,10 @@ def linear(packed, scales, x, out, xs=None, outs=None, accumulate=False, stream=
     if accumulate and outs is not None:
         raise ValueError("accumulate takes an fp32 out")
     T, tok, res = _dense(x, xs, out, outs, N, K, accumulate, dev)
-    _call(lib().k3moe_linear, "k3moe_linear", dev, stream, wp, sp, N, K, *tok, T, *res)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return linear(packed, scales, x, out, xs, outs, accumulate, stream)
+    _done(lib().k3moe_linear(wp, sp, N, K, *tok, T, *res, _queue(dev, stream)), "k3moe_linear")
 
 
 def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=None, act=ACT_SITU,
@@ -588,4 +600,7 @@ def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=No
     up, us = _weight(up_packed, up_scales, "up_", dev)
     N, K = gate_packed.shape[0], 2 * gate_packed.shape[1]
     T, tok, res = _dense(x, xs, out, outs, N, K, False, dev)
-    _call(lib().k3moe_glu, "k3moe_glu", dev, stream, gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs, outs, act, situ_b1, situ_b2, stream)
+    _done(lib().k3moe_glu(gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res, _queue(dev, stream)), "k3moe_glu")

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
     auto rows = [&](int tile) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const int64_t n = min(16 * (RT * tile + r) + l16, p.N - 1);
+            const int64_t n = min((int64_t)16 * (RT * tile + r) + l16, (int64_t)p.N - 1);
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
                 wr[m][r] = p.w[m] + n * (p.K / 2);

@@ -29,6 +29,7 @@ struct AddNormParams {
 constexpr int kNoD = 0, kDBf16 = 1, kDF32 = 2;
 constexpr int kAnThreads = 256;
 constexpr int kAnHeld = 8192;  // widest row that stays in registers
+constexpr int kAnMaxWidth = 1 << 30;  // columns and a block's steps past them are counted in 32 bits
 
 template <int VEC> struct Vals { float v[VEC]; };
 
@@ -183,11 +184,16 @@ void launch_add_norm(const AddNormParams &p, hipStream_t s)
 {
     const unsigned grid = (unsigned)(p.T < (1 << 20) ? p.T : (1 << 20));
     const int per = (p.H + VEC * kAnThreads - 1) / (VEC * kAnThreads);  // loads per thread
-    if (p.H > kAnHeld) k_add_norm<VEC, DK, 0><<<grid, kAnThreads, 0, s>>>(p);
-    else if (VEC == 4 && per <= 2) k_add_norm<VEC, DK, 2><<<grid, kAnThreads, 0, s>>>(p);
-    else if (VEC == 4 && per <= 4) k_add_norm<VEC, DK, 4><<<grid, kAnThreads, 0, s>>>(p);
-    else if (per <= 8) k_add_norm<VEC, DK, 8><<<grid, kAnThreads, 0, s>>>(p);
-    else k_add_norm<VEC, DK, 32 / VEC><<<grid, kAnThreads, 0, s>>>(p);
+    if (p.H > kAnHeld) {
+        k_add_norm<VEC, DK, 0><<<grid, kAnThreads, 0, s>>>(p);
+    } else if constexpr (VEC == 4) {
+        if (per <= 2) k_add_norm<VEC, DK, 2><<<grid, kAnThreads, 0, s>>>(p);
+        else if (per <= 4) k_add_norm<VEC, DK, 4><<<grid, kAnThreads, 0, s>>>(p);
+        else k_add_norm<VEC, DK, 8><<<grid, kAnThreads, 0, s>>>(p);
+    } else {
+        if (per <= 8) k_add_norm<VEC, DK, 8><<<grid, kAnThreads, 0, s>>>(p);
+        else k_add_norm<VEC, DK, 32><<<grid, kAnThreads, 0, s>>>(p);
+    }
 }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -203,6 +209,7 @@ extern "C" k3moe_status k3moe_add_norm(float *h, int64_t h_stride, const void *d
                                        int64_t qs_stride, void *stream)
 {
     if (T < 0 || H <= 0 || !(eps > 0.0f && eps < INFINITY)) return K3MOE_E_INVALID_ARG;
+    if (H > kAnMaxWidth) return K3MOE_E_UNSUPPORTED_SHAPE;
     if (d ? d_kind != K3MOE_ADD_BF16 && d_kind != K3MOE_ADD_F32 : d_kind != K3MOE_ADD_NONE)
         return K3MOE_E_INVALID_ARG;
     if (T == 0) return K3MOE_OK;

@@ -30,6 +30,13 @@ def test_add_norm_refusals(kw, status):
     assert _norm(**kw) == status
 
 
+def test_add_norm_refuses_rows_that_32_bits_do_not_count():
+    """Columns are counted in 32 bits, a block's steps behind the last one included."""
+    big = 2 ** 31 - 1
+    assert _norm(H=2 ** 30 + 1, hs=big, ds=big, xs=big) == SHAPE
+    assert _norm(H=big, hs=big, ds=big, xs=big) == SHAPE
+
+
 def _linear(**kw):
     a = dict(p=A, s=A + 0x1000, N=32, K=64, x=A + 0x2000, xst=64, xs=None, xsst=0, T=2, out=A + 0x3000, ost=32,
              outs=None, osst=0, kind=k3.OUT_BF16)
@@ -126,6 +133,18 @@ def test_binding_refuses_wrong_tensors_of_the_products(monkeypatch):
         with pytest.raises(ValueError):
             k3.glu(v["packed"], v["scales"], v.get("up_packed", good["packed"]), good["scales"], v["x"], v["out"],
                    xs=v.get("xs"), outs=v.get("outs"))
+
+
+def test_binding_refuses_sizes_past_32_bits(monkeypatch):
+    """A row count would be cut to its low 32 bits on its way into the library."""
+    monkeypatch.setattr(k3, "lib", lambda: pytest.fail("the call was made"))
+    wide = torch.empty(1, 32).expand(2 ** 32 + 2, 32)
+    with pytest.raises(ValueError, match="counted in 32 bits"):
+        k3.add_norm(wide, _z(32), 1e-5, x=wide)
+    x = torch.empty(1, 32, dtype=torch.bfloat16).expand(2 ** 32 + 2, 32)
+    w, s = _z(32, 16, dtype=torch.uint8), _z(32, 1, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        k3.linear(w, s, x, x)
 
 
 def test_numbers_agree_with_the_header():
