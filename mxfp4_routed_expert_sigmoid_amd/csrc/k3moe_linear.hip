@@ -6,13 +6,22 @@
 // byte"), the activation §9's k3_situ_glu.
 //
 // Weights and 8-bit tokens are expanded to bf16 in registers, which is exact
-// (an fp4 or e4m3 value times a power of two is a bf16), and multiplied on
-// v_mfma_f32_16x16x32_bf16: exact products, fp32 sums.
+// (an fp4 or e4m3 value times a power of two is a bf16; one past bf16's range is
+// infinite), and multiplied on v_mfma_f32_16x16x32_bf16: exact products, fp32
+// sums. More than four MXFP8 tokens whose results are rounded to bf16 go as
+// they are to the block-scaled MFMA, 16x16x128 at twice the rate.
 //
-// K mapping. A lane's 16-byte weight load holds one 32-weight block of its
-// row: lane 16g + r of an MFMA tile loads block 4c + g of row r in chunk c (128
-// columns), and step s of the chunk multiplies columns 128c + 32g + 8s + [0, 8)
-// of every g; the token side reads the same columns.
+// Three kernels by the number of tokens, each reading every weight once per
+// block of tokens that it holds:
+//   k_mx_gemv    1 to 4: a stream of weights, bound by memory
+//   k_mx_stream  more, where tiles would not fill the card: bound by what one
+//                CU's direct loads bring
+//   k_mx_tile    batches: bound by the MFMAs and the expansion beside them
+//
+// K mapping. A 16-byte piece of a row is one block of 32 weights: in chunk c
+// (128 columns) lane 16g + r of an MFMA tile holds block 4c + g of row r, and
+// step s of the chunk multiplies columns 128c + 32g + 8s + [0, 8) of every g; the
+// token side reads the same columns.
 #include "k3moe_internal.h"
 #include "k3moe_mx8.h"
 
@@ -106,14 +115,22 @@ __device__ __forceinline__ void dense_store(const DenseParams &p, int64_t t, int
 }
 
 // ---------------------------------------------------------------------------
-// A few tokens: the product is a stream of weights. A block owns 16 RT rows
-// of each matrix; its waves split the columns, so that a narrow matrix still
-// fills the card, and their fp32 sums are added in wave order. A wave reads
-// 16 rows x 256 bytes per unit (512 columns) and matrix tile, the next unit in
-// flight while one is multiplied; its share of the tokens goes into LDS first
-// (behind the first weight loads), so that the loads in flight are all weights.
+// A few tokens: the product is a stream of weights. A block owns tiles of 16
+// rows of each matrix (for an MXFP8 result pairs of them, whose 32 results of a
+// token share a scale); its waves split the columns, so that a narrow matrix
+// still fills the card, and their fp32 sums are added in wave order. A wave
+// reads 16 rows x 128 or 256 bytes per unit (U chunks) and matrix, the next unit
+// in flight while one is multiplied; its share of the tokens goes into LDS
+// first (behind the first weight loads), so that the loads in flight are all
+// weights. A pair's two tiles are taken one after the other: side by side they
+// took 173 registers and half the waves (2 x 18432 x 7168 to MXFP8: 51 us, 37 so).
+//
+// One token, in a graph: 1536 x 7168 5.2 us (a launch and one unit's latency),
+// 7168 x 18432 16.3 us (4.3 TB/s), 2 x 18432 x 7168 34 us (4.1 TB/s); four tokens
+// of 163840 x 7168 127 us (4.9 TB/s). A plain read of such sizes reaches 4 to 6.
 constexpr int kGvTok = 4, kGvMaxWaves = 8;
 constexpr int kGvMaxLds = 65536;   // token bytes of a block
+constexpr int kGvPieces = 8;       // token pieces a lane has in flight (one at a time: 7168 x 28672 31.0 us, 29.2 so)
 // A matrix of fewer tiles has a block for each, which the card schedules as
 // they end (18432 rows x 2 matrices x 7168: 33 us, 39 us with two or three
 // tiles per block); a longer one two blocks per CU, each with many tiles,
@@ -156,7 +173,7 @@ __device__ __forceinline__ void lds_barrier()
     asm volatile("" ::: "memory");
 }
 
-template <int NM, bool X8, int RT, int U>
+template <int NM, bool X8, bool PAIR, int U>
 __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int tiles)
 {
     extern __shared__ __align__(16) uint8_t lds[];
@@ -164,47 +181,43 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
     const int g = lane >> 4, l16 = lane & 15;
     const int KB = p.K / 32, NU = (KB + 4 * U - 1) / (4 * U);
     const int u0 = NU * wave / nw, u1 = NU * (wave + 1) / nw;  // at least one unit each
-    // this block's row tiles (16 RT rows)
-    const int tile0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), tile1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+    // this block's row tiles (PAIR: an even number of them)
+    tiles >>= PAIR;
+    const int tile0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x) << PAIR;
+    const int tile1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x) << PAIR;
     const int xrow = 2 * p.K;                                  // LDS bytes of a token: bf16
     uint8_t *xl = lds;
-    float *red0 = reinterpret_cast<float *>(lds + p.T * xrow); // two of [wave][NM][RT][token][16]
-    const int rsize = nw * NM * RT * kGvTok * 16;
+    float *red0 = reinterpret_cast<float *>(lds + p.T * xrow); // RB of [wave][NM][token][16]
+    constexpr int RB = PAIR ? 4 : 2;
+    const int rsize = nw * NM * kGvTok * 16;
 
-    const uint8_t *wr[NM][RT], *sr[NM][RT];
+    const uint8_t *wr[NM], *sr[NM];
     auto rows = [&](int tile) {
+        const int64_t n = min((int64_t)16 * tile + l16, (int64_t)p.N - 1);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int64_t n = min((int64_t)16 * (RT * tile + r) + l16, (int64_t)p.N - 1);
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                wr[m][r] = p.w[m] + n * (p.K / 2);
-                sr[m][r] = p.ws[m] + n * KB;
-            }
+        for (int m = 0; m < NM; ++m) {
+            wr[m] = p.w[m] + n * (p.K / 2);
+            sr[m] = p.ws[m] + n * KB;
         }
     };
-    GvUnit<U> ua[NM][RT], ub[NM][RT];
+    GvUnit<U> ua[NM], ub[NM];
     int lt = tile0, lu = u0;                                   // the next unit to load
-    auto load = [&](GvUnit<U> (&q)[NM][RT]) {
+    auto load = [&](GvUnit<U> (&q)[NM]) {
         if (lt >= tile1) return;
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) gv_load(q[m][r], wr[m][r], sr[m][r], lu, KB, g);
+        for (int m = 0; m < NM; ++m) gv_load(q[m], wr[m], sr[m], lu, KB, g);
         if (++lu == u1) {
             lu = u0;
             rows(++lt);
         }
     };
-    v4f acc[NM][RT];
+    v4f acc[NM];
     auto clear = [&]() {
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) acc[m][r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int m = 0; m < NM; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     };
     const uint8_t *bx = xl + min(l16, p.T - 1) * xrow;
-    auto mul = [&](int u, const GvUnit<U> (&q)[NM][RT]) {
+    auto mul = [&](int u, const GvUnit<U> (&q)[NM]) {
         bf8 b[U][4];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
@@ -216,64 +229,77 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
 #pragma unroll
         for (int j = 0; j < U; ++j) {
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
+            for (int m = 0; m < NM; ++m) {
+                const uint32_t sw = (q[m].s[j] >> (8 * g)) & 0xffu, keep = keep_mask(sw, 0u);
+                const u4 a = and_u4(q[m].a[j], keep);
+                const float f = scale_f32(sw & keep);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const uint32_t sw = (q[m][r].s[j] >> (8 * g)) & 0xffu, keep = keep_mask(sw, 0u);
-                    const u4 a = and_u4(q[m][r].a[j], keep);
-                    const float f = scale_f32(sw & keep);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) acc[m][r] = mfma_bf16(dequant8_bf16(a[s], f), b[j][s], acc[m][r]);
-                }
+                for (int s = 0; s < 4; ++s) acc[m] = mfma_bf16(dequant8_bf16(a[s], f), b[j][s], acc[m]);
+            }
         }
     };
-    // a tile's sums: added in wave order, one value per thread of the first waves (32 rows, or 16, of a token)
+    // A tile's sums go to LDS; they are added in wave order, one value per thread: 16 rows of a token, or the 32 of
+    // a pair behind its second tile (an MXFP8 group). The areas take turns, so that a wave may be one tile (pair)
+    // ahead of those that still add.
     auto finish = [&](int tile) {
-        float *red = red0 + ((tile - tile0) & 1 ? rsize : 0);
+        const int area = (tile - tile0) & (RB - 1);
+        float *red = red0 + area * rsize;
         if (l16 < p.T) {
 #pragma unroll
             for (int m = 0; m < NM; ++m)
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    *reinterpret_cast<float4 *>(red + (((wave * NM + m) * RT + r) * kGvTok + l16) * 16 + 4 * g) =
-                        float4{acc[m][r][0], acc[m][r][1], acc[m][r][2], acc[m][r][3]};
+                *reinterpret_cast<float4 *>(red + ((wave * NM + m) * kGvTok + l16) * 16 + 4 * g) =
+                    float4{acc[m][0], acc[m][1], acc[m][2], acc[m][3]};
         }
+        clear();
+        if (PAIR && !(area & 1)) return;
         lds_barrier();
-        for (int i = tid; i < 16 * RT * ((p.T + 1) & ~1); i += 64 * nw) {
-            const int row = i % (16 * RT), tok = i / (16 * RT), tc = min(tok, p.T - 1), n = 16 * RT * tile + row;
+        constexpr int ROWS = PAIR ? 32 : 16;
+        if constexpr (PAIR) red -= rsize;                      // the pair's first tile
+        const int n0 = 16 * (tile - PAIR);
+        for (int i = tid; i < ROWS * ((p.T + 1) & ~1); i += 64 * nw) {
+            const int row = i % ROWS, tok = i / ROWS, tc = min(tok, p.T - 1), n = n0 + row;
+            const float *from = red + (row >> 4) * rsize + tc * 16 + (row & 15);
             float v[NM];
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
                 v[m] = 0.0f;
-                for (int w = 0; w < nw; ++w) v[m] += red[(((w * NM + m) * RT + (row >> 4)) * kGvTok + tc) * 16 + (row & 15)];
+                for (int w = 0; w < nw; ++w) v[m] += from[(w * NM + m) * kGvTok * 16];
             }
             float y = v[0];
             if constexpr (NM == 2) y = act_fn(v[0], v[1], p.act, p.b1, p.b2);
-            dense_store(p, tok, n, tok < p.T && n < p.N, y);
+            dense_store(p, tok, n, tok < p.T && row < p.N - n0, y);
         }
-        clear();
     };
 
     rows(tile0);
     load(ua);
     clear();
     {
-        // the wave's columns of every token, as bf16
-        const int c0 = 128 * U * u0, per = (min(128 * U * u1, p.K) - c0) / (X8 ? 16 : 8);   // 16-byte pieces of a token
-        for (int i = lane; i < p.T * per; i += 64) {
-            const int t = i / per, q = i - t * per;
-            if constexpr (X8) {
-                const int c = c0 + 16 * q;
-                const u4 x = *reinterpret_cast<const u4 *>(static_cast<const uint8_t *>(p.x) + t * p.xst + c);
-                const uint32_t sx = p.xs[t * p.xsst + c / 32], keep = keep_mask(sx, 0u);
-                const u4 v = and_u4(x, keep);
-                const float f = scale_f32(sx & keep);
-                bf8 *d = reinterpret_cast<bf8 *>(xl + t * xrow + 2 * c);
-                d[0] = expand8_fp8(v.x, v.y, f), d[1] = expand8_fp8(v.z, v.w, f);
-            } else {
-                const int c = c0 + 8 * q;
-                *reinterpret_cast<u4 *>(xl + t * xrow + 2 * c) =
-                    *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(p.x) + t * p.xst + c);
+        // the wave's columns of every token, as bf16: pieces of 16 bytes, kGvPieces per lane in flight
+        const int c0 = 128 * U * u0, per = (min(128 * U * u1, p.K) - c0) / (X8 ? 16 : 8), n = p.T * per;   // pieces of a token, of all
+        for (int i0 = lane; i0 < n; i0 += 64 * kGvPieces) {
+            u4 x[kGvPieces];
+            uint32_t sx[X8 ? kGvPieces : 1];
+            int at[kGvPieces];                                 // LDS offsets
+#pragma unroll
+            for (int j = 0; j < kGvPieces; ++j) {
+                const int i = min(i0 + 64 * j, n - 1), t = i / per, c = c0 + (X8 ? 16 : 8) * (i - t * per);
+                at[j] = t * xrow + 2 * c;
+                x[j] = *reinterpret_cast<const u4 *>(static_cast<const uint8_t *>(p.x) + (t * p.xst + c) * (X8 ? 1 : 2));
+                if constexpr (X8) sx[j] = p.xs[t * p.xsst + c / 32];
+            }
+#pragma unroll
+            for (int j = 0; j < kGvPieces; ++j) {
+                if (i0 + 64 * j >= n) break;
+                if constexpr (X8) {
+                    const uint32_t keep = keep_mask(sx[j], 0u);
+                    const u4 v = and_u4(x[j], keep);
+                    const float f = scale_f32(sx[j] & keep);
+                    bf8 *d = reinterpret_cast<bf8 *>(xl + at[j]);
+                    d[0] = expand8_fp8(v.x, v.y, f), d[1] = expand8_fp8(v.z, v.w, f);
+                } else {
+                    *reinterpret_cast<u4 *>(xl + at[j]) = x[j];
+                }
             }
         }
         wave_lds_sync();
@@ -347,9 +373,14 @@ __device__ __forceinline__ v8i f8_operand(u4 lo, u4 hi, int &s)
 // each matrix and 16 NT tokens; its eight waves take the chunks of 128
 // columns in turn, eight chunks (a phase) at a time, and add their sums at the
 // end in wave order. The tokens of a phase go into LDS by direct loads of
-// whole rows (read from memory in operand order, a fragment would touch 64
-// lines per load: 48 tokens x 7168 x 7168 took 26 us so); weights go straight
-// to the registers of the one wave that needs them.
+// whole rows, and so do each wave's weights, four lanes to a row: read from
+// memory in operand order, a load costs the address unit about a cycle per
+// lane (48 MXFP8 tokens x 7168 x 7168: 26 us, 16.5 so).
+//
+// Measured on 7168 rows x 7168: 8 MXFP8 tokens 10 us, 16 bf16 tokens 12 us, 48
+// MXFP8 tokens 16.5 us (300 TFLOP/s, 1.7 TB/s of weights), of which 6.6 are left
+// at one phase: launch, first latency and the joining of the sums. A phase of
+// 64 KB takes 1.2 us, as far as the loads of the one before it let it.
 //
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15).
 constexpr int kStW = 8;
@@ -613,11 +644,18 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 // Tiles for batches. A block of 8 waves owns 256 weight rows (256 of the one
 // matrix, or 128 of each of the two) and 128 tokens; a wave 64 rows x 64
 // tokens (gate and up rows of the same columns, so the activation stays in
-// its lanes). Tokens pass through LDS, 256 bytes of every token per K step,
-// double-buffered with one barrier per step; weights go from memory straight
-// into the registers of the two waves that share them, one step ahead.
-// Rows rather than tokens are the long side because a token's bytes are
-// four times a weight row's: LDS reads take half the cycles of the MFMAs.
+// its lanes). Tokens and packed weights pass through LDS, 128 columns per step,
+// by direct loads into three buffers (four of the smaller MXFP8 steps), one
+// barrier per step; 8-bit tokens that are expanded go through registers, once
+// per block instead of once per wave. Rows rather than tokens are the long
+// side because a token's bytes are four times a weight row's: LDS reads take
+// half the cycles of the MFMAs.
+//
+// 2048 tokens x 7168 x 18432: bf16 510 us (1.06 PFLOP/s; the library's bf16
+// product of that size 522), MXFP8 to bf16 347 us (1.56), MXFP8 to fp32 570 us
+// (0.95: the expansion of the tokens). Of the 510, 349 are left without loads
+// and LDS reads, the MFMAs with the expansion of the weights, and 388 with the
+// reads; 448 tiles on 256 CUs are two rounds of which the second is 3/4 full.
 //
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15), so a
 // fragment read (one slot of 16 rows) touches every bank once.
@@ -936,17 +974,17 @@ void launch_tile(const DenseParams &p, int64_t blocks, int tok_tiles, hipStream_
     k_mx_tile<NM, TK><<<(unsigned)blocks, 64 * kTlWaves, tl_lds<TK>(), s>>>(p, tok_tiles);
 }
 
-template <int NM, bool X8, int RT, int U>
+template <int NM, bool X8, bool PAIR, int U>
 void launch_gemv(const DenseParams &p, int tiles, int blocks, hipStream_t s)
 {
     const int NU = (p.K / 32 + 4 * U - 1) / (4 * U);
     // waves per block: the fewest that give the same longest share as the most
     const int share = (NU + kGvMaxWaves - 1) / kGvMaxWaves, nw = (NU + share - 1) / share;
-    const int lds = p.T * 2 * p.K + 2 * nw * NM * RT * kGvTok * 64;
+    const int lds = p.T * 2 * p.K + (PAIR ? 4 : 2) * nw * NM * kGvTok * 64;
     if (lds > 65536)
-        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_gemv<NM, X8, RT, U>),
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_gemv<NM, X8, PAIR, U>),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, kGvMaxLds + 65536);
-    k_mx_gemv<NM, X8, RT, U><<<(unsigned)blocks, 64 * nw, lds, s>>>(p, tiles);
+    k_mx_gemv<NM, X8, PAIR, U><<<(unsigned)blocks, 64 * nw, lds, s>>>(p, tiles);
 }
 
 template <int NM, int TK, int NT>
@@ -1026,9 +1064,9 @@ template <int NM, bool X8>
 void launch_few(const DenseParams &p, hipStream_t s)
 {
     const int t1 = (int)(((int64_t)p.N + 15) / 16), t2 = (t1 + 1) / 2;
-    if (p.kind == K3MOE_OUT_MXFP8) launch_gemv<NM, X8, 2, 2>(p, t2, t2 < kGvBlocks ? t2 : kGvBlocks, s);  // 32 rows share a scale
-    else if (t1 < kGvLong) launch_gemv<NM, X8, 1, 2>(p, t1, t1, s);
-    else launch_gemv<NM, X8, 1, 4>(p, t1, kGvBlocks, s);
+    if (p.kind == K3MOE_OUT_MXFP8) launch_gemv<NM, X8, true, 2>(p, 2 * t2, t1 < kGvLong ? t2 : kGvBlocks, s);
+    else if (t1 < kGvLong) launch_gemv<NM, X8, false, 2>(p, t1, t1, s);
+    else launch_gemv<NM, X8, false, 4>(p, t1, kGvBlocks, s);
 }
 
 template <int NM>
