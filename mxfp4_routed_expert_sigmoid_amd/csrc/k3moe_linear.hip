@@ -1046,7 +1046,8 @@ k3moe_status launch_batch(const DenseParams &p, hipStream_t s)
         if (u < us) us = u, nt = NT;
     });
     constexpr int64_t es = st_es<TK>();
-    const bool tile_ok = p.K >= 128 && (kTlTok - 1) * p.xst * es + p.K * es < ((int64_t)1 << 32);   // 32-bit offsets
+    constexpr int64_t far = (int64_t)1 << 32;
+    const bool tile_ok = p.K >= 128 && p.xst < far && (kTlTok - 1) * p.xst * es + p.K * es < far;   // 32-bit offsets
     if (tile_ok && tile_us<NM, TK>(p) < us) {
         const int64_t rb = ((int64_t)p.N * NM + kTlRows - 1) / kTlRows, tb = ((int64_t)p.T + kTlTok - 1) / kTlTok;
         if (rb * tb > kMaxItems / (64 * kTlWaves)) return K3MOE_E_UNSUPPORTED_SHAPE;
