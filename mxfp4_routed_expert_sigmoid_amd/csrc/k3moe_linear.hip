@@ -31,6 +31,8 @@ namespace {
 // Widest matrix: a block's rows are addressed by 32-bit offsets (256 rows x
 // 2^22 / 2 bytes).
 constexpr int kMaxCols = 1 << 22;
+// Largest stride of token rows: two neighbouring rows are addressed by 32-bit offsets.
+constexpr int64_t kMaxTokenStride = 1 << 30;
 
 struct DenseParams {
     const uint8_t *w[2], *ws[2];   // packed rows [N][K / 2], scale rows [N][K / 32] (one or two matrices)
@@ -337,7 +339,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 // A buffer resource over the 4 GiB behind p: the direct loads take 32-bit
 // offsets from it (and, unlike those of the global form, leave the waits for
 // loads into registers exact).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_src(const uint8_t *p, int bytes = -1)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_src(const uint8_t *p, int bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, bytes, 0x00020000);
 }
@@ -370,29 +372,38 @@ __device__ __forceinline__ v8i f8_operand(u4 lo, u4 hi, int &s)
 
 // ---------------------------------------------------------------------------
 // More tokens on a card that tiles would not fill. A block owns 32 rows of
-// each matrix and 16 NT tokens; its eight waves take the chunks of 128
-// columns in turn, eight chunks (a phase) at a time, and add their sums at the
-// end in wave order. The tokens of a phase go into LDS by direct loads of
-// whole rows, and so do each wave's weights, four lanes to a row: read from
-// memory in operand order, a load costs the address unit about a cycle per
-// lane (48 MXFP8 tokens x 7168 x 7168: 26 us, 16.5 so).
+// each matrix and 16 NT tokens; each of its eight waves takes one of the two
+// row tiles and every fourth part of the columns, four chunks of 128 columns (a
+// phase) at a time, and the four parts' sums are added at the end in their
+// order. The tokens of a phase go into LDS by direct loads of whole rows, and
+// so do each wave's weights, four lanes to a row: read from memory in operand
+// order, a load costs the address unit about a cycle per lane (48 MXFP8 tokens
+// x 7168 x 7168: 26 us so).
 //
-// Measured on 7168 rows x 7168: 8 MXFP8 tokens 10 us, 16 bf16 tokens 12 us, 48
-// MXFP8 tokens 16.5 us (300 TFLOP/s, 1.7 TB/s of weights), of which 6.6 are left
-// at one phase: launch, first latency and the joining of the sums. A phase of
-// 64 KB takes 1.2 us, as far as the loads of the one before it let it.
+// Measured on 7168 rows x 7168, in a graph: 8 MXFP8 tokens 9.7 us, 16 bf16
+// tokens 11.0, 48 MXFP8 tokens 14.6 (340 TFLOP/s), 48 bf16 tokens 19.5. Bound by what
+// a CU's direct loads bring, 50 to 60 KB/us whatever their order or depth: every
+// block reads its tokens anew, which only more rows per block would change, and
+// those would leave CUs idle. Phases of eight chunks, one per wave and both row
+// tiles: 16.5 us for the 48 MXFP8 tokens, and 64 bf16 tokens do not fit (301 tokens
+// x 1001 x 2080: 16.0 us, 9.8 so).
 //
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15).
-constexpr int kStW = 8;
+constexpr int kStW = 8, kStC = 4;                 // waves, chunks of a phase
+constexpr int kStMaxBuf = 3;                      // (8 MXFP8 tokens x 7168 x 7168: 9.7 us, 10.0 with four buffers, 10.4 with six)
 template <int TK> __host__ __device__ constexpr int st_es() { return TK == kTkBf16 ? 2 : 1; }  // bytes per token element
 constexpr int kMaxLds = 163840;
-template <int NM, int TK, int NT> __host__ __device__ constexpr int st_x() { return 16 * NT * 1024 * st_es<TK>(); }   // tokens of a phase
-template <int NM, int TK, int NT> __host__ __device__ constexpr int st_buf() { return st_x<NM, TK, NT>() + kStW * NM * 2048; }
-template <int NM, int TK, int NT> __host__ __device__ constexpr int st_nbuf() { return 3 * st_buf<NM, TK, NT>() <= kMaxLds ? 3 : 2; }
+template <int NM, int TK, int NT> __host__ __device__ constexpr int st_x() { return 16 * NT * 128 * kStC * st_es<TK>(); }   // tokens of a phase
+template <int NM, int TK, int NT> __host__ __device__ constexpr int st_buf() { return st_x<NM, TK, NT>() + kStW * NM * 1024; }
+template <int NM, int TK, int NT> __host__ __device__ constexpr int st_nbuf()
+{
+    constexpr int n = kMaxLds / st_buf<NM, TK, NT>();
+    return n > kStMaxBuf ? kStMaxBuf : n;
+}
 template <int NM, int TK, int NT> __host__ __device__ constexpr int st_lds()
 {
-    constexpr int x = st_nbuf<NM, TK, NT>() * st_buf<NM, TK, NT>(), red = kStW / 2 * NM * 2 * NT * 1024;
-    static_assert(x <= kMaxLds && red <= kMaxLds, "a block's LDS");
+    constexpr int x = st_nbuf<NM, TK, NT>() * st_buf<NM, TK, NT>(), red = kStW * NM * NT * 1024;
+    static_assert(x <= kMaxLds && red <= kMaxLds && st_nbuf<NM, TK, NT>() >= 2, "a block's LDS");
     return x > red ? x : red;
 }
 
@@ -401,7 +412,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 {
 #ifdef __HIP_DEVICE_COMPILE__   // the buffer resource type exists on the device side only
     constexpr int ES = st_es<TK>(), XBUF = st_x<NM, TK, NT>(), BUF = st_buf<NM, TK, NT>(), NB = st_nbuf<NM, TK, NT>(), D = NB - 1;
-    constexpr int XL = 2 * NT * ES;               // direct loads per wave and phase
+    constexpr int XL = NT * ES;                   // direct loads per wave and phase
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
     const int uw = __builtin_amdgcn_readfirstlane(wave);
@@ -410,26 +421,23 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
     const int at = xcd * per + min(xcd, rest) + (int)(blockIdx.x >> 3);
     const int rb = at / tok_blocks, tb = at - rb * tok_blocks;
     const int n0 = 32 * rb, t0 = 16 * NT * tb;
-    const int KB = p.K / 32, NC = (KB + 3) / 4, NP = (NC + kStW - 1) / kStW;   // chunks, phases
-    // wave w multiplies the chunks [c0(w), c0(w + 1)) of 128 columns, one per phase
-    auto c0 = [&](int w) { return NC * w / kStW; };
-    const int cw = c0(wave), cn = c0(wave + 1) - cw;
+    const int KB = p.K / 32, NC = (KB + 3) / 4, NP = (NC + kStC - 1) / kStC;   // chunks, phases
+    // a wave multiplies one of the two row tiles by the chunks [c0(s), c0(s + 1)) of its slot s, one per phase
+    auto c0 = [&](int s) { return NC * s / kStC; };
+    const int cs = wave & (kStC - 1), rt = wave >> 2;
+    const int cw = c0(cs), cn = c0(cs + 1) - cw;
     // Weights, four lanes per row (a lane of the MFMA's order per row would cost the address unit a cycle per
-    // lane): load i brings 16 bytes x 4 of rows 16 i .. 16 i + 15, slot j of row r at j ^ (r / 4 mod 4).
-    const uint8_t *sr[NM][2];
-    __amdgpu_buffer_rsrc_t wsrc[NM];
-    uint32_t wo[2];
-    int64_t sleft[2], xleft[NT];
+    // lane): a load brings 16 bytes x 4 of the wave's 16 rows, slot j of row r at j ^ (r / 4 mod 4).
+    const uint8_t *sr[NM];
+    int64_t xleft[NT];
+    const int64_t ns = min(n0 + 16 * rt + l16, p.N - 1), sleft = (p.N - ns) * KB;
+    const uint32_t wo = (uint32_t)min(16 * rt + (lane >> 2), p.N - 1 - n0) * (uint32_t)(p.K / 2);
 #pragma unroll
-    for (int m = 0; m < NM; ++m) wsrc[m] = buf_src(p.w[m] + (size_t)n0 * (p.K / 2));
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int64_t ns = min(n0 + 16 * r + l16, p.N - 1);
-        wo[r] = (uint32_t)min(16 * r + (lane >> 2), p.N - 1 - n0) * (uint32_t)(p.K / 2);
-        sleft[r] = (p.N - ns) * KB;
-#pragma unroll
-        for (int m = 0; m < NM; ++m) sr[m][r] = p.ws[m] + ns * KB;
+    for (int m = 0; m < NM; ++m) {
+        sr[m] = p.ws[m] + ns * KB;
     }
+    // a phase behind the last one is loaded from empty buffers: no traffic, and the counts of loads stay
+    auto bytes = [&](int ph) { return ph < NP ? 0x7fffffff : 0; };
     const int wj = (lane & 3) ^ (lane >> 4);      // this lane's block of a chunk
     const uint8_t *xsr[NT];
     if constexpr (TK != kTkBf16) {
@@ -444,66 +452,60 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
         const int kc = min(4 * (cw + max(min(ph, cn - 1), 0)) + wj, KB - 1);   // (a wave may have no chunk)
 #pragma unroll
         for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc[m], (lds_void *)(lds + buf * BUF + XBUF + ((uw * NM + m) * 2 + r) * 1024),
-                                                         16, (int)(wo[r] + 16u * (uint32_t)kc), 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf_src(p.w[m] + (size_t)n0 * (p.K / 2), bytes(ph)),
+                                                     (lds_void *)(lds + buf * BUF + XBUF + (uw * NM + m) * 1024), 16,
+                                                     (int)(wo + 16u * (uint32_t)kc), 0, 0, 0);
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
     struct Scales {                               // of 16 phases
-        u4 w[NM][2], x[TK == kTkBf16 ? 1 : NT];
+        u4 w[NM], x[TK == kTkBf16 ? 1 : NT];
     };
     auto sload = [&](int seg, Scales &q) {
         const int o = 4 * min(cw + 16 * seg, (KB - 1) / 4);
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) q.w[m][r] = run_load(sr[m][r] + o, sleft[r] - o, (int64_t)p.N * KB, g);
+        for (int m = 0; m < NM; ++m) q.w[m] = run_load(sr[m] + o, sleft - o, (int64_t)p.N * KB, g);
         if constexpr (TK != kTkBf16) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) q.x[t] = run_load(xsr[t] + o, xleft[t] - o, (p.T - 1) * p.xsst + KB, g);
         }
     };
-    // direct loads: 64 slots of one row per wave and load, those of all eight waves' chunks
+    // direct loads: 64 slots per wave and load, one row of bf16 tokens or two of 8-bit ones, of all four chunks
+    constexpr int RL = 2 / ES, SL = 64 / RL;      // rows per load, slots per row
     const int last = p.K * ES / 16 - 1;           // last slot of a token row
     auto xload = [&](int ph, int buf) {
 #pragma unroll
         for (int i = 0; i < XL; ++i) {
-            const int q = kStW * i + uw, row = q / ES, half = q - row * ES;
+            const int q = kStW * i + uw, first = RL * q, up = RL == 1 ? 0 : lane >> 5, row = first + up;
             const __amdgpu_buffer_rsrc_t src =
-                buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)min(t0 + row, p.T - 1) * p.xst * ES, 0x7fffffff);
+                buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)min(t0 + first, p.T - 1) * p.xst * ES, bytes(ph));
             const uint32_t none = t0 + row < p.T ? 0u : 0x80000000u;   // rows past the last token: outside, read as zeros
-            const int j = (64 * half + lane) ^ (row & 15), w = j / (8 * ES);   // the slot this lane brings, its wave
+            const int j = (lane & (SL - 1)) ^ (row & 15), w = j / (8 * ES);   // the slot this lane brings, its chunk's
             const int slot = min(8 * ES * (c0(w) + ph) + (j & (8 * ES - 1)), last);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void *)(lds + buf * BUF + 1024 * q), 16,
-                                                     (int)(16u * (uint32_t)slot | none), 0, 0, 0);
+            const uint32_t o = 16u * (uint32_t)slot + (up ? (uint32_t)p.xst : 0u);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void *)(lds + buf * BUF + 1024 * q), 16, (int)(o | none), 0, 0, 0);
         }
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
-    v4f acc[NM][2][NT];
+    v4f acc[NM][NT];
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[m][r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < NT; ++t) acc[m][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
     // phase ph = 16 seg + 4 quarter + k with the scales of its segment
     auto mul = [&](int ph, int quarter, int k, const Scales &sc, int buf) {
         const uint32_t past = 4 * (cw + ph) + g < KB && ph < cn ? 0u : ~0u;   // no block of this wave: zero weights
-        const uint8_t *B = lds + buf * BUF + l16 * 1024 * ES;
-        const uint8_t *A = lds + buf * BUF + XBUF + wave * NM * 2048 + 64 * l16 + 16 * (g ^ (l16 >> 2));
+        const uint8_t *B = lds + buf * BUF + l16 * 512 * ES;
+        const uint8_t *A = lds + buf * BUF + XBUF + wave * NM * 1024 + 64 * l16 + 16 * (g ^ (l16 >> 2));
         const int from = 16 * quarter + l16;      // the lane that holds the phase's scales
-        u4 a[NM][2];
-        uint32_t sw[NM][2], xsb[NT];
+        u4 a[NM];
+        uint32_t sw[NM], xsb[NT];
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t sv = ((uint32_t)__shfl((int)sc.w[m][r][k], from) >> (8 * g)) & 0xffu, keep = keep_mask(sv, past);
-                a[m][r] = and_u4(*reinterpret_cast<const u4 *>(A + (2 * m + r) * 1024), keep);
-                sw[m][r] = sv & keep;
-            }
+        for (int m = 0; m < NM; ++m) {
+            const uint32_t sv = ((uint32_t)__shfl((int)sc.w[m][k], from) >> (8 * g)) & 0xffu, keep = keep_mask(sv, past);
+            a[m] = and_u4(*reinterpret_cast<const u4 *>(A + m * 1024), keep);
+            sw[m] = sv & keep;
+        }
         if constexpr (TK != kTkBf16) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {   // (every lane takes part in the exchange)
@@ -519,8 +521,8 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < XF; ++i) {
-                const int slot = TK == kTkBf16 ? 16 * wave + 4 * g + i : TK == kTkExp ? 8 * wave + 2 * g + i : 8 * wave + 4 * i + g;
-                x[t][i] = *reinterpret_cast<const u4 *>(B + 16384 * ES * t + 16 * (slot ^ l16));
+                const int slot = TK == kTkBf16 ? 16 * cs + 4 * g + i : TK == kTkExp ? 8 * cs + 2 * g + i : 8 * cs + 4 * i + g;
+                x[t][i] = *reinterpret_cast<const u4 *>(B + 8192 * ES * t + 16 * (slot ^ l16));
             }
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (TK == kTkF8) {
@@ -529,10 +531,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
                 int sx = (int)xsb[t];
                 const v8i b = f8_operand(x[t][0], x[t][1], sx);
 #pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        acc[m][r][t] = mfma_fp4_fp8(a_operand(a[m][r]), b, acc[m][r][t], (int)sw[m][r], sx);
+                for (int m = 0; m < NM; ++m) acc[m][t] = mfma_fp4_fp8(a_operand(a[m]), b, acc[m][t], (int)sw[m], sx);
             }
         } else {
             float xf[NT];
@@ -546,20 +545,16 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
             }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                bf8 w[NM][2];
+                bf8 w[NM];
 #pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) w[m][r] = dequant8_bf16(a[m][r][s], scale_f32(sw[m][r]));
+                for (int m = 0; m < NM; ++m) w[m] = dequant8_bf16(a[m][s], scale_f32(sw[m]));
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     bf8 b;
                     if constexpr (TK == kTkExp) b = expand8_fp8(x[t][s >> 1][2 * (s & 1)], x[t][s >> 1][2 * (s & 1) + 1], xf[t]);
                     else b = as_bf8(x[t][s]);
 #pragma unroll
-                    for (int m = 0; m < NM; ++m)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) acc[m][r][t] = mfma_bf16(w[m][r], b, acc[m][r][t]);
+                    for (int m = 0; m < NM; ++m) acc[m][t] = mfma_bf16(w[m], b, acc[m][t]);
                 }
             }
         }
@@ -568,15 +563,15 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
     // Pipeline. A phase's tokens and weights are loaded D phases ahead; phase ph
     // waits until only the loads of the D - 1 phases behind it are in flight,
     // and for the block. A buffer is loaded again behind the barrier that
-    // follows the phase which read it. Phases past a wave's last load it again
-    // and are not multiplied.
-    constexpr int LPP = XL + 2 * NM;              // loads per phase
+    // follows the phase which read it. A wave's phases past
+    // its last chunk load that again and are not multiplied.
+    constexpr int LPP = XL + NM;                  // loads per phase
     Scales sc;
     sload(0, sc);
 #pragma unroll
     for (int k = 0; k < D; ++k) {
         wload(k, k);
-        xload(min(k, NP - 1), k);
+        xload(k, k);
     }
     int cur = 0, in = D;
     for (int ph = 0; ph < NP; ph += 4) {
@@ -586,7 +581,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
             if (ph + k < NP) {
                 tile_barrier<LPP *(D - 1)>();
                 wload(ph + k + D, in);
-                xload(min(ph + k + D, NP - 1), in);
+                xload(ph + k + D, in);
                 mul(ph + k, (ph >> 2) & 3, k, sc, cur);
                 cur = cur == NB - 1 ? 0 : cur + 1;
                 in = in == NB - 1 ? 0 : in + 1;
@@ -595,32 +590,14 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
     }
     tile_barrier<0>();   // the buffers become the sums' area
 
-    // the upper half of the waves hands its sums to the lower half: (w) + (w + 4), then in wave order
+    // the four chunk slots' sums are added in their order
     float4 *red = reinterpret_cast<float4 *>(lds);
-    auto put = [&](int w) {
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+    for (int m = 0; m < NM; ++m)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)   // [token][row]: lane l16 holds rows 4g + i of token l16
-                    red[(((w * NM + m) * 2 + r) * NT + t) * 64 + 4 * l16 + g] =
-                        float4{acc[m][r][t][0], acc[m][r][t][1], acc[m][r][t][2], acc[m][r][t][3]};
-    };
-    if (wave >= kStW / 2) put(wave - kStW / 2);
-    tile_barrier<0>();
-    if (wave < kStW / 2) {
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const float4 z = red[(((wave * NM + m) * 2 + r) * NT + t) * 64 + 4 * l16 + g];
-                    acc[m][r][t] += v4f{z.x, z.y, z.z, z.w};
-                }
-        put(wave);
-    }
+        for (int t = 0; t < NT; ++t)              // [token][row]: lane l16 holds rows 4g + i of token l16
+            red[((wave * NM + m) * NT + t) * 64 + 4 * l16 + g] =
+                float4{acc[m][t][0], acc[m][t][1], acc[m][t][2], acc[m][t][3]};
     tile_barrier<0>();
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
@@ -630,8 +607,8 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
         for (int m = 0; m < NM; ++m) {
             v[m] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kStW / 2; ++w)
-                v[m] += reinterpret_cast<const float *>(red + (((w * NM + m) * 2 + (row >> 4)) * NT + q) * 64)[16 * tok + (row & 15)];
+            for (int w = 0; w < kStC; ++w)
+                v[m] += reinterpret_cast<const float *>(red + (((w + kStC * (row >> 4)) * NM + m) * NT + q) * 64)[16 * tok + (row & 15)];
         }
         float y = v[0];
         if constexpr (NM == 2) y = act_fn(v[0], v[1], p.act, p.b1, p.b2);
@@ -757,15 +734,14 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     uint32_t wo[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) wo[i] = (uint32_t)min(lrow((tid >> 2) + 128 * i), p.N - 1 - n0) * (uint32_t)(p.K / 2);
-    __amdgpu_buffer_rsrc_t wsrc[NM];
-#pragma unroll
-    for (int m = 0; m < NM; ++m) wsrc[m] = buf_src(p.w[m] + (size_t)n0 * (p.K / 2));
+    // a step behind the last one is loaded from empty buffers: no traffic, and the counts of loads stay
+    auto bytes = [&](int k) { return k < NS ? -1 : 0; };
     const int wj = (tid & 3) ^ ((tid >> 4) & 3);  // slot j of row r lies at j ^ (r / 4 mod 4)
     auto wdirect = [&](int k, int buf) {
         const uint32_t kc = 16u * (uint32_t)min(4 * k + wj, KB - 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc[NM == 1 ? 0 : i],
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf_src(p.w[NM == 1 ? 0 : i] + (size_t)n0 * (p.K / 2), bytes(k)),
                                                      (lds_void *)(lds + buf * BUF + XB + (512 * i + 64 * wave) * 16), 16,
                                                      (int)(wo[i] + kc), 0, 0, 0);
     };
@@ -789,7 +765,6 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     const uint8_t *xb = static_cast<const uint8_t *>(p.x);
     const uint8_t *xr[EP], *xsr[EP];
     uint32_t xo[XP];
-    const __amdgpu_buffer_rsrc_t xsrc = buf_src(xb + (int64_t)t0 * p.xst * ES);
     if constexpr (TK == kTkExp) {
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
@@ -809,7 +784,8 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
         const uint32_t o = 16u * (uint32_t)min(SL * k + ((tid & (SL - 1)) ^ xsw), last);
 #pragma unroll
         for (int i = 0; i < XP; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xsrc, (lds_void *)(lds + buf * BUF + (512 * i + 64 * wave) * 16), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf_src(xb + (int64_t)t0 * p.xst * ES, bytes(k)),
+                                                     (lds_void *)(lds + buf * BUF + (512 * i + 64 * wave) * 16), 16,
                                                      (int)(xo[i] + o), 0, 0, 0);
     };
     u4 xe[EP];
@@ -894,17 +870,16 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     // through registers (stored to their buffer one step later), then the
     // direct ones. Step k waits until only the loads of the NB - 2 steps
     // behind it are in flight, and for the block; its buffer is then whole,
-    // and the buffer of step k - 1 is read and free for step k + NB - 1. Steps
-    // past the last load the last one's operands again, so that every step
-    // issues LPS loads.
+    // and the buffer of step k - 1 is read and free for step k + NB - 1. Every
+    // step issues LPS loads, also those behind the last.
     constexpr int LPS = 1 + (TK == kTkExp ? 2 * EP : XP) + 2;
     constexpr int D = NB - 1;
     auto issue = [&](int k, int buf) {
         const int kc = min(k, NS - 1);
         sload(kc);
         if constexpr (TK == kTkExp) eload(kc);
-        wdirect(kc, buf);
-        if constexpr (TK != kTkExp) xdirect(kc, buf);
+        wdirect(k, buf);
+        if constexpr (TK != kTkExp) xdirect(k, buf);
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
     auto settle = [&](int k, int buf) {
@@ -999,20 +974,25 @@ k3moe_status launch_stream(const DenseParams &p, hipStream_t s)
     return K3MOE_OK;
 }
 
-// Time models (us) that choose between the batch kernels, from what they
-// measured at 65 to 2048 tokens x 512 to 16384 rows x 2048 and 7168 columns: a
-// block per CU at a time, every round of them
-//   stream: the bytes of its phases' buffers at 45 KB/us and 2.5 us around them
-//   tiles:  1.75 us per step of 128 columns (1.2 on the scaled MFMA)
-// (2048 rows x 7168, 65 tokens: stream 16 us, tiles 100; 7168 x 7168, 300 tokens:
-// 119 and 101; 16384 x 2048, 300 tokens: 120 and 35.)
+// Time models (us) that choose between the batch kernels and the streaming
+// kernel's tokens per block, from what they measured at 8 to 2048 tokens x 512 to
+// 18432 rows x 2048 and 7168 columns:
+//   stream: a CU brings a phase's buffer at 60 KB/us for every block it gets;
+//           0.25 us per phase and 4 us around them for every round of the
+//           blocks that its LDS holds at once
+//   tiles:  1.75 us per step of 128 columns (1.2 on the scaled MFMA), a block
+//           per CU at a time
+// (2048 rows x 7168, 65 bf16 tokens: stream 15 us, tiles 100; 7168 x 7168, 300 of them:
+// 103 and 102; 16384 x 2048, 300: 81 and 35.)
 constexpr double kCus = 256.0;
 
 template <int NM, int TK, int NT>
 double stream_us(const DenseParams &p)
 {
-    const double blocks = ceil(p.N / 32.0) * ceil(p.T / (16.0 * NT)), phases = ceil(ceil(p.K / 128.0) / kStW);
-    return ceil(blocks / kCus) * (phases * (st_buf<NM, TK, NT>() / 1024) / 45.0 + 2.5);
+    const double blocks = ceil(p.N / 32.0) * ceil(p.T / (16.0 * NT)), phases = ceil(ceil(p.K / 128.0) / kStC);
+    constexpr int held = kMaxLds / st_lds<NM, TK, NT>() < 2 ? 1 : 2;   // blocks in a CU's LDS
+    return ceil(blocks / kCus) * phases * (st_buf<NM, TK, NT>() / 1024 / 60.0) +
+           ceil(blocks / (kCus * held)) * (phases * 0.25 + 4.0);
 }
 
 template <int NM, int TK>
@@ -1037,7 +1017,7 @@ template <int NM, int TK>
 k3moe_status launch_batch(const DenseParams &p, hipStream_t s)
 {
     // token tiles per block: as many as the LDS holds at most
-    constexpr int most = TK == kTkBf16 ? 3 - NM : 5 - NM;
+    constexpr int most = TK == kTkBf16 ? 5 - NM : 4;
     double us = stream_us<NM, TK, 1>(p);
     int nt = 1;
     each<2, most + 1>([&](auto k) {
@@ -1114,6 +1094,7 @@ k3moe_status check_dense(DenseParams &p, const uint8_t *const *w, const uint8_t 
     if (T == 1) x_stride = cols, xs_stride = KB, out_stride = rows, outs_stride = G;  // one row: no stride is used
     if (x_stride < cols || (xs && xs_stride < KB) || out_stride < rows || (outs && outs_stride < G))
         return K3MOE_E_INVALID_ARG;
+    if (T > 1 && x_stride > kMaxTokenStride) return K3MOE_E_UNSUPPORTED_SHAPE;
     for (int m = 0; m < nm; ++m)
         if (!at(w[m], 16) || !at(ws[m], 16)) return K3MOE_E_ALIGNMENT;
     if (!at(x, 16) || x_stride % (xs ? 16 : 8)) return K3MOE_E_ALIGNMENT;
