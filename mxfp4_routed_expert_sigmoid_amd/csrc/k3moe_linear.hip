@@ -339,7 +339,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 // A buffer resource over the 4 GiB behind p: the direct loads take 32-bit
 // offsets from it (and, unlike those of the global form, leave the waits for
 // loads into registers exact).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_src(const uint8_t *p, int bytes)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_src(const uint8_t *p, int bytes = -1)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, bytes, 0x00020000);
 }
@@ -429,15 +429,15 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
     // Weights, four lanes per row (a lane of the MFMA's order per row would cost the address unit a cycle per
     // lane): a load brings 16 bytes x 4 of the wave's 16 rows, slot j of row r at j ^ (r / 4 mod 4).
     const uint8_t *sr[NM];
+    __amdgpu_buffer_rsrc_t wsrc[NM];
     int64_t xleft[NT];
     const int64_t ns = min(n0 + 16 * rt + l16, p.N - 1), sleft = (p.N - ns) * KB;
     const uint32_t wo = (uint32_t)min(16 * rt + (lane >> 2), p.N - 1 - n0) * (uint32_t)(p.K / 2);
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
+        wsrc[m] = buf_src(p.w[m] + (size_t)n0 * (p.K / 2));
         sr[m] = p.ws[m] + ns * KB;
     }
-    // a phase behind the last one is loaded from empty buffers: no traffic, and the counts of loads stay
-    auto bytes = [&](int ph) { return ph < NP ? 0x7fffffff : 0; };
     const int wj = (lane & 3) ^ (lane >> 4);      // this lane's block of a chunk
     const uint8_t *xsr[NT];
     if constexpr (TK != kTkBf16) {
@@ -452,8 +452,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
         const int kc = min(4 * (cw + max(min(ph, cn - 1), 0)) + wj, KB - 1);   // (a wave may have no chunk)
 #pragma unroll
         for (int m = 0; m < NM; ++m)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf_src(p.w[m] + (size_t)n0 * (p.K / 2), bytes(ph)),
-                                                     (lds_void *)(lds + buf * BUF + XBUF + (uw * NM + m) * 1024), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc[m], (lds_void *)(lds + buf * BUF + XBUF + (uw * NM + m) * 1024), 16,
                                                      (int)(wo + 16u * (uint32_t)kc), 0, 0, 0);
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
@@ -477,7 +476,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
         for (int i = 0; i < XL; ++i) {
             const int q = kStW * i + uw, first = RL * q, up = RL == 1 ? 0 : lane >> 5, row = first + up;
             const __amdgpu_buffer_rsrc_t src =
-                buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)min(t0 + first, p.T - 1) * p.xst * ES, bytes(ph));
+                buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)min(t0 + first, p.T - 1) * p.xst * ES, 0x7fffffff);
             const uint32_t none = t0 + row < p.T ? 0u : 0x80000000u;   // rows past the last token: outside, read as zeros
             const int j = (lane & (SL - 1)) ^ (row & 15), w = j / (8 * ES);   // the slot this lane brings, its chunk's
             const int slot = min(8 * ES * (c0(w) + ph) + (j & (8 * ES - 1)), last);
@@ -571,7 +570,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 #pragma unroll
     for (int k = 0; k < D; ++k) {
         wload(k, k);
-        xload(k, k);
+        xload(min(k, NP - 1), k);
     }
     int cur = 0, in = D;
     for (int ph = 0; ph < NP; ph += 4) {
@@ -581,7 +580,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
             if (ph + k < NP) {
                 tile_barrier<LPP *(D - 1)>();
                 wload(ph + k + D, in);
-                xload(ph + k + D, in);
+                xload(min(ph + k + D, NP - 1), in);
                 mul(ph + k, (ph >> 2) & 3, k, sc, cur);
                 cur = cur == NB - 1 ? 0 : cur + 1;
                 in = in == NB - 1 ? 0 : in + 1;
@@ -734,14 +733,15 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     uint32_t wo[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) wo[i] = (uint32_t)min(lrow((tid >> 2) + 128 * i), p.N - 1 - n0) * (uint32_t)(p.K / 2);
-    // a step behind the last one is loaded from empty buffers: no traffic, and the counts of loads stay
-    auto bytes = [&](int k) { return k < NS ? -1 : 0; };
+    __amdgpu_buffer_rsrc_t wsrc[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) wsrc[m] = buf_src(p.w[m] + (size_t)n0 * (p.K / 2));
     const int wj = (tid & 3) ^ ((tid >> 4) & 3);  // slot j of row r lies at j ^ (r / 4 mod 4)
     auto wdirect = [&](int k, int buf) {
         const uint32_t kc = 16u * (uint32_t)min(4 * k + wj, KB - 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf_src(p.w[NM == 1 ? 0 : i] + (size_t)n0 * (p.K / 2), bytes(k)),
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc[NM == 1 ? 0 : i],
                                                      (lds_void *)(lds + buf * BUF + XB + (512 * i + 64 * wave) * 16), 16,
                                                      (int)(wo[i] + kc), 0, 0, 0);
     };
@@ -765,6 +765,7 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     const uint8_t *xb = static_cast<const uint8_t *>(p.x);
     const uint8_t *xr[EP], *xsr[EP];
     uint32_t xo[XP];
+    const __amdgpu_buffer_rsrc_t xsrc = buf_src(xb + (int64_t)t0 * p.xst * ES);
     if constexpr (TK == kTkExp) {
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
@@ -784,8 +785,7 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
         const uint32_t o = 16u * (uint32_t)min(SL * k + ((tid & (SL - 1)) ^ xsw), last);
 #pragma unroll
         for (int i = 0; i < XP; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf_src(xb + (int64_t)t0 * p.xst * ES, bytes(k)),
-                                                     (lds_void *)(lds + buf * BUF + (512 * i + 64 * wave) * 16), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xsrc, (lds_void *)(lds + buf * BUF + (512 * i + 64 * wave) * 16), 16,
                                                      (int)(xo[i] + o), 0, 0, 0);
     };
     u4 xe[EP];
@@ -870,16 +870,18 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     // through registers (stored to their buffer one step later), then the
     // direct ones. Step k waits until only the loads of the NB - 2 steps
     // behind it are in flight, and for the block; its buffer is then whole,
-    // and the buffer of step k - 1 is read and free for step k + NB - 1. Every
-    // step issues LPS loads, also those behind the last.
+    // and the buffer of step k - 1 is read and free for step k + NB - 1. Steps
+    // past the last load the last one's operands again, so that every step
+    // issues LPS loads (from empty buffers, whose descriptors are then made
+    // anew for each step, the kernel took 2 to 7 % longer).
     constexpr int LPS = 1 + (TK == kTkExp ? 2 * EP : XP) + 2;
     constexpr int D = NB - 1;
     auto issue = [&](int k, int buf) {
         const int kc = min(k, NS - 1);
         sload(kc);
         if constexpr (TK == kTkExp) eload(kc);
-        wdirect(k, buf);
-        if constexpr (TK != kTkExp) xdirect(k, buf);
+        wdirect(kc, buf);
+        if constexpr (TK != kTkExp) xdirect(kc, buf);
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
     auto settle = [&](int k, int buf) {
