@@ -425,7 +425,7 @@ typedef enum {
  * format of k3moe_mxfp4). rows >= 1; cols a multiple of 32, at
  * most 2^22 (K3MOE_E_UNSUPPORTED_SHAPE otherwise).
  *   x   bf16 [T][cols], or e4m3 [T][cols] with xs E8M0 [T][cols/32] (xs NULL =
- *       bf16); 16-byte aligned rows, strides up to 2^30 elements
+ *       bf16); 16-byte aligned rows, strides up to 2^24 elements
  *       (K3MOE_E_UNSUPPORTED_SHAPE above)
  *   out, outs  as out_kind (k3moe_out) says; outs NULL unless K3MOE_OUT_MXFP8
  * Products of finite tokens (a value beyond bf16's range is infinite) are

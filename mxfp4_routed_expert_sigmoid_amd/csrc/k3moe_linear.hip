@@ -31,8 +31,10 @@ namespace {
 // Widest matrix: a block's rows are addressed by 32-bit offsets (256 rows x
 // 2^22 / 2 bytes).
 constexpr int kMaxCols = 1 << 22;
-// Largest stride of token rows: two neighbouring rows are addressed by 32-bit offsets.
-constexpr int64_t kMaxTokenStride = 1 << 30;
+// Largest stride of token rows: a block's 128 rows are addressed by 32-bit
+// offsets, 64 rows by 31-bit ones (bit 31 marks a row that is not there):
+// 127 * 2^25 + 2^23 < 2^32, 63 * 2^25 + 2^23 < 2^31 bytes.
+constexpr int64_t kMaxTokenStride = 1 << 24;
 
 struct DenseParams {
     const uint8_t *w[2], *ws[2];   // packed rows [N][K / 2], scale rows [N][K / 32] (one or two matrices)
@@ -471,18 +473,21 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
     // direct loads: 64 slots per wave and load, one row of bf16 tokens or two of 8-bit ones, of all four chunks
     constexpr int RL = 2 / ES, SL = 64 / RL;      // rows per load, slots per row
     const int last = p.K * ES / 16 - 1;           // last slot of a token row
+    const __amdgpu_buffer_rsrc_t xsrc = buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)t0 * p.xst * ES, 0x7fffffff);
+    uint32_t xo[XL];                              // row offsets; rows past the last token lie outside, read as zeros
+    int xs0[ES];                                  // this lane's slot of phase 0 (rows 8 apart take turns in bf16)
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+        const int row = RL * (kStW * i + uw) + (RL == 1 ? 0 : lane >> 5);
+        xo[i] = t0 + row < p.T ? (uint32_t)row * (uint32_t)(p.xst * ES) : 0x80000000u;
+        const int j = (lane & (SL - 1)) ^ (row & 15), w = j / (8 * ES);   // its slot of the phase, its chunk's
+        if (i < ES) xs0[i] = 8 * ES * c0(w) + (j & (8 * ES - 1));
+    }
     auto xload = [&](int ph, int buf) {
 #pragma unroll
-        for (int i = 0; i < XL; ++i) {
-            const int q = kStW * i + uw, first = RL * q, up = RL == 1 ? 0 : lane >> 5, row = first + up;
-            const __amdgpu_buffer_rsrc_t src =
-                buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)min(t0 + first, p.T - 1) * p.xst * ES, 0x7fffffff);
-            const uint32_t none = t0 + row < p.T ? 0u : 0x80000000u;   // rows past the last token: outside, read as zeros
-            const int j = (lane & (SL - 1)) ^ (row & 15), w = j / (8 * ES);   // the slot this lane brings, its chunk's
-            const int slot = min(8 * ES * (c0(w) + ph) + (j & (8 * ES - 1)), last);
-            const uint32_t o = 16u * (uint32_t)slot + (up ? (uint32_t)p.xst : 0u);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void *)(lds + buf * BUF + 1024 * q), 16, (int)(o | none), 0, 0, 0);
-        }
+        for (int i = 0; i < XL; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xsrc, (lds_void *)(lds + buf * BUF + 1024 * (kStW * i + uw)), 16,
+                                                     (int)(xo[i] + 16u * (uint32_t)min(xs0[i % ES] + 8 * ES * ph, last)), 0, 0, 0);
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
     v4f acc[NM][NT];
@@ -1027,10 +1032,7 @@ k3moe_status launch_batch(const DenseParams &p, hipStream_t s)
         const double u = stream_us<NM, TK, NT>(p);
         if (u < us) us = u, nt = NT;
     });
-    constexpr int64_t es = st_es<TK>();
-    constexpr int64_t far = (int64_t)1 << 32;
-    const bool tile_ok = p.K >= 128 && p.xst < far && (kTlTok - 1) * p.xst * es + p.K * es < far;   // 32-bit offsets
-    if (tile_ok && tile_us<NM, TK>(p) < us) {
+    if (p.K >= 128 && tile_us<NM, TK>(p) < us) {
         const int64_t rb = ((int64_t)p.N * NM + kTlRows - 1) / kTlRows, tb = ((int64_t)p.T + kTlTok - 1) / kTlTok;
         if (rb * tb > kMaxItems / (64 * kTlWaves)) return K3MOE_E_UNSUPPORTED_SHAPE;
         launch_tile<NM, TK>(p, rb * tb, (int)tb, s);

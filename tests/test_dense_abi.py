@@ -59,7 +59,7 @@ DENSE = [
     (dict(xs=A, xsst=1), INVALID), (dict(kind=k3.OUT_MXFP8, outs=A, osst=0), INVALID),
     (dict(p=A + 8), ALIGN), (dict(s=A + 4), ALIGN), (dict(x=A + 8), ALIGN), (dict(xst=68), ALIGN),
     (dict(xs=A, xsst=2, xst=72), ALIGN), (dict(out=A + 1), ALIGN), (dict(out=A + 2, kind=k3.OUT_F32), ALIGN),
-    (dict(xst=2 ** 30 + 16), SHAPE), (dict(xs=A, xsst=2, xst=2 ** 30 + 16), SHAPE),
+    (dict(xst=2 ** 24 + 16), SHAPE), (dict(xs=A, xsst=2, xst=2 ** 24 + 16), SHAPE),
     (dict(T=0, x=None, out=None), OK),
 ]
 
