@@ -130,8 +130,8 @@ __device__ __forceinline__ void dense_store(const DenseParams &p, int64_t t, int
 // took 173 registers and half the waves (2 x 18432 x 7168 to MXFP8: 51 us, 37 so).
 //
 // One token, in a graph: 1536 x 7168 5.2 us (a launch and one unit's latency),
-// 7168 x 18432 16.3 us (4.3 TB/s), 2 x 18432 x 7168 34 us (4.1 TB/s); four tokens
-// of 163840 x 7168 127 us (4.9 TB/s). A plain read of such sizes reaches 4 to 6.
+// 7168 x 18432 17 us (4.1 TB/s), 2 x 18432 x 7168 34 us (4.1 TB/s); four tokens
+// of 163840 x 7168 127 to 132 us (4.9 TB/s). A plain read of such sizes reaches 4 to 6.
 constexpr int kGvTok = 4, kGvMaxWaves = 8;
 constexpr int kGvMaxLds = 65536;   // token bytes of a block
 constexpr int kGvPieces = 8;       // token pieces a lane has in flight (one at a time: 7168 x 28672 31.0 us, 29.2 so)
@@ -382,13 +382,13 @@ __device__ __forceinline__ v8i f8_operand(u4 lo, u4 hi, int &s)
 // order, a load costs the address unit about a cycle per lane (48 MXFP8 tokens
 // x 7168 x 7168: 26 us so).
 //
-// Measured on 7168 rows x 7168, in a graph: 8 MXFP8 tokens 9.7 us, 16 bf16
-// tokens 11.0, 48 MXFP8 tokens 14.6 (340 TFLOP/s), 48 bf16 tokens 19.5. Bound by what
+// Measured on 7168 rows x 7168, in a graph: 8 MXFP8 tokens 9.5 us, 8 bf16
+// tokens 10.9, 48 MXFP8 tokens 14.2 to 14.8 (340 TFLOP/s), 48 bf16 tokens 19.5. Bound by what
 // a CU's direct loads bring, 50 to 60 KB/us whatever their order or depth: every
 // block reads its tokens anew, which only more rows per block would change, and
 // those would leave CUs idle. Phases of eight chunks, one per wave and both row
 // tiles: 16.5 us for the 48 MXFP8 tokens, and 64 bf16 tokens do not fit (301 tokens
-// x 1001 x 2080: 16.0 us, 9.8 so).
+// x 1001 x 2080: 16.0 us, 9.2 so).
 //
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15).
 constexpr int kStW = 8, kStC = 4;                 // waves, chunks of a phase
@@ -632,9 +632,9 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 // side because a token's bytes are four times a weight row's: LDS reads take
 // half the cycles of the MFMAs.
 //
-// 2048 tokens x 7168 x 18432: bf16 510 us (1.06 PFLOP/s; the library's bf16
-// product of that size 522), MXFP8 to bf16 347 us (1.56), MXFP8 to fp32 570 us
-// (0.95: the expansion of the tokens). Of the 510, 349 are left without loads
+// 2048 tokens x 7168 x 18432: bf16 to bf16 514 us (1.05 PFLOP/s; the library's
+// bf16 product of that size 522), MXFP8 to bf16 347 us (1.56), MXFP8 to fp32 550 us
+// (0.98: the expansion of the tokens), += 569. Of the 514, 349 are left without loads
 // and LDS reads, the MFMAs with the expansion of the weights, and 388 with the
 // reads; 448 tiles on 256 CUs are two rounds of which the second is 3/4 full.
 //
