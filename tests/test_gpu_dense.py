@@ -284,6 +284,23 @@ def test_linear_streamed(T, K, x8):
         _linear(T, 45, K, x8, out)
 
 
+# 130 row blocks: two to four 16-token tiles per block, one phase to a second run of scales, a last block of 9 rows
+@pytest.mark.parametrize("T", [32, 47, 61])
+@pytest.mark.parametrize("K", [96, 1184, 8736])
+@pytest.mark.parametrize("x8", [False, True])
+def test_linear_streamed_in_wide_token_blocks(T, K, x8):
+    for out in ("f32", "bf16"):
+        _linear(T, 4137, K, x8, out, pad=3, xpad=16)
+
+
+@pytest.mark.parametrize("T", [32, 47, 61])
+@pytest.mark.parametrize("K", [96, 1184])
+@pytest.mark.parametrize("x8", [False, True])
+def test_glu_streamed_in_wide_token_blocks(T, K, x8):
+    for out in ("mxfp8", "bf16"):
+        _glu_scaled(T, 4137, K, x8, out, 1)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 100, 7168), (5, 130, 2080), (48, 257, 1536), (300, 160, 1056), (2048, 256, 512)])
 @pytest.mark.parametrize("x8", [False, True])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
