@@ -130,11 +130,10 @@ __device__ __forceinline__ void dense_store(const DenseParams &p, int64_t t, int
 // took 173 registers and half the waves (2 x 18432 x 7168 to MXFP8: 51 us, 37 so).
 //
 // One token, in a graph: 1536 x 7168 5.2 us (a launch and one unit's latency),
-// 7168 x 18432 17 us (4.1 TB/s), 2 x 18432 x 7168 34 us (4.1 TB/s); four tokens
+// 7168 x 18432 16.3 us (4.3 TB/s), 2 x 18432 x 7168 34 us (4.1 TB/s); four tokens
 // of 163840 x 7168 127 to 132 us (4.9 TB/s). A plain read of such sizes reaches 4 to 6.
 constexpr int kGvTok = 4, kGvMaxWaves = 8;
 constexpr int kGvMaxLds = 65536;   // token bytes of a block
-constexpr int kGvPieces = 8;       // token pieces a lane has in flight (one at a time: 7168 x 28672 31.0 us, 29.2 so)
 // A matrix of fewer tiles has a block for each, which the card schedules as
 // they end (18432 rows x 2 matrices x 7168: 33 us, 39 us with two or three
 // tiles per block); a longer one two blocks per CU, each with many tiles,
@@ -279,31 +278,20 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
     load(ua);
     clear();
     {
-        // the wave's columns of every token, as bf16: pieces of 16 bytes, kGvPieces per lane in flight
-        const int c0 = 128 * U * u0, per = (min(128 * U * u1, p.K) - c0) / (X8 ? 16 : 8), n = p.T * per;   // pieces of a token, of all
-        for (int i0 = lane; i0 < n; i0 += 64 * kGvPieces) {
-            u4 x[kGvPieces];
-            uint32_t sx[X8 ? kGvPieces : 1];
-            int at[kGvPieces];                                 // LDS offsets
-#pragma unroll
-            for (int j = 0; j < kGvPieces; ++j) {
-                const int i = min(i0 + 64 * j, n - 1), t = i / per, c = c0 + (X8 ? 16 : 8) * (i - t * per);
-                at[j] = t * xrow + 2 * c;
-                x[j] = *reinterpret_cast<const u4 *>(static_cast<const uint8_t *>(p.x) + (t * p.xst + c) * (X8 ? 1 : 2));
-                if constexpr (X8) sx[j] = p.xs[t * p.xsst + c / 32];
-            }
-#pragma unroll
-            for (int j = 0; j < kGvPieces; ++j) {
-                if (i0 + 64 * j >= n) break;
-                if constexpr (X8) {
-                    const uint32_t keep = keep_mask(sx[j], 0u);
-                    const u4 v = and_u4(x[j], keep);
-                    const float f = scale_f32(sx[j] & keep);
-                    bf8 *d = reinterpret_cast<bf8 *>(xl + at[j]);
-                    d[0] = expand8_fp8(v.x, v.y, f), d[1] = expand8_fp8(v.z, v.w, f);
-                } else {
-                    *reinterpret_cast<u4 *>(xl + at[j]) = x[j];
-                }
+        // the wave's columns of every token, as bf16, 16 bytes at a time (eight in flight per lane took 1 to 2 % longer)
+        const int c0 = 128 * U * u0, per = (min(128 * U * u1, p.K) - c0) / (X8 ? 16 : 8);   // 16-byte pieces of a token
+        for (int i = lane; i < p.T * per; i += 64) {
+            const int t = i / per, c = c0 + (X8 ? 16 : 8) * (i - t * per);
+            const u4 x = *reinterpret_cast<const u4 *>(static_cast<const uint8_t *>(p.x) + (t * p.xst + c) * (X8 ? 1 : 2));
+            uint8_t *at = xl + t * xrow + 2 * c;
+            if constexpr (X8) {
+                const uint32_t sx = p.xs[t * p.xsst + c / 32], keep = keep_mask(sx, 0u);
+                const u4 v = and_u4(x, keep);
+                const float f = scale_f32(sx & keep);
+                bf8 *d = reinterpret_cast<bf8 *>(at);
+                d[0] = expand8_fp8(v.x, v.y, f), d[1] = expand8_fp8(v.z, v.w, f);
+            } else {
+                *reinterpret_cast<u4 *>(at) = x;
             }
         }
         wave_lds_sync();
