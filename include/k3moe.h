@@ -429,9 +429,8 @@ typedef enum {
  *       (K3MOE_E_UNSUPPORTED_SHAPE above)
  *   out, outs  as out_kind (k3moe_out) says; outs NULL unless K3MOE_OUT_MXFP8
  * Products of finite tokens (a value beyond bf16's range is infinite) are
- * exact and summed in fp32; from MXFP8 tokens to K3MOE_OUT_BF16 the sums of
- * more than four tokens may keep only about 14 bits below the largest of each
- * 16 products (the block-scaled MFMA), which the rounding to bf16 hides. */
+ * exact and summed in fp32, whatever the number of tokens and the kind of the
+ * result; only a K3MOE_OUT_BF16 or K3MOE_OUT_MXFP8 result is then rounded. */
 k3moe_status k3moe_linear(const uint8_t *packed, const uint8_t *scales, int32_t rows, int32_t cols,
                           const void *x, int64_t x_stride, const uint8_t *xs, int64_t xs_stride,
                           int32_t T, void *out, int64_t out_stride, uint8_t *outs,

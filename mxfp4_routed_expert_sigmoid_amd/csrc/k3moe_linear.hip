@@ -8,13 +8,15 @@
 // Weights and 8-bit tokens are expanded to bf16 in registers, which is exact
 // (an fp4 or e4m3 value times a power of two is a bf16; one past bf16's range is
 // infinite), and multiplied on v_mfma_f32_16x16x32_bf16: exact products, fp32
-// sums. More than four MXFP8 tokens whose results are rounded to bf16 go as
-// they are to the block-scaled MFMA, 16x16x128 at twice the rate.
+// sums. (The block-scaled MFMA would take 8-bit tokens as they are at twice the rate,
+// but sums each run of 16 products to about 14 bits below the largest, which shows in a
+// result where large products cancel: it is not used, whatever the result's type.)
 //
 // Three kernels by the number of tokens, each reading every weight once per
 // block of tokens that it holds:
-//   k_mx_gemv    1 to 4: a stream of weights, bound by memory
-//   k_mx_stream  more, where tiles would not fill the card: bound by what one
+//   k_mx_gemv    1 to 4 of at most 64 KiB together as bf16: a stream of weights,
+//                bound by memory
+//   k_mx_stream  more or longer ones, where tiles would not fill the card: bound by what one
 //                CU's direct loads bring
 //   k_mx_tile    batches: bound by the MFMAs and the expansion beside them
 //
@@ -318,11 +320,6 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
 }
 
 // ---------------------------------------------------------------------------
-// Token kinds of the batch kernels. kTkBf16: bf16 tokens. kTkExp: MXFP8 tokens
-// expanded to bf16. kTkF8: MXFP8 tokens as they are on the block-scaled MFMA
-// v_mfma_scale_f32_16x16x128_f8f6f4.
-constexpr int kTkBf16 = 0, kTkExp = 1, kTkF8 = 2;
-
 typedef __attribute__((address_space(3))) void lds_void;
 
 #ifdef __HIP_DEVICE_COMPILE__
@@ -345,21 +342,6 @@ __device__ __forceinline__ void tile_barrier()
     asm volatile("" ::: "memory");
 }
 
-// The scaled MFMA's fp8 operand of 16 tokens (lane group g: columns
-// [16g, 16g + 16) in lo, [64 + 16g, 80 + 16g) in hi of 128) with its scale byte
-// s (block g). A dropped group's values lie in lanes of two groups: found on the
-// wave's ballot, which is almost always empty.
-__device__ __forceinline__ v8i f8_operand(u4 lo, u4 hi, int &s)
-{
-    if (__any(s == 255)) {
-        const int l16 = threadIdx.x & 15, h = (threadIdx.x & 63) >> 5;   // blocks h and 2 + h are held here
-        if (__shfl(s, 16 * h + l16) == 255) lo = u4{0u, 0u, 0u, 0u};
-        if (__shfl(s, 32 + 16 * h + l16) == 255) hi = u4{0u, 0u, 0u, 0u};
-        if (s == 255) s = 127;
-    }
-    return b_operand(lo, hi);
-}
-
 // ---------------------------------------------------------------------------
 // More tokens on a card that tiles would not fill. A block owns 32 rows of
 // each matrix and 16 NT tokens; each of its eight waves takes one of the two
@@ -367,41 +349,39 @@ __device__ __forceinline__ v8i f8_operand(u4 lo, u4 hi, int &s)
 // phase) at a time, and the four parts' sums are added at the end in their
 // order. The tokens of a phase go into LDS by direct loads of whole rows, and
 // so do each wave's weights, four lanes to a row: read from memory in operand
-// order, a load costs the address unit about a cycle per lane (48 MXFP8 tokens
-// x 7168 x 7168: 26 us so).
+// order, a load costs the address unit about a cycle per lane.
 //
-// Measured on 7168 rows x 7168, in a graph: 8 MXFP8 tokens 9.5 us, 8 bf16
-// tokens 10.9, 48 MXFP8 tokens 14.2 to 14.8 (340 TFLOP/s), 48 bf16 tokens 19.5. Bound by what
-// a CU's direct loads bring, 50 to 60 KB/us whatever their order or depth: every
-// block reads its tokens anew, which only more rows per block would change, and
-// those would leave CUs idle. Phases of eight chunks, one per wave and both row
-// tiles: 16.5 us for the 48 MXFP8 tokens, and 64 bf16 tokens do not fit (301 tokens
-// x 1001 x 2080: 16.0 us, 9.2 so).
+// Measured on 7168 rows x 7168, in a graph: 8 MXFP8 tokens 10.4 us, 8 bf16
+// tokens 10.6, 48 MXFP8 tokens 18.7 (264 TFLOP/s), 48 bf16 tokens 18.6. Every
+// block reads its tokens anew (and expands those in 8 bits), which only more rows
+// per block would change, and those would leave CUs idle. Phases of eight chunks,
+// one per wave and both row tiles, do not hold 64 bf16 tokens (301 tokens x 1001 x
+// 2080: 16.0 us, 9.1 so).
 //
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15).
 constexpr int kStW = 8, kStC = 4;                 // waves, chunks of a phase
 constexpr int kStMaxBuf = 3;                      // (8 MXFP8 tokens x 7168 x 7168: 9.7 us, 10.0 with four buffers, 10.4 with six)
-template <int TK> __host__ __device__ constexpr int st_es() { return TK == kTkBf16 ? 2 : 1; }  // bytes per token element
+template <bool X8> __host__ __device__ constexpr int st_es() { return X8 ? 1 : 2; }  // bytes per token element
 constexpr int kMaxLds = 163840;
-template <int NM, int TK, int NT> __host__ __device__ constexpr int st_x() { return 16 * NT * 128 * kStC * st_es<TK>(); }   // tokens of a phase
-template <int NM, int TK, int NT> __host__ __device__ constexpr int st_buf() { return st_x<NM, TK, NT>() + kStW * NM * 1024; }
-template <int NM, int TK, int NT> __host__ __device__ constexpr int st_nbuf()
+template <int NM, bool X8, int NT> __host__ __device__ constexpr int st_x() { return 16 * NT * 128 * kStC * st_es<X8>(); }   // tokens of a phase
+template <int NM, bool X8, int NT> __host__ __device__ constexpr int st_buf() { return st_x<NM, X8, NT>() + kStW * NM * 1024; }
+template <int NM, bool X8, int NT> __host__ __device__ constexpr int st_nbuf()
 {
-    constexpr int n = kMaxLds / st_buf<NM, TK, NT>();
+    constexpr int n = kMaxLds / st_buf<NM, X8, NT>();
     return n > kStMaxBuf ? kStMaxBuf : n;
 }
-template <int NM, int TK, int NT> __host__ __device__ constexpr int st_lds()
+template <int NM, bool X8, int NT> __host__ __device__ constexpr int st_lds()
 {
-    constexpr int x = st_nbuf<NM, TK, NT>() * st_buf<NM, TK, NT>(), red = kStW * NM * NT * 1024;
-    static_assert(x <= kMaxLds && red <= kMaxLds && st_nbuf<NM, TK, NT>() >= 2, "a block's LDS");
+    constexpr int x = st_nbuf<NM, X8, NT>() * st_buf<NM, X8, NT>(), red = kStW * NM * NT * 1024;
+    static_assert(x <= kMaxLds && red <= kMaxLds && st_nbuf<NM, X8, NT>() >= 2, "a block's LDS");
     return x > red ? x : red;
 }
 
-template <int NM, int TK, int NT>
+template <int NM, bool X8, int NT>
 __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_blocks)
 {
 #ifdef __HIP_DEVICE_COMPILE__   // the buffer resource type exists on the device side only
-    constexpr int ES = st_es<TK>(), XBUF = st_x<NM, TK, NT>(), BUF = st_buf<NM, TK, NT>(), NB = st_nbuf<NM, TK, NT>(), D = NB - 1;
+    constexpr int ES = st_es<X8>(), XBUF = st_x<NM, X8, NT>(), BUF = st_buf<NM, X8, NT>(), NB = st_nbuf<NM, X8, NT>(), D = NB - 1;
     constexpr int XL = NT * ES;                   // direct loads per wave and phase
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
@@ -430,7 +410,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
     }
     const int wj = (lane & 3) ^ (lane >> 4);      // this lane's block of a chunk
     const uint8_t *xsr[NT];
-    if constexpr (TK != kTkBf16) {
+    if constexpr (X8) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int64_t tt = min(t0 + 16 * t + l16, p.T - 1);
@@ -447,13 +427,13 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
     struct Scales {                               // of 16 phases
-        u4 w[NM], x[TK == kTkBf16 ? 1 : NT];
+        u4 w[NM], x[X8 ? NT : 1];
     };
     auto sload = [&](int seg, Scales &q) {
         const int o = 4 * min(cw + 16 * seg, (KB - 1) / 4);
 #pragma unroll
         for (int m = 0; m < NM; ++m) q.w[m] = run_load(sr[m] + o, sleft - o, (int64_t)p.N * KB, g);
-        if constexpr (TK != kTkBf16) {
+        if constexpr (X8) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) q.x[t] = run_load(xsr[t] + o, xleft[t] - o, (p.T - 1) * p.xsst + KB, g);
         }
@@ -498,7 +478,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
             a[m] = and_u4(*reinterpret_cast<const u4 *>(A + m * 1024), keep);
             sw[m] = sv & keep;
         }
-        if constexpr (TK != kTkBf16) {
+        if constexpr (X8) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {   // (every lane takes part in the exchange)
                 const uint32_t sx = ((uint32_t)__shfl((int)sc.x[t][k], from) >> (8 * g)) & 0xffu;
@@ -507,47 +487,37 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
         }
         // every fragment of the chunk is read before the first product (the compiler would read each where it
         // is used, a wait of the LDS's latency every few MFMAs)
-        constexpr int XF = TK == kTkBf16 ? 4 : 2;
+        constexpr int XF = X8 ? 2 : 4;
         u4 x[NT][XF];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < XF; ++i) {
-                const int slot = TK == kTkBf16 ? 16 * cs + 4 * g + i : TK == kTkExp ? 8 * cs + 2 * g + i : 8 * cs + 4 * i + g;
+                const int slot = 8 * ES * cs + 2 * ES * g + i;
                 x[t][i] = *reinterpret_cast<const u4 *>(B + 8192 * ES * t + 16 * (slot ^ l16));
             }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (TK == kTkF8) {
+        float xf[NT];
+        if constexpr (X8) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                int sx = (int)xsb[t];
-                const v8i b = f8_operand(x[t][0], x[t][1], sx);
-#pragma unroll
-                for (int m = 0; m < NM; ++m) acc[m][t] = mfma_fp4_fp8(a_operand(a[m]), b, acc[m][t], (int)sw[m], sx);
+                const uint32_t keep = keep_mask(xsb[t], 0u);
+                x[t][0] = and_u4(x[t][0], keep), x[t][1] = and_u4(x[t][1], keep);
+                xf[t] = scale_f32(xsb[t] & keep);
             }
-        } else {
-            float xf[NT];
-            if constexpr (TK == kTkExp) {
+        }
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint32_t keep = keep_mask(xsb[t], 0u);
-                    x[t][0] = and_u4(x[t][0], keep), x[t][1] = and_u4(x[t][1], keep);
-                    xf[t] = scale_f32(xsb[t] & keep);
-                }
-            }
+        for (int s = 0; s < 4; ++s) {
+            bf8 w[NM];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                bf8 w[NM];
+            for (int m = 0; m < NM; ++m) w[m] = dequant8_bf16(a[m][s], scale_f32(sw[m]));
 #pragma unroll
-                for (int m = 0; m < NM; ++m) w[m] = dequant8_bf16(a[m][s], scale_f32(sw[m]));
+            for (int t = 0; t < NT; ++t) {
+                bf8 b;
+                if constexpr (X8) b = expand8_fp8(x[t][s >> 1][2 * (s & 1)], x[t][s >> 1][2 * (s & 1) + 1], xf[t]);
+                else b = as_bf8(x[t][s]);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    bf8 b;
-                    if constexpr (TK == kTkExp) b = expand8_fp8(x[t][s >> 1][2 * (s & 1)], x[t][s >> 1][2 * (s & 1) + 1], xf[t]);
-                    else b = as_bf8(x[t][s]);
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) acc[m][t] = mfma_bf16(w[m], b, acc[m][t]);
-                }
+                for (int m = 0; m < NM; ++m) acc[m][t] = mfma_bf16(w[m], b, acc[m][t]);
             }
         }
     };
@@ -621,8 +591,8 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 // half the cycles of the MFMAs.
 //
 // 2048 tokens x 7168 x 18432: bf16 to bf16 514 us (1.05 PFLOP/s; the library's
-// bf16 product of that size 522), MXFP8 to bf16 347 us (1.56), MXFP8 to fp32 550 us
-// (0.98: the expansion of the tokens), += 569. Of the 514, 349 are left without loads
+// bf16 product of that size 522), MXFP8 to bf16 or fp32 549 us (0.99: the expansion of
+// the tokens), += 569. Of the 514, 349 are left without loads
 // and LDS reads, the MFMAs with the expansion of the weights, and 388 with the
 // reads; 448 tiles on 256 CUs are two rounds of which the second is 3/4 full.
 //
@@ -678,13 +648,11 @@ __device__ __forceinline__ void dense_store4(const DenseParams &p, int64_t t, in
     }
 }
 
-// A step is 128 columns: 64 bytes of every weight row, 256 (bf16) or 128 (kTkF8)
-// of every token, one dword of every scale row. The buffers of a block:
-template <int TK> __host__ __device__ constexpr int tl_xrow() { return TK == kTkF8 ? 128 : 256; }
-template <int TK> __host__ __device__ constexpr int tl_nbuf() { return TK == kTkF8 ? 4 : 3; }
+// A step is 128 columns: 64 bytes of every weight row, 256 (as bf16) of every
+// token, one dword of every scale row. The buffers of a block:
+constexpr int kTlBufs = 3, kTlXRow = 256;
 constexpr int kTlWBuf = kTlRows * 64, kTlSRows = 64 * kTlWaves;  // one scale dword per thread
-template <int TK> __host__ __device__ constexpr int tl_buf() { return kTlTok * tl_xrow<TK>() + kTlWBuf + 4 * kTlSRows; }
-template <int TK> __host__ __device__ constexpr int tl_lds() { return tl_nbuf<TK>() * tl_buf<TK>(); }
+constexpr int kTlBuf = kTlTok * kTlXRow + kTlWBuf + 4 * kTlSRows, kTlLds = kTlBufs * kTlBuf;
 
 // LDS stores of the tile pipeline. As plain stores the compiler would first
 // wait for every direct load in flight, which may write the same LDS for all
@@ -701,11 +669,11 @@ __device__ __forceinline__ void lds_put16(const uint8_t *at, bf8 v)
                  : "memory");
 }
 
-template <int NM, int TK>
+template <int NM, bool X8>
 __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int tok_tiles)
 {
 #ifdef __HIP_DEVICE_COMPILE__   // the buffer resource type exists on the device side only
-    constexpr int NB = tl_nbuf<TK>(), BUF = tl_buf<TK>(), XR = tl_xrow<TK>();
+    constexpr int NB = kTlBufs, BUF = kTlBuf, XR = kTlXRow;
     constexpr int XB = kTlTok * XR;               // a buffer: tokens, weights, scales
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
@@ -738,11 +706,10 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
                                                      (lds_void *)(lds + buf * BUF + XB + (512 * i + 64 * wave) * 16), 16,
                                                      (int)(wo[i] + kc), 0, 0, 0);
     };
-    // Scales: thread i < 256 holds the dword (four blocks) of LDS weight row i, thread 256 + t (kTkF8, t < 128)
-    // that of token t, in a register for a step before it goes to its buffer; blocks past the row's last read
-    // as 255. K >= 128: the last dword of a row is loaded and shifted.
+    // Scales: thread i < 256 holds the dword (four blocks) of LDS weight row i in a register for a step before it
+    // goes to its buffer (the other threads a copy: every wave issues the same loads); blocks past the row's last
+    // read as 255. K >= 128: the last dword of a row is loaded and shifted.
     const uint8_t *sp = p.ws[NM == 1 ? 0 : (tid & 255) >> 7] + (size_t)min(n0 + lrow(tid & 255), p.N - 1) * KB;
-    if (TK == kTkF8 && tid >= 256) sp = p.xs + (int64_t)min(t0 + (tid & 127), p.T - 1) * p.xsst;
     uint32_t sreg = 0;
     auto sload = [&](int k) { __builtin_memcpy(&sreg, sp + min(4 * k, KB - 4), 4); };
     auto sstore = [&](int k, int buf) {
@@ -750,16 +717,16 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
         lds_put(lds + buf * BUF + XB + kTlWBuf + 4 * tid, (sreg >> sh) | ~(~0u >> sh));
     };
 
-    // Token staging. Direct (kTkBf16, kTkF8): slots of 16 bytes, XP per thread. kTkExp: two slots of 16 values
-    // per thread, held in registers for a step and expanded on their way into LDS.
-    constexpr int ES = TK == kTkBf16 ? 2 : 1;     // bytes per token element in memory
+    // Token staging. bf16: direct, slots of 16 bytes, XP per thread. MXFP8: two slots of 16 values per thread, held
+    // in registers for a step and expanded on their way into LDS.
+    constexpr int ES = X8 ? 1 : 2;                // bytes per token element in memory
     constexpr int SL = XR / 16, XP = XB / 8192;   // slots per row, passes
     constexpr int EP = 2;
     const uint8_t *xb = static_cast<const uint8_t *>(p.x);
     const uint8_t *xr[EP], *xsr[EP];
     uint32_t xo[XP];
     const __amdgpu_buffer_rsrc_t xsrc = buf_src(xb + (int64_t)t0 * p.xst * ES);
-    if constexpr (TK == kTkExp) {
+    if constexpr (X8) {
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
             const int64_t t = min(t0 + (tid >> 3) + 64 * i, p.T - 1);
@@ -833,28 +800,17 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
             a[r] = and_u4(a[r], keep);
             s4[r] = sv & keep;
         }
-        if constexpr (TK == kTkF8) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                int sx = (int)((*reinterpret_cast<const uint32_t *>(S + 4 * (kTlRows + 64 * wt + 16 * t + l16)) >> (8 * g)) & 0xffu);
-                const v8i b = f8_operand(*reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * (g ^ (l16 >> 1))),
-                                         *reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * ((4 + g) ^ (l16 >> 1))), sx);
+        for (int s = 0; s < 4; ++s) {
+            bf8 b[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r][t] = mfma_fp4_fp8(a_operand(a[r]), b, acc[r][t], (int)s4[r], sx);
-            }
-        } else {
+            for (int t = 0; t < 4; ++t)
+                b[t] = as_bf8(*reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * ((4 * g + s) ^ l16)));
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                bf8 b[4];
+            for (int r = 0; r < 4; ++r) {
+                const bf8 av = dequant8_bf16(a[r][s], scale_f32(s4[r]));
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    b[t] = as_bf8(*reinterpret_cast<const u4 *>(B + 16 * XR * t + 16 * ((4 * g + s) ^ l16)));
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const bf8 av = dequant8_bf16(a[r][s], scale_f32(s4[r]));
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) acc[r][t] = mfma_bf16(av, b[t], acc[r][t]);
-                }
+                for (int t = 0; t < 4; ++t) acc[r][t] = mfma_bf16(av, b[t], acc[r][t]);
             }
         }
     };
@@ -867,19 +823,19 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     // past the last load the last one's operands again, so that every step
     // issues LPS loads (from empty buffers, whose descriptors are then made
     // anew for each step, the kernel took 2 to 7 % longer).
-    constexpr int LPS = 1 + (TK == kTkExp ? 2 * EP : XP) + 2;
+    constexpr int LPS = 1 + (X8 ? 2 * EP : XP) + 2;
     constexpr int D = NB - 1;
     auto issue = [&](int k, int buf) {
         const int kc = min(k, NS - 1);
         sload(kc);
-        if constexpr (TK == kTkExp) eload(kc);
+        if constexpr (X8) eload(kc);
         wdirect(kc, buf);
-        if constexpr (TK != kTkExp) xdirect(kc, buf);
+        if constexpr (!X8) xdirect(kc, buf);
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
     auto settle = [&](int k, int buf) {
         sstore(min(k, NS - 1), buf);
-        if constexpr (TK == kTkExp) estore(buf);
+        if constexpr (X8) estore(buf);
     };
 #pragma unroll
     for (int k = 0; k < D; ++k) {
@@ -936,12 +892,12 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
 // work-items of a launch are counted in 32 bits
 constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;
 
-template <int NM, int TK>
+template <int NM, bool X8>
 void launch_tile(const DenseParams &p, int64_t blocks, int tok_tiles, hipStream_t s)
 {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_tile<NM, TK>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, tl_lds<TK>());
-    k_mx_tile<NM, TK><<<(unsigned)blocks, 64 * kTlWaves, tl_lds<TK>(), s>>>(p, tok_tiles);
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_tile<NM, X8>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, kTlLds);
+    k_mx_tile<NM, X8><<<(unsigned)blocks, 64 * kTlWaves, kTlLds, s>>>(p, tok_tiles);
 }
 
 template <int NM, bool X8, bool PAIR, int U>
@@ -957,15 +913,15 @@ void launch_gemv(const DenseParams &p, int tiles, int blocks, hipStream_t s)
     k_mx_gemv<NM, X8, PAIR, U><<<(unsigned)blocks, 64 * nw, lds, s>>>(p, tiles);
 }
 
-template <int NM, int TK, int NT>
+template <int NM, bool X8, int NT>
 k3moe_status launch_stream(const DenseParams &p, hipStream_t s)
 {
     const int64_t rb = ((int64_t)p.N + 31) / 32, tb = ((int64_t)p.T + 16 * NT - 1) / (16 * NT);
     if (rb * tb > kMaxItems / (64 * kStW)) return K3MOE_E_UNSUPPORTED_SHAPE;
-    if (st_lds<NM, TK, NT>() > 65536)
-        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_stream<NM, TK, NT>),
-                                  hipFuncAttributeMaxDynamicSharedMemorySize, st_lds<NM, TK, NT>());
-    k_mx_stream<NM, TK, NT><<<(unsigned)(rb * tb), 64 * kStW, st_lds<NM, TK, NT>(), s>>>(p, (int)tb);
+    if (st_lds<NM, X8, NT>() > 65536)
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_stream<NM, X8, NT>),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, st_lds<NM, X8, NT>());
+    k_mx_stream<NM, X8, NT><<<(unsigned)(rb * tb), 64 * kStW, st_lds<NM, X8, NT>(), s>>>(p, (int)tb);
     return K3MOE_OK;
 }
 
@@ -975,26 +931,25 @@ k3moe_status launch_stream(const DenseParams &p, hipStream_t s)
 //   stream: a CU brings a phase's buffer at 60 KB/us for every block it gets;
 //           0.25 us per phase and 4 us around them for every round of the
 //           blocks that its LDS holds at once
-//   tiles:  1.75 us per step of 128 columns (1.2 on the scaled MFMA), a block
-//           per CU at a time
+//   tiles:  1.75 us per step of 128 columns, a block per CU at a time
 // (2048 rows x 7168, 65 bf16 tokens: stream 15 us, tiles 100; 7168 x 7168, 300 of them:
 // 103 and 102; 16384 x 2048, 300: 81 and 35.)
 constexpr double kCus = 256.0;
 
-template <int NM, int TK, int NT>
+template <int NM, bool X8, int NT>
 double stream_us(const DenseParams &p)
 {
     const double blocks = ceil(p.N / 32.0) * ceil(p.T / (16.0 * NT)), phases = ceil(ceil(p.K / 128.0) / kStC);
-    constexpr int held = kMaxLds / st_lds<NM, TK, NT>() < 2 ? 1 : 2;   // blocks in a CU's LDS
-    return ceil(blocks / kCus) * phases * (st_buf<NM, TK, NT>() / 1024 / 60.0) +
+    constexpr int held = kMaxLds / st_lds<NM, X8, NT>() < 2 ? 1 : 2;   // blocks in a CU's LDS
+    return ceil(blocks / kCus) * phases * (st_buf<NM, X8, NT>() / 1024 / 60.0) +
            ceil(blocks / (kCus * held)) * (phases * 0.25 + 4.0);
 }
 
-template <int NM, int TK>
+template <int NM, bool X8>
 double tile_us(const DenseParams &p)
 {
     const double blocks = ceil(p.N * (double)NM / kTlRows) * ceil(p.T / (double)kTlTok);
-    return ceil(blocks / kCus) * ceil(p.K / 128.0) * (TK == kTkF8 ? 1.2 : 1.75) + 2.5;
+    return ceil(blocks / kCus) * ceil(p.K / 128.0) * 1.75 + 2.5;
 }
 
 // f(std::integral_constant<int, I>) for I in [B, E), on the host.
@@ -1007,28 +962,28 @@ void each(F &&f)
     }
 }
 
-// More than kGvTok tokens.
-template <int NM, int TK>
+// More than kGvTok tokens, or fewer whose rows the LDS of k_mx_gemv does not hold.
+template <int NM, bool X8>
 k3moe_status launch_batch(const DenseParams &p, hipStream_t s)
 {
     // token tiles per block: as many as the LDS holds at most
-    constexpr int most = TK == kTkBf16 ? 5 - NM : 4;
-    double us = stream_us<NM, TK, 1>(p);
+    constexpr int most = X8 ? 4 : 5 - NM;
+    double us = stream_us<NM, X8, 1>(p);
     int nt = 1;
     each<2, most + 1>([&](auto k) {
         constexpr int NT = decltype(k)::value;
-        const double u = stream_us<NM, TK, NT>(p);
+        const double u = stream_us<NM, X8, NT>(p);
         if (u < us) us = u, nt = NT;
     });
-    if (p.K >= 128 && tile_us<NM, TK>(p) < us) {
+    if (p.K >= 128 && tile_us<NM, X8>(p) < us) {
         const int64_t rb = ((int64_t)p.N * NM + kTlRows - 1) / kTlRows, tb = ((int64_t)p.T + kTlTok - 1) / kTlTok;
         if (rb * tb > kMaxItems / (64 * kTlWaves)) return K3MOE_E_UNSUPPORTED_SHAPE;
-        launch_tile<NM, TK>(p, rb * tb, (int)tb, s);
+        launch_tile<NM, X8>(p, rb * tb, (int)tb, s);
         return K3MOE_OK;
     }
     k3moe_status st = K3MOE_E_UNSUPPORTED_SHAPE;
     each<1, most + 1>([&](auto k) {
-        if (nt == decltype(k)::value) st = launch_stream<NM, TK, decltype(k)::value>(p, s);
+        if (nt == decltype(k)::value) st = launch_stream<NM, X8, decltype(k)::value>(p, s);
     });
     return st;
 }
@@ -1049,15 +1004,10 @@ k3moe_status launch_dense(const DenseParams &p, hipStream_t s)
     if (p.T <= kGvTok && (int64_t)p.T * 2 * p.K <= kGvMaxLds) {
         if (p.xs) launch_few<NM, true>(p, s);
         else launch_few<NM, false>(p, s);
-    } else if (!p.xs) {
-        st = launch_batch<NM, kTkBf16>(p, s);
-    } else if (p.kind == K3MOE_OUT_BF16) {
-        // the scaled MFMA sums each run of 16 products to about 14 bits below the largest: enough for a bf16
-        // result, and twice the rate; the others take exact products and fp32 sums (an MXFP8 result
-        // because its scale follows its largest value's last bits)
-        st = launch_batch<NM, kTkF8>(p, s);
+    } else if (p.xs) {
+        st = launch_batch<NM, true>(p, s);
     } else {
-        st = launch_batch<NM, kTkExp>(p, s);
+        st = launch_batch<NM, false>(p, s);
     }
     if (st != K3MOE_OK) return st;
     return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
