@@ -430,7 +430,9 @@ typedef enum {
  *   out, outs  as out_kind (k3moe_out) says; outs NULL unless K3MOE_OUT_MXFP8
  * Products of finite tokens (a value beyond bf16's range is infinite) are
  * exact and summed in fp32, whatever the number of tokens and the kind of the
- * result; only a K3MOE_OUT_BF16 or K3MOE_OUT_MXFP8 result is then rounded. */
+ * result; only a K3MOE_OUT_BF16 or K3MOE_OUT_MXFP8 result is then rounded. An
+ * infinite token gives what such sums give: infinities, and NaN where a weight
+ * of its column is zero. */
 k3moe_status k3moe_linear(const uint8_t *packed, const uint8_t *scales, int32_t rows, int32_t cols,
                           const void *x, int64_t x_stride, const uint8_t *xs, int64_t xs_stride,
                           int32_t T, void *out, int64_t out_stride, uint8_t *outs,

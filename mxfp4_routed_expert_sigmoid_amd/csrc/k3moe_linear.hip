@@ -23,7 +23,8 @@
 // K mapping. A 16-byte piece of a row is one block of 32 weights: in chunk c
 // (128 columns) lane 16g + r of an MFMA tile holds block 4c + g of row r, and
 // step s of the chunk multiplies columns 128c + 32g + 8s + [0, 8) of every g; the
-// token side reads the same columns.
+// token side reads the same columns. What a chunk holds past the row's last block
+// is zero on both sides: a zero weight alone would make NaN of an infinite token.
 #include "k3moe_internal.h"
 #include "k3moe_mx8.h"
 
@@ -136,6 +137,7 @@ __device__ __forceinline__ void dense_store(const DenseParams &p, int64_t t, int
 // of 163840 x 7168 127 to 132 us (4.9 TB/s). A plain read of such sizes reaches 4 to 6.
 constexpr int kGvTok = 4, kGvMaxWaves = 8;
 constexpr int kGvMaxLds = 65536;   // token bytes of a block
+constexpr int kGvZeros = 64;       // a block of zeros behind each token: 32 bf16 values
 // A matrix of fewer tiles has a block for each, which the card schedules as
 // they end (18432 rows x 2 matrices x 7168: 33 us, 39 us with two or three
 // tiles per block); a longer one two blocks per CU, each with many tiles,
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
     tiles >>= PAIR;
     const int tile0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x) << PAIR;
     const int tile1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x) << PAIR;
-    const int xrow = 2 * p.K;                                  // LDS bytes of a token: bf16
+    const int xrow = 2 * p.K + kGvZeros;                       // LDS bytes of a token: bf16, a block of zeros
     uint8_t *xl = lds;
     float *red0 = reinterpret_cast<float *>(lds + p.T * xrow); // RB of [wave][NM][token][16]
     constexpr int RB = PAIR ? 4 : 2;
@@ -226,7 +228,7 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
         bf8 b[U][4];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int kc = min(4 * (U * u + j) + g, KB - 1);    // past the row's last block the weights are zeros
+            const int kc = min(4 * (U * u + j) + g, KB);        // past the row's last block: the zeros
 #pragma unroll
             for (int s = 0; s < 4; ++s) b[j][s] = as_bf8(*reinterpret_cast<const u4 *>(bx + 64 * kc + 16 * s));
         }
@@ -296,6 +298,8 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
                 *reinterpret_cast<u4 *>(at) = x;
             }
         }
+        if (__builtin_expect(KB % (4 * U) != 0, 0) && lane < 4 * p.T)
+            *reinterpret_cast<u4 *>(xl + (lane >> 2) * xrow + 2 * p.K + 16 * (lane & 3)) = u4{0u, 0u, 0u, 0u};
         wave_lds_sync();
     }
     // two units at a time: while one is multiplied the other is in flight, across the tiles' borders
@@ -363,6 +367,8 @@ constexpr int kStW = 8, kStC = 4;                 // waves, chunks of a phase
 constexpr int kStMaxBuf = 3;                      // (8 MXFP8 tokens x 7168 x 7168: 9.7 us, 10.0 with four buffers, 10.4 with six)
 template <bool X8> __host__ __device__ constexpr int st_es() { return X8 ? 1 : 2; }  // bytes per token element
 constexpr int kMaxLds = 163840;
+// An offset behind every token's (63 * 2^25 + 2^23 at most): read as zeros.
+constexpr int kStOut = 0x7f000000;
 template <int NM, bool X8, int NT> __host__ __device__ constexpr int st_x() { return 16 * NT * 128 * kStC * st_es<X8>(); }   // tokens of a phase
 template <int NM, bool X8, int NT> __host__ __device__ constexpr int st_buf() { return st_x<NM, X8, NT>() + kStW * NM * 1024; }
 template <int NM, bool X8, int NT> __host__ __device__ constexpr int st_nbuf()
@@ -440,22 +446,28 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
     };
     // direct loads: 64 slots per wave and load, one row of bf16 tokens or two of 8-bit ones, of all four chunks
     constexpr int RL = 2 / ES, SL = 64 / RL;      // rows per load, slots per row
-    const int last = p.K * ES / 16 - 1;           // last slot of a token row
-    const __amdgpu_buffer_rsrc_t xsrc = buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)t0 * p.xst * ES, 0x7fffffff);
+    const __amdgpu_buffer_rsrc_t xsrc = buf_src(static_cast<const uint8_t *>(p.x) + (int64_t)t0 * p.xst * ES, kStOut);
     uint32_t xo[XL];                              // row offsets; rows past the last token lie outside, read as zeros
-    int xs0[ES];                                  // this lane's slot of phase 0 (rows 8 apart take turns in bf16)
+    int xs0[ES], xend[ES];                        // this lane's slot of phase 0 (rows 8 apart take turns in bf16), its run's end
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
         const int row = RL * (kStW * i + uw) + (RL == 1 ? 0 : lane >> 5);
         xo[i] = t0 + row < p.T ? (uint32_t)row * (uint32_t)(p.xst * ES) : 0x80000000u;
         const int j = (lane & (SL - 1)) ^ (row & 15), w = j / (8 * ES);   // its slot of the phase, its chunk's
-        if (i < ES) xs0[i] = 8 * ES * c0(w) + (j & (8 * ES - 1));
+        if (i < ES) xs0[i] = 8 * ES * c0(w) + (j & (8 * ES - 1)), xend[i] = min(8 * ES * c0(w + 1), p.K * ES / 16);
     }
     auto xload = [&](int ph, int buf) {
+        uint32_t slot[ES];
+#pragma unroll
+        for (int i = 0; i < ES; ++i) {
+            const int j = xs0[i] + 8 * ES * ph;
+            if constexpr (X8) slot[i] = 16u * (uint32_t)min(j, p.K / 16 - 1);   // (dropped by their scale bytes, below)
+            else slot[i] = j < xend[i] ? 16u * (uint32_t)j : (uint32_t)kStOut;  // past its run: outside, zeros
+        }
 #pragma unroll
         for (int i = 0; i < XL; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(xsrc, (lds_void *)(lds + buf * BUF + 1024 * (kStW * i + uw)), 16,
-                                                     (int)(xo[i] + 16u * (uint32_t)min(xs0[i % ES] + 8 * ES * ph, last)), 0, 0, 0);
+                                                     (int)(xo[i] + slot[i % ES]), 0, 0, 0);
         asm volatile("" ::: "memory");            // no load moves behind the products
     };
     v4f acc[NM][NT];
@@ -466,7 +478,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 
     // phase ph = 16 seg + 4 quarter + k with the scales of its segment
     auto mul = [&](int ph, int quarter, int k, const Scales &sc, int buf) {
-        const uint32_t past = 4 * (cw + ph) + g < KB && ph < cn ? 0u : ~0u;   // no block of this wave: zero weights
+        const uint32_t past = 4 * (cw + ph) + g < KB && ph < cn ? 0u : ~0u;   // no block of this wave: zeros
         const uint8_t *B = lds + buf * BUF + l16 * 512 * ES;
         const uint8_t *A = lds + buf * BUF + XBUF + wave * NM * 1024 + 64 * l16 + 16 * (g ^ (l16 >> 2));
         const int from = 16 * quarter + l16;      // the lane that holds the phase's scales
@@ -482,7 +494,7 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 #pragma unroll
             for (int t = 0; t < NT; ++t) {   // (every lane takes part in the exchange)
                 const uint32_t sx = ((uint32_t)__shfl((int)sc.x[t][k], from) >> (8 * g)) & 0xffu;
-                xsb[t] = (sx & ~past) | (127u & past);   // past the last block: any finite scale, the weights are zeros
+                xsb[t] = (sx & ~past) | (255u & past);   // past the last block: dropped
             }
         }
         // every fragment of the chunk is read before the first product (the compiler would read each where it
@@ -599,6 +611,8 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15), so a
 // fragment read (one slot of 16 rows) touches every bank once.
 constexpr int kTlRows = 256, kTlTok = 128, kTlWaves = 8;
+// An offset behind every token's (127 * 2^25 + 2^23 at most): read as zeros.
+constexpr int kTlOut = (int)0xff000000u;
 // Four neighbouring results (columns n .. n + 3 of token t; the 8 lanes of an
 // octet hold one group of 32 columns). nin: how many of them exist (0: none).
 __device__ __forceinline__ void dense_store4(const DenseParams &p, int64_t t, int n, int nin, float4 y)
@@ -725,7 +739,7 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     const uint8_t *xb = static_cast<const uint8_t *>(p.x);
     const uint8_t *xr[EP], *xsr[EP];
     uint32_t xo[XP];
-    const __amdgpu_buffer_rsrc_t xsrc = buf_src(xb + (int64_t)t0 * p.xst * ES);
+    const __amdgpu_buffer_rsrc_t xsrc = buf_src(xb + (int64_t)t0 * p.xst * ES, kTlOut);
     if constexpr (X8) {
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
@@ -739,14 +753,13 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
             xo[i] = (uint32_t)min((tid + 512 * i) / SL, p.T - 1 - t0) * (uint32_t)(p.xst * ES);
     }
     const int last = p.K * ES / 16 - 1;           // last slot of a token row
-    // slot j of token r lies at j ^ (r mod 16) of 16, or j ^ (r / 2 mod 8) of 8 (the passes keep r mod 16)
-    const int xsw = SL == 16 ? (tid >> 4) & 15 : (tid >> 4) & 7;
+    const int xsw = (tid >> 4) & 15;              // slot j of token r lies at j ^ (r mod 16) (the passes keep r mod 16)
     auto xdirect = [&](int k, int buf) {
-        const uint32_t o = 16u * (uint32_t)min(SL * k + ((tid & (SL - 1)) ^ xsw), last);
+        const int slot = SL * k + ((tid & (SL - 1)) ^ xsw);
 #pragma unroll
         for (int i = 0; i < XP; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(xsrc, (lds_void *)(lds + buf * BUF + (512 * i + 64 * wave) * 16), 16,
-                                                     (int)(xo[i] + o), 0, 0, 0);
+                                                     (int)(slot <= last ? xo[i] + 16u * (uint32_t)slot : (uint32_t)kTlOut), 0, 0, 0);
     };
     u4 xe[EP];
     uint32_t xes[EP];
@@ -758,7 +771,7 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
             xes[i] = xsr[i][slot >> 1];
         }
     };
-    auto estore = [&](int buf) {
+    auto estore = [&](int k, int buf) {
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
             const int row = (tid >> 3) + 64 * i, j = 2 * (tid & 7);
@@ -768,6 +781,15 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
             uint8_t *d = lds + buf * BUF + row * 256;
             lds_put16(d + 16 * (j ^ (row & 15)), expand8_fp8(v.x, v.y, f));
             lds_put16(d + 16 * ((j + 1) ^ (row & 15)), expand8_fp8(v.z, v.w, f));
+        }
+        if (4 * k + 4 > KB && 8 * k + (tid & 7) > last) {   // behind the row's last slot: zeros
+#pragma unroll
+            for (int i = 0; i < EP; ++i) {
+                const int row = (tid >> 3) + 64 * i, j = 2 * (tid & 7);
+                uint8_t *d = lds + buf * BUF + row * 256;
+                lds_put16(d + 16 * (j ^ (row & 15)), bf8{});
+                lds_put16(d + 16 * ((j + 1) ^ (row & 15)), bf8{});
+            }
         }
     };
 
@@ -835,7 +857,7 @@ __global__ __launch_bounds__(64 * kTlWaves) void k_mx_tile(DenseParams p, int to
     };
     auto settle = [&](int k, int buf) {
         sstore(min(k, NS - 1), buf);
-        if constexpr (X8) estore(buf);
+        if constexpr (X8) estore(min(k, NS - 1), buf);
     };
 #pragma unroll
     for (int k = 0; k < D; ++k) {
@@ -906,7 +928,7 @@ void launch_gemv(const DenseParams &p, int tiles, int blocks, hipStream_t s)
     const int NU = (p.K / 32 + 4 * U - 1) / (4 * U);
     // waves per block: the fewest that give the same longest share as the most
     const int share = (NU + kGvMaxWaves - 1) / kGvMaxWaves, nw = (NU + share - 1) / share;
-    const int lds = p.T * 2 * p.K + (PAIR ? 4 : 2) * nw * NM * kGvTok * 64;
+    const int lds = p.T * (2 * p.K + kGvZeros) + (PAIR ? 4 : 2) * nw * NM * kGvTok * 64;
     if (lds > 65536)
         (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&k_mx_gemv<NM, X8, PAIR, U>),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, kGvMaxLds + 65536);

@@ -1,6 +1,7 @@
 """GPU tests of what the dense products make of values that ordinary inputs do
-not hold: products of very different sizes in one run of the sum. Against the
-64-bit statements of ``dense_ref``; what is exact is compared bit for bit."""
+not hold: products of very different sizes in one run of the sum, infinite
+tokens. Against the 64-bit statements of ``dense_ref``; what is exact is
+compared bit for bit."""
 import numpy as np
 import pytest
 import torch
@@ -98,3 +99,65 @@ def test_glu_sums_keep_32_bits(T, N, K, x8):
         k3.glu(*map(_t, mats[0]), *map(_t, mats[1]), x, o, xs=xs, act=k3.ACT_SWIGLU)
         half = 2.0 ** -8 if out == "bf16" else 2.0 ** -24
         assert np.all(np.abs(o.double().cpu().numpy() - want) <= np.abs(want) * (ACT_TOL + half * (1 + ACT_TOL)))
+
+
+# --- infinite tokens --------------------------------------------------------
+# A token t holds one infinity, in block t mod (K / 32) (so every block has one
+# where there are tokens enough; the last token holds it in the last column), at a
+# column whose weight is zero in no row: its results are infinities with the sign of
+# the weights. In MXFP8 the infinity is 448 * 2^127, beyond bf16's range.
+def _infinite(T, N, K, x8, r):
+    codes = r.integers(0, 16, (N, K))
+    s = np.full((N, K // 32), 127, np.uint8)
+    v = r.integers(-15, 16, (T, K)).astype(np.float64)
+    at = 32 * (np.arange(T) % (K // 32)) + (7 * np.arange(T) + 31) % 32
+    at[-1] = K - 1
+    cols = np.unique(at)
+    codes[:, cols] = np.where(codes[:, cols] & 7, codes[:, cols], 1)
+    neg = r.integers(0, 2, T).astype(bool)
+    x, xs, _ = _tokens(v, x8)
+    rows = np.arange(T)
+    if x8:
+        q, sb = x.cpu().numpy(), xs.cpu().numpy()
+        for t in range(T):
+            b = at[t] // 32
+            q[t, 32 * b:32 * b + 32], q[t, at[t]], sb[t, b] = 0, 0xfe if neg[t] else 0x7e, 254
+        x, xs = _t(q), _t(sb)
+    else:
+        x[_t(rows), _t(at)] = _t(np.where(neg, -np.inf, np.inf).astype(np.float32)).to(torch.bfloat16)
+    p = _pack(codes)
+    w = R.dense(p, s)[:, at].T                # [T][N]: the weights at each token's infinity
+    return p, s, x, xs, np.where((w < 0) == neg[:, None], np.inf, -np.inf)
+
+
+INF = [(1, 40, 32), (1, 40, 160), (4, 40, 96), (3, 40, 1056), (4, 66001, 288), (2, 16500, 2080), (5, 45, 160), (9, 45, 288),
+       (40, 40, 160), (33, 45, 1056), (66, 45, 2080), (47, 4137, 1184), (130, 20001, 160), (300, 9001, 1056),
+       (129, 16640, 2048)]
+
+
+@pytest.mark.parametrize("T,N,K", INF)
+@pytest.mark.parametrize("x8", [False, True])
+def test_linear_of_infinite_tokens(T, N, K, x8):
+    _need()
+    r = np.random.default_rng([T, N, K])
+    p, s, x, xs, want = _infinite(T, N, K, x8, r)
+    for out in ("f32", "bf16", "add"):
+        _, o, _, _, _ = _result(out, T, N, 0, r)
+        print(f"[linear] T={T} N={N} K={K} x8={x8} out={out}", flush=True)
+        k3.linear(_t(p), _t(s), x, o, xs=xs, accumulate=out == "add")
+        assert np.array_equal(o.double().cpu().numpy(), want)
+    _, o, _, os_, _ = _result("mxfp8", T, N, 0, r)
+    k3.linear(_t(p), _t(s), x, o, xs=xs, outs=os_)
+    assert bool((_t(_f8(o)) & 127 == 127).all()) and bool((os_ == 0).all())
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 40, 160), (3, 40, 1056), (5, 45, 160), (33, 257, 1184), (130, 20001, 160)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_glu_of_infinite_tokens(T, N, K, x8):
+    # SiTU's arms end at +-b1 and +-b2 and its sigmoid at 0 and 1
+    _need()
+    r = np.random.default_rng([T, N, K])
+    p, s, x, xs, y = _infinite(T, N, K, x8, r)
+    out = torch.empty((T, N), device=DEV)
+    k3.glu(_t(p), _t(s), _t(p), _t(s), x, out, xs=xs)
+    assert np.array_equal(out.double().cpu().numpy(), np.where(y > 0, 100.0, 0.0))
