@@ -428,10 +428,12 @@ typedef enum {
  *       bf16); 16-byte aligned rows, strides up to 2^24 elements
  *       (K3MOE_E_UNSUPPORTED_SHAPE above)
  *   out, outs  as out_kind (k3moe_out) says; outs NULL unless K3MOE_OUT_MXFP8
- * Products of finite tokens (a value beyond bf16's range is infinite) are
- * exact and summed in fp32, whatever the number of tokens and the kind of the
- * result; only a K3MOE_OUT_BF16 or K3MOE_OUT_MXFP8 result is then rounded. An
- * infinite token gives what such sums give: infinities, and NaN where a weight
+ * Weights and tokens are multiplied as bf16. That holds every MXFP4 weight and
+ * MXFP8 value but those out of its range: one beyond it is infinite, and an
+ * MXFP8 value that is no multiple of 2^-133 (groups of byte 0 to 2 only) is off
+ * by less than 2^-133. Products are exact (in fp32's range) and summed in fp32,
+ * whatever the number of tokens and the kind of the result; only a
+ * K3MOE_OUT_BF16 or K3MOE_OUT_MXFP8 result is then rounded. An infinite token gives what such sums give: infinities, and NaN where a weight
  * of its column is zero. */
 k3moe_status k3moe_linear(const uint8_t *packed, const uint8_t *scales, int32_t rows, int32_t cols,
                           const void *x, int64_t x_stride, const uint8_t *xs, int64_t xs_stride,

@@ -6,8 +6,9 @@
 // byte"), the activation §9's k3_situ_glu.
 //
 // Weights and 8-bit tokens are expanded to bf16 in registers, which is exact
-// (an fp4 or e4m3 value times a power of two is a bf16; one past bf16's range is
-// infinite), and multiplied on v_mfma_f32_16x16x32_bf16: exact products, fp32
+// within bf16's range (an fp4 or e4m3 value times a power of two has few bits; one past
+// the range is infinite, and an e4m3 value below 2^-126 that is no multiple of 2^-133,
+// from a group of byte 0 to 2, loses what lies below), and multiplied on v_mfma_f32_16x16x32_bf16: exact products, fp32
 // sums. (The block-scaled MFMA would take 8-bit tokens as they are at twice the rate,
 // but sums each run of 16 products to about 14 bits below the largest, which shows in a
 // result where large products cancel: it is not used, whatever the result's type.)

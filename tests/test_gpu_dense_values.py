@@ -1,7 +1,7 @@
 """GPU tests of what the dense products make of values that ordinary inputs do
 not hold: products of very different sizes in one run of the sum, infinite
-tokens. Against the 64-bit statements of ``dense_ref``; what is exact is
-compared bit for bit."""
+tokens, tokens below bf16's range. Against the 64-bit statements of
+``dense_ref``; what is exact is compared bit for bit."""
 import numpy as np
 import pytest
 import torch
@@ -161,3 +161,26 @@ def test_glu_of_infinite_tokens(T, N, K, x8):
     out = torch.empty((T, N), device=DEV)
     k3.glu(_t(p), _t(s), _t(p), _t(s), x, out, xs=xs)
     assert np.array_equal(out.double().cpu().numpy(), np.where(y > 0, 100.0, 0.0))
+
+
+# --- tokens below bf16's range ----------------------------------------------
+# e4m3 goes down to 2^-9, so a group of byte 0 to 2 holds multiples of 2^-136, which bf16
+# (multiples of 2^-133 at least) does not: such a token value is taken within one
+# step 2^-133. From byte 3 on every value is a bf16. The weights are about 2^123.
+@pytest.mark.parametrize("T,N,K", [(1, 33, 160), (3, 33, 1056), (7, 45, 160), (40, 45, 1056), (130, 20001, 160)])
+@pytest.mark.parametrize("byte", [0, 1, 2, 3, 4])
+def test_smallest_tokens(T, N, K, byte):
+    _need()
+    r = np.random.default_rng([T, N, K, byte])
+    p = r.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    s = np.full((N, K // 32), 250, np.uint8)
+    q = R.e4m3_rne(r.integers(-15, 16, (T, K)) * 2.0 ** -9)
+    xs = np.full((T, K // 32), byte, np.uint8)
+    out = torch.empty((T, N), device=DEV)
+    k3.linear(_t(p), _t(s), _t(q), out, xs=_t(xs))
+    got, W, xv = out.double().cpu().numpy(), R.dense(p, s), R.tokens8(q, xs)
+    want = xv @ W.T
+    if byte >= 3:      # multiples of 2^-133 * 2^122, sums below 2^24 of them
+        assert np.array_equal(got, want)
+    else:
+        assert np.all(np.abs(got - want) <= 2.0 ** -133 * np.abs(W).sum(1))
