@@ -433,8 +433,9 @@ typedef enum {
  * MXFP8 value that is no multiple of 2^-133 (groups of byte 0 to 2 only) is off
  * by less than 2^-133. Products are exact (in fp32's range) and summed in fp32,
  * whatever the number of tokens and the kind of the result; only a
- * K3MOE_OUT_BF16 or K3MOE_OUT_MXFP8 result is then rounded. An infinite token gives what such sums give: infinities, and NaN where a weight
- * of its column is zero. */
+ * K3MOE_OUT_BF16 or K3MOE_OUT_MXFP8 result is then rounded. An infinite token
+ * gives what such sums give: infinities, and NaN where a weight of its column
+ * is zero. */
 k3moe_status k3moe_linear(const uint8_t *packed, const uint8_t *scales, int32_t rows, int32_t cols,
                           const void *x, int64_t x_stride, const uint8_t *xs, int64_t xs_stride,
                           int32_t T, void *out, int64_t out_stride, uint8_t *outs,

@@ -1,7 +1,8 @@
-"""GPU tests of what the dense products make of values that ordinary inputs do
-not hold: products of very different sizes in one run of the sum, infinite
-tokens, tokens below bf16's range. Against the 64-bit statements of
-``dense_ref``; what is exact is compared bit for bit."""
+"""GPU tests of what the dense operators make of values and sizes that ordinary
+inputs do not have: products of very different sizes in one run of the sum,
+infinite tokens, tokens below bf16's range, more rows than a grid has blocks.
+Against the 64-bit statements of ``dense_ref``; what is exact is compared bit
+for bit."""
 import numpy as np
 import pytest
 import torch
@@ -184,3 +185,27 @@ def test_smallest_tokens(T, N, K, byte):
         assert np.array_equal(got, want)
     else:
         assert np.all(np.abs(got - want) <= 2.0 ** -133 * np.abs(W).sum(1))
+
+
+# --- sizes ------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,want", [(8, "both"), (9, "mxfp8")])
+def test_norm_of_more_rows_than_a_grid_holds(H, want):
+    # 2^20 blocks: the last rows are a block's second one. Rows repeat every 1021, so each is compared
+    # with the same row of a short call
+    _need()
+    T, R0 = (1 << 20) + 1500, 1021
+    r = np.random.default_rng(H)
+    h0, d0, gamma = (_t((4 * r.standard_normal(s)).astype(np.float32)) for s in ((R0, H), (R0, H), (H,)))
+
+    def call(h, d):
+        t = h.shape[0]
+        x = torch.empty((t, H), dtype=torch.bfloat16, device=DEV) if want == "both" else None
+        q = torch.empty((t, H), dtype=torch.uint8, device=DEV)
+        qs = torch.empty((t, 1), dtype=torch.uint8, device=DEV)
+        k3.add_norm(h, gamma, 1e-5, d=d, x=x, q=q, qs=qs)
+        return [h, q, qs] + ([x.view(torch.int16)] if x is not None else [])
+    short = call(h0.clone(), d0)
+    i = torch.arange(T, device=DEV) % R0
+    for a, b in zip(short, call(h0[i], d0[i])):
+        assert torch.equal(a[i], b)
