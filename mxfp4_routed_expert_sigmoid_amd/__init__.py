@@ -454,6 +454,8 @@ class Cache:
 # ---------------------------------------------------------------------------
 # Dense operators (k3moe_add_norm, k3moe_linear, k3moe_glu): functions over
 # device tensors. Rows may be views of wider buffers (unit stride in a row).
+# They have no backward: results that require grad are refused, and what a call
+# wrote counts as changed in place.
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values or their bit patterns
 _F32 = (torch.float32,)
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
@@ -487,7 +489,7 @@ def _mat(t, rows, width, dtypes, name, dev):
 
 def _vec(t, n, name, dev):
     """The address of an fp32 [n] tensor on device number `dev`."""
-    if tuple(t.shape) != (n,) or t.dtype != torch.float32 or not t.is_contiguous():
+    if t.shape != (n,) or t.dtype != torch.float32 or not t.is_contiguous():
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous float32 ({n},)")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
@@ -500,9 +502,23 @@ def _queue(dev, stream):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _done(status, what):
+_grad_enabled = torch.is_grad_enabled
+_changed = torch._C._increment_version
+
+
+def _untracked(written):
+    """Refuse results that autograd tracks: these calls have no backward."""
+    for t in written:
+        if t.requires_grad:
+            raise ValueError("a result requires grad: no gradient passes through this call")
+
+
+def _done(status, what, written):
+    """Raise for a refused call; mark what a made one wrote as changed, so that
+    a backward pass that saved it raises instead of using the new values."""
     if status:
         raise K3MoeError(status, what)
+    _changed(written)
 
 
 def _elsewhere(dev):
@@ -533,11 +549,18 @@ def add_norm(h, gamma, eps, d=None, x=None, q=None, qs=None, stream=None):
     if q is not None:
         qp, qst = _mat(q, T, H, _E4M3, "q", dev)
         qsp, qsst = _mat(qs, T, (H + 31) // 32, _E8M0, "qs", dev)
+    written = () if x is None else (x,)
+    if q is not None:
+        written += (q, qs)
+    if d is not None:
+        written += (h,)
+    if _grad_enabled():
+        _untracked(written)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return add_norm(h, gamma, eps, d, x, q, qs, stream)
     _done(lib().k3moe_add_norm(hp, hst, dp, dk, dst, T, H, gp, eps, xp, xst, qp, qst, qsp, qsst, _queue(dev, stream)),
-          "k3moe_add_norm")
+          "k3moe_add_norm", written)
 
 
 _U8 = (torch.uint8,)
@@ -584,10 +607,13 @@ def linear(packed, scales, x, out, xs=None, outs=None, accumulate=False, stream=
     if accumulate and outs is not None:
         raise ValueError("accumulate takes an fp32 out")
     T, tok, res = _dense(x, xs, out, outs, N, K, accumulate, dev)
+    written = (out,) if outs is None else (out, outs)
+    if _grad_enabled():
+        _untracked(written)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return linear(packed, scales, x, out, xs, outs, accumulate, stream)
-    _done(lib().k3moe_linear(wp, sp, N, K, *tok, T, *res, _queue(dev, stream)), "k3moe_linear")
+    _done(lib().k3moe_linear(wp, sp, N, K, *tok, T, *res, _queue(dev, stream)), "k3moe_linear", written)
 
 
 def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=None, act=ACT_SITU,
@@ -600,7 +626,11 @@ def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=No
     up, us = _weight(up_packed, up_scales, "up_", dev)
     N, K = gate_packed.shape[0], 2 * gate_packed.shape[1]
     T, tok, res = _dense(x, xs, out, outs, N, K, False, dev)
+    written = (out,) if outs is None else (out, outs)
+    if _grad_enabled():
+        _untracked(written)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs, outs, act, situ_b1, situ_b2, stream)
-    _done(lib().k3moe_glu(gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res, _queue(dev, stream)), "k3moe_glu")
+    _done(lib().k3moe_glu(gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res, _queue(dev, stream)), "k3moe_glu",
+          written)
