@@ -29,6 +29,8 @@
 #include "k3moe_internal.h"
 #include "k3moe_mx8.h"
 
+#include <algorithm>
+
 namespace k3moe {
 namespace {
 
@@ -139,12 +141,20 @@ __device__ __forceinline__ void dense_store(const DenseParams &p, int64_t t, int
 constexpr int kGvTok = 4, kGvMaxWaves = 8;
 constexpr int kGvMaxLds = 65536;   // token bytes of a block
 constexpr int kGvZeros = 64;       // a block of zeros behind each token: 32 bf16 values
-// A matrix of fewer tiles has a block for each, which the card schedules as
-// they end (18432 rows x 2 matrices x 7168: 33 us, 39 us with two or three
-// tiles per block); a longer one two blocks per CU, each with many tiles,
-// which keeps the tokens in LDS and the loads in flight between them
-// (4 tokens x 163840 rows x 7168: 124 us, a block per tile 161 us).
-constexpr int kGvLong = 4096, kGvBlocks = 512;
+// A matrix of fewer tiles has a block for each (or for each pair), which the card
+// schedules as they end; a longer one two blocks per CU, each with many tiles, which
+// keeps the tokens in LDS and the loads in flight between them (without pairs, 512
+// bytes of a row per unit instead of 256). Measured, us with a block per tile / so, on
+// one token and on four (7168 columns; 2048 columns cross over earlier):
+//   one matrix          700 tiles 12.0 / 13.3   15.7 / 15.7    1152 16.8 / 17.1   22.0 / 19.4
+//                      1700       25.4 / 23.9   32.9 / 26.2   10240 133 / 113     171 / 124
+//   one, in pairs      1152       17.2 / 19.0   20.1 / 20.7    1700 24.6 / 23.7   28.2 / 25.3
+//   two                1152       33.0 / 40.1   40.1 / 43.7    1700 46.9 / 50.5   55.4 / 54.8
+//                      2000       55.2 / 53.2   65.8 / 57.6    4095 103 / 96
+//   two, in pairs      1152       35.8 / 46.1   40.9 / 50.3    2300 58.7 / 68.8   67.0 / 72.5
+//                      3000       78.9 / 73.8   87.2 / 77.8    6000 142 / 142     157 / 147
+template <int NM, bool PAIR> __host__ __device__ constexpr int gv_long() { return (1024 * NM) << PAIR; }   // tiles
+constexpr int kGvBlocks = 512;
 
 // Weights of one unit (U chunks of 128 columns) of a 16-row tile: its chunks of
 // this lane's row, and the row's scale bytes of them (chunk j in dword j).
@@ -189,7 +199,7 @@ __global__ __launch_bounds__(64 * kGvMaxWaves) void k_mx_gemv(DenseParams p, int
     const int g = lane >> 4, l16 = lane & 15;
     const int KB = p.K / 32, NU = (KB + 4 * U - 1) / (4 * U);
     const int u0 = NU * wave / nw, u1 = NU * (wave + 1) / nw;  // at least one unit each
-    // this block's row tiles (PAIR: an even number of them)
+    // this block's row tiles, one at least (without one it would not end; PAIR: an even number of them)
     tiles >>= PAIR;
     const int tile0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x) << PAIR;
     const int tile1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x) << PAIR;
@@ -926,6 +936,7 @@ void launch_tile(const DenseParams &p, int64_t blocks, int tok_tiles, hipStream_
 template <int NM, bool X8, bool PAIR, int U>
 void launch_gemv(const DenseParams &p, int tiles, int blocks, hipStream_t s)
 {
+    blocks = std::min(blocks, tiles >> PAIR);   // each has a tile
     const int NU = (p.K / 32 + 4 * U - 1) / (4 * U);
     // waves per block: the fewest that give the same longest share as the most
     const int share = (NU + kGvMaxWaves - 1) / kGvMaxWaves, nw = (NU + share - 1) / share;
@@ -1015,8 +1026,8 @@ template <int NM, bool X8>
 void launch_few(const DenseParams &p, hipStream_t s)
 {
     const int t1 = (int)(((int64_t)p.N + 15) / 16), t2 = (t1 + 1) / 2;
-    if (p.kind == K3MOE_OUT_MXFP8) launch_gemv<NM, X8, true, 2>(p, 2 * t2, t1 < kGvLong ? t2 : kGvBlocks, s);
-    else if (t1 < kGvLong) launch_gemv<NM, X8, false, 2>(p, t1, t1, s);
+    if (p.kind == K3MOE_OUT_MXFP8) launch_gemv<NM, X8, true, 2>(p, 2 * t2, t1 < gv_long<NM, true>() ? t2 : kGvBlocks, s);
+    else if (t1 < gv_long<NM, false>()) launch_gemv<NM, X8, false, 2>(p, t1, t1, s);
     else launch_gemv<NM, X8, false, 4>(p, t1, kGvBlocks, s);
 }
 

@@ -10,7 +10,7 @@ import torch
 import dense_ref as R
 import mxfp4_routed_expert_sigmoid_amd as k3
 from gpu_helpers import bf16_rne_np
-from test_gpu_dense import ACT_TOL, DEV, _f8, _need, _result, _t
+from test_gpu_dense import ACT_TOL, DEV, _f8, _glu_scaled, _linear, _need, _result, _t
 
 pytestmark = pytest.mark.gpu
 
@@ -188,6 +188,16 @@ def test_smallest_tokens(T, N, K, byte):
 
 
 # --- sizes ------------------------------------------------------------------
+# a block per tile and blocks of many tiles, on both sides of the borders between them (1024 to 4096 tiles), one unit
+# of columns per wave and more
+@pytest.mark.parametrize("T,N,K", [(1, 16368, 256), (2, 16400, 2048), (4, 16385, 1056), (1, 32752, 512), (3, 32785, 288),
+                                   (2, 65552, 96)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_few_tokens_at_the_borders_of_long_matrices(T, N, K, x8):
+    for out in ("f32", "mxfp8"):
+        _linear(T, N, K, x8, out)
+        _glu_scaled(T, N, K, x8, out, 1)
+
 
 @pytest.mark.parametrize("H,want", [(8, "both"), (9, "mxfp8")])
 def test_norm_of_more_rows_than_a_grid_holds(H, want):
