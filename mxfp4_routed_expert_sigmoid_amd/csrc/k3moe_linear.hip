@@ -136,8 +136,8 @@ __device__ __forceinline__ void dense_store(const DenseParams &p, int64_t t, int
 // took 173 registers and half the waves (2 x 18432 x 7168 to MXFP8: 51 us, 37 so).
 //
 // One token, in a graph: 1536 x 7168 5.2 us (a launch and one unit's latency),
-// 7168 x 18432 16.3 us (4.3 TB/s), 2 x 18432 x 7168 34 us (4.1 TB/s); four tokens
-// of 163840 x 7168 127 to 132 us (4.9 TB/s). A plain read of such sizes reaches 4 to 6.
+// 7168 x 18432 16.5 us (4.3 TB/s), 2 x 18432 x 7168 33 us (4.3 TB/s); four tokens
+// of 163840 x 7168 122 us (5.2 TB/s). A plain read of such sizes reaches 4 to 6.
 constexpr int kGvTok = 4, kGvMaxWaves = 8;
 constexpr int kGvMaxLds = 65536;   // token bytes of a block
 constexpr int kGvZeros = 64;       // a block of zeros behind each token: 32 bf16 values
@@ -367,15 +367,18 @@ __device__ __forceinline__ void tile_barrier()
 // order, a load costs the address unit about a cycle per lane.
 //
 // Measured on 7168 rows x 7168, in a graph: 8 MXFP8 tokens 10.4 us, 8 bf16
-// tokens 10.6, 48 MXFP8 tokens 18.7 (264 TFLOP/s), 48 bf16 tokens 18.6. Every
-// block reads its tokens anew (and expands those in 8 bits), which only more rows
-// per block would change, and those would leave CUs idle. Phases of eight chunks,
+// tokens 10.6, 48 MXFP8 tokens 18.7 (264 TFLOP/s), 48 bf16 tokens 18.6. No unit of
+// the card is busy for much more than half of that (data return of the loads 44 to 53 %,
+// MFMAs 7 to 12 %, L2 misses only the weights): two waves per SIMD wait 45 % of
+// their cycles for loads and barriers. Every block reads its tokens anew (and
+// expands those in 8 bits), which only more rows per block would change, and those
+// would leave CUs idle. Phases of eight chunks,
 // one per wave and both row tiles, do not hold 64 bf16 tokens (301 tokens x 1001 x
 // 2080: 16.0 us, 9.1 so).
 //
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15).
 constexpr int kStW = 8, kStC = 4;                 // waves, chunks of a phase
-constexpr int kStMaxBuf = 3;                      // (8 MXFP8 tokens x 7168 x 7168: 9.7 us, 10.0 with four buffers, 10.4 with six)
+constexpr int kStMaxBuf = 3;                      // (8 MXFP8 tokens x 7168 x 7168: 10.6 us, 11.0 with four buffers, 11.6 with six)
 template <bool X8> __host__ __device__ constexpr int st_es() { return X8 ? 1 : 2; }  // bytes per token element
 constexpr int kMaxLds = 163840;
 // An offset behind every token's (63 * 2^25 + 2^23 at most): read as zeros.
@@ -613,11 +616,11 @@ __global__ __launch_bounds__(64 * kStW) void k_mx_stream(DenseParams p, int tok_
 // side because a token's bytes are four times a weight row's: LDS reads take
 // half the cycles of the MFMAs.
 //
-// 2048 tokens x 7168 x 18432: bf16 to bf16 514 us (1.05 PFLOP/s; the library's
-// bf16 product of that size 522), MXFP8 to bf16 or fp32 549 us (0.99: the expansion of
-// the tokens), += 569. Of the 514, 349 are left without loads
-// and LDS reads, the MFMAs with the expansion of the weights, and 388 with the
-// reads; 448 tiles on 256 CUs are two rounds of which the second is 3/4 full.
+// 2048 tokens x 7168 x 18432: bf16 to bf16 508 us (1.07 PFLOP/s; the library's
+// bf16 product of that size 522), MXFP8 to bf16 557 us (0.97: the expansion of the
+// tokens), += 577. MFMAs are busy for 43 and 39 % of it. Of 514 us for bf16, 349 were left
+// without loads and LDS reads, the MFMAs with the expansion of the weights, and 388
+// with the reads; 448 tiles on 256 CUs are two rounds of which the second is 3/4 full.
 //
 // LDS holds slot j (16 bytes) of token row r at slot j ^ (r & 15), so a
 // fragment read (one slot of 16 rows) touches every bank once.
@@ -966,8 +969,9 @@ k3moe_status launch_stream(const DenseParams &p, hipStream_t s)
 //           0.25 us per phase and 4 us around them for every round of the
 //           blocks that its LDS holds at once
 //   tiles:  1.75 us per step of 128 columns, a block per CU at a time
-// (2048 rows x 7168, 65 bf16 tokens: stream 15 us, tiles 100; 7168 x 7168, 300 of them:
-// 103 and 102; 16384 x 2048, 300: 81 and 35.)
+// (2048 rows x 7168, 65 bf16 tokens: stream 15 us, tiles 99; 7168 x 7168, 300 of them:
+// 101 and 100; 16384 x 2048, 300: 76 and 35. MXFP8 tokens: 15 and 109; 103 and 109; 86
+// and 38.)
 constexpr double kCus = 256.0;
 
 template <int NM, bool X8, int NT>
