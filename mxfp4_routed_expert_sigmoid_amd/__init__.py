@@ -503,6 +503,7 @@ def _queue(dev, stream):
 
 
 _grad_enabled = torch.is_grad_enabled
+# marks tensors as changed in place: a backward pass that saved one raises instead of using its new values
 _changed = torch._C._increment_version
 
 
@@ -511,14 +512,6 @@ def _untracked(written):
     for t in written:
         if t.requires_grad:
             raise ValueError("a result requires grad: no gradient passes through this call")
-
-
-def _done(status, what, written):
-    """Raise for a refused call; mark what a made one wrote as changed, so that
-    a backward pass that saved it raises instead of using the new values."""
-    if status:
-        raise K3MoeError(status, what)
-    _changed(written)
 
 
 def _elsewhere(dev):
@@ -559,8 +552,10 @@ def add_norm(h, gamma, eps, d=None, x=None, q=None, qs=None, stream=None):
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return add_norm(h, gamma, eps, d, x, q, qs, stream)
-    _done(lib().k3moe_add_norm(hp, hst, dp, dk, dst, T, H, gp, eps, xp, xst, qp, qst, qsp, qsst, _queue(dev, stream)),
-          "k3moe_add_norm", written)
+    status = lib().k3moe_add_norm(hp, hst, dp, dk, dst, T, H, gp, eps, xp, xst, qp, qst, qsp, qsst, _queue(dev, stream))
+    if status:
+        raise K3MoeError(status, "k3moe_add_norm")
+    _changed(written)
 
 
 _U8 = (torch.uint8,)
@@ -613,7 +608,10 @@ def linear(packed, scales, x, out, xs=None, outs=None, accumulate=False, stream=
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return linear(packed, scales, x, out, xs, outs, accumulate, stream)
-    _done(lib().k3moe_linear(wp, sp, N, K, *tok, T, *res, _queue(dev, stream)), "k3moe_linear", written)
+    status = lib().k3moe_linear(wp, sp, N, K, *tok, T, *res, _queue(dev, stream))
+    if status:
+        raise K3MoeError(status, "k3moe_linear")
+    _changed(written)
 
 
 def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=None, act=ACT_SITU,
@@ -632,5 +630,7 @@ def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=No
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs, outs, act, situ_b1, situ_b2, stream)
-    _done(lib().k3moe_glu(gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res, _queue(dev, stream)), "k3moe_glu",
-          written)
+    status = lib().k3moe_glu(gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res, _queue(dev, stream))
+    if status:
+        raise K3MoeError(status, "k3moe_glu")
+    _changed(written)
