@@ -452,6 +452,139 @@ k3moe_status k3moe_glu(const uint8_t *gate_packed, const uint8_t *gate_scales,
                        void *out, int64_t out_stride, uint8_t *outs, int64_t outs_stride,
                        int32_t out_kind, void *stream);
 
+/* Attention and what stands around it: the steps between a decoder's q/k/v
+ * projection (k3moe_linear) and its output projection, whose result
+ * k3moe_add_norm adds, and the log probabilities of its logits. They run on the
+ * current HIP device, allocate nothing, may be captured into a graph, keep no
+ * state, and use a workspace where they say so (256-byte aligned, the caller's;
+ * calls in flight at the same time need different ones; what is in it before a
+ * call does not matter). Inference only. Deterministic: the same call gives the
+ * same bits.
+ *
+ * Heads: queries [T][q_heads][dim], keys and values [T][kv_heads][dim], each
+ * row's heads contiguous, rows `stride` elements apart (rows may be part of a
+ * wider projection). Query head h reads key/value head h / (q_heads / kv_heads);
+ * q_heads is a multiple of kv_heads.
+ *
+ * Cache pages: keys k [pages][kv_heads][page][k_dim] and values v
+ * [pages][kv_heads][page][v_dim], contiguous, page a power of two, 16 to 2^20. In
+ * bf16 (ks, vs NULL) or in MXFP8: e4m3 values and E8M0 bytes
+ * [pages][kv_heads][page][dim/32], as the tokens above are held. */
+typedef struct {
+    void *k, *v;
+    uint8_t *ks, *vs;
+    int32_t pages, page;
+} k3moe_pages;
+
+/* Which dimensions of a head turn together. */
+typedef enum {
+    K3MOE_ROT_HALVES = 1, /* i and i + rot_dim / 2 */
+    K3MOE_ROT_PAIRS = 2   /* 2 i and 2 i + 1       */
+} k3moe_rot;
+
+/* Norm of every query and key head, rotation by position, and the write of keys
+ * and values into the cache, in one pass. Per head x of width dim:
+ *   n = x * inv * gamma, inv = (float)(1 / sqrt(sum x^2 / dim + eps))    fp32
+ *       (gamma NULL: n = x; q and k have a gamma each)
+ *   a = positions[t] * inv_freq[i], i < rot_dim / 2                      64 bits
+ *   y1 = n1 cos a - n2 sin a,  y2 = n2 cos a + n1 sin a                  fp32
+ *       (the two dimensions rot_kind names for i; the rest of the head: y = n)
+ *   q   bf16 [T][q_heads][dim], k bf16 [T][kv_heads][dim]
+ *   v   bf16 [T][kv_heads][v_dim]; NULL without a cache
+ *   gamma_q, gamma_k  fp32 [dim], each may be NULL;  eps > 0 and finite
+ *   positions  int32 [T];  inv_freq fp32 [rot_dim / 2] (NULL iff rot_dim is 0)
+ *   q_out, k_out  bf16 [T][heads][dim] out (optional, NULL = not written; q_out
+ *                 may be q and k_out k, with its stride)
+ *   cache  pages out (optional): token t's keys y and values v go to place
+ *          slots[t] = page number * page + row of the page; a token whose place
+ *          is outside the cache (negative: a padding row) is not written there.
+ *          Two tokens with one place: either's.
+ *   slots  int64 [T], NULL iff no cache
+ * dim and v_dim multiples of 8 up to 256 (of 32 with an MXFP8 cache), rot_dim a
+ * multiple of 16 up to dim, heads up to 4096 each, T up to 2^25. Rows 16-byte
+ * aligned. */
+k3moe_status k3moe_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                const uint16_t *v, int64_t v_stride, int32_t T, int32_t q_heads,
+                                int32_t kv_heads, int32_t dim, int32_t v_dim, const float *gamma_q,
+                                const float *gamma_k, float eps, const int32_t *positions,
+                                const float *inv_freq, int32_t rot_dim, int32_t rot_kind, uint16_t *q_out,
+                                int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                                const k3moe_pages *cache, const int64_t *slots, void *stream);
+
+/* Attention of packed sequences: sequence b has queries cu_q[b] .. cu_q[b + 1)
+ * and keys cu_k[b] .. cu_k[b + 1). For every query and head
+ *   out = sum_j p_j v_j,  p = softmax over the keys seen of scale * q . k_j,
+ *   lse = log sum_j exp(scale * q . k_j)
+ * causal: query i of n sees the keys j <= i + (number of keys) - n, so the last
+ * query sees every key (n smaller than the number of keys: a later chunk of a
+ * prompt); else all keys of its sequence. A query that sees none: out 0, lse
+ * -inf. What a query does not see has no influence on its result, NaN and
+ * infinities included.
+ *   cu_q, cu_k  int32 [seqs + 1] on the device, ascending; cu_k NULL = cu_q.
+ *               They are held to 0 .. Tq and 0 .. Tk. Rows of out and lse that
+ *               belong to no sequence are left as they were.
+ *   q bf16 [Tq][q_heads][k_dim], k bf16 [Tk][kv_heads][k_dim], v bf16 [Tk][kv_heads][v_dim]
+ *   out bf16 [Tq][q_heads][v_dim], lse fp32 [Tq][q_heads] (optional, NULL = not written)
+ * (k_dim, v_dim): (64, 64), (128, 128) or (192, 128), others
+ * K3MOE_E_UNSUPPORTED_SHAPE; scale > 0 and finite. Rows 16-byte aligned, strides
+ * up to 2^24 elements. Scores and sums are fp32; the weights are rounded to bf16
+ * for their product with the values. */
+k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                             const uint16_t *v, int64_t v_stride, const int32_t *cu_q, const int32_t *cu_k,
+                             int32_t seqs, int32_t Tq, int32_t Tk, int32_t q_heads, int32_t kv_heads,
+                             int32_t k_dim, int32_t v_dim, float scale, int32_t causal, uint16_t *out,
+                             int64_t out_stride, float *lse, void *stream);
+
+/* Attention of drafted tokens over the cache. Sequence b has lens[b] tokens of
+ * context at positions 0 .. lens[b) and n_b drafted ones whose keys and values
+ * the cache holds behind them: the j-th at position lens[b] + j. Drafted token i
+ * sees the whole context and the drafted tokens j whose bit j is set in its word
+ * of `tree` (itself only if its own bit is); tree NULL: j <= i, a chain. One
+ * drafted token per sequence is ordinary decoding. out and lse as in
+ * k3moe_attention.
+ *   pages  int32 [seqs][pages_width]: position p of sequence b lies in row p mod
+ *          page of page pages[b][p / page]. A position behind the table's end, or
+ *          whose page number is outside the cache, is seen by nobody.
+ *   lens   int32 [seqs] (a negative one counts as 0)
+ *   cu_q   int32 [seqs + 1]: drafted tokens cu_q[b] .. cu_q[b + 1) of q, out, lse
+ *          and tree; NULL: Tq / seqs each (then Tq is a multiple of seqs, and
+ *          max_q at least that)
+ *   max_q  1 to 64: the most tokens a sequence has. Tokens behind the first
+ *          max_q of a sequence, and rows of no sequence, are left as they were.
+ *   tree   uint64 [Tq] (optional)
+ *   q bf16 [Tq][q_heads][k_dim], out bf16 [Tq][q_heads][v_dim], lse fp32 [Tq][q_heads] (optional)
+ * (k_dim, v_dim) and alignment as in k3moe_attention. The workspace's size
+ * depends on neither lens nor the number of sequences. */
+k3moe_status k3moe_tree_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t v_dim,
+                                                 int32_t max_q, size_t *bytes);
+k3moe_status k3moe_tree_attention(const uint16_t *q, int64_t q_stride, const k3moe_pages *cache,
+                                  const int32_t *pages, int32_t pages_width, const int32_t *lens,
+                                  const int32_t *cu_q, const uint64_t *tree, int32_t seqs, int32_t Tq,
+                                  int32_t max_q, int32_t q_heads, int32_t kv_heads, int32_t k_dim,
+                                  int32_t v_dim, float scale, uint16_t *out, int64_t out_stride, float *lse,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Log probabilities of T rows of logits (fp32 or bf16 [T][V], as k3moe_linear
+ * writes them):
+ *   lp[t][j]  = log softmax(x[t])[ids[t][j]], j < n_ids    (an id outside 0 .. V: NaN)
+ *   entropy[t] = - sum p log p, in nats
+ *   top_ids[t], top_lp[t]: the k largest logits and their log probabilities,
+ *              largest first, equal ones by their number
+ *   logits  fp32 (logits_f32 = 1) or bf16 (0), rows `stride` elements apart; -inf
+ *           is a token that cannot be drawn. Bases need only their elements'
+ *           alignment; 16-byte aligned rows take wider loads.
+ *   ids int32 [T][n_ids], lp fp32 [T][n_ids]  both or neither (n_ids 0)
+ *   entropy fp32 [T]                          optional
+ *   top_ids int32 [T][k], top_lp fp32 [T][k]  both or neither (k 0); k <= 64, k <= V
+ * A row that is no distribution (a NaN, +inf, or every logit -inf) gives NaN in
+ * lp, entropy and top_lp; its top_ids go by the logits all the same (NaN lowest,
+ * with -inf). V up to 2^24, n_ids up to 4096. A term e^(x - max) is an
+ * fp32 number (below 2^-126: 0), sums are joined in 64 bits. T == 0 does nothing. */
+k3moe_status k3moe_logprobs_workspace_size(int32_t T, int32_t V, int32_t k, size_t *bytes);
+k3moe_status k3moe_logprobs(const void *logits, int32_t logits_f32, int64_t stride, int32_t T, int32_t V,
+                            const int32_t *ids, int32_t n_ids, float *lp, float *entropy, int32_t *top_ids,
+                            float *top_lp, int32_t k, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Frees the handle and its error counter (synchronises the device first).
  * NULL is accepted. */
 void k3moe_layer_destroy(k3moe_layer *layer);

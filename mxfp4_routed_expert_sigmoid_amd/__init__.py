@@ -18,6 +18,7 @@ ABI_VERSION = 3
 ACT_SITU, ACT_SWIGLU = 1, 2
 ADD_NONE, ADD_BF16, ADD_F32 = 0, 1, 2
 OUT_BF16, OUT_F32, OUT_F32_ADD, OUT_MXFP8 = 1, 2, 3, 4
+ROT_HALVES, ROT_PAIRS = 1, 2
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "invalid or incomplete config",
           3: "unsupported shape", 4: "pointer or stride not aligned",
@@ -61,6 +62,11 @@ class CacheStats(ctypes.Structure):
                                                 "evictions", "dropped", "bytes_read")]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("vs", ctypes.c_void_p),
+                ("pages", ctypes.c_int32), ("page", ctypes.c_int32)]
+
+
 _lib = None
 EXPORTS = ("k3moe_layer_create", "k3moe_workspace_size", "k3moe_route", "k3moe_forward",
            "k3moe_route_forward", "k3moe_forward_noalloc", "k3moe_forward_residual", "k3moe_step",
@@ -68,7 +74,9 @@ EXPORTS = ("k3moe_layer_create", "k3moe_workspace_size", "k3moe_route", "k3moe_f
            "k3moe_cache_forward", "k3moe_cache_stats_read", "k3moe_cache_slots", "k3moe_cache_reset", "k3moe_cache_destroy",
            "k3moe_error_count", "k3moe_error_reset", "k3moe_profile_enable",
            "k3moe_profile_read", "k3moe_layer_destroy", "k3moe_status_string",
-           "k3moe_add_norm", "k3moe_linear", "k3moe_glu")
+           "k3moe_add_norm", "k3moe_linear", "k3moe_glu", "k3moe_qk_norm_rope", "k3moe_attention",
+           "k3moe_tree_attention_workspace_size", "k3moe_tree_attention", "k3moe_logprobs_workspace_size",
+           "k3moe_logprobs")
 STAGES = ("router", "topk", "perm", "gateup", "shared_gateup", "down", "combine",
           "latent_in", "latent_out", "prenorm", "cache_plan", "cache_fill", "gateup_tiles",
           "down_tiles")
@@ -134,6 +142,23 @@ def lib():
         L.k3moe_linear.argtypes = [P, P, i32, i32, P, i64, P, i64, i32, P, i64, P, i64, i32, P]
         L.k3moe_glu.restype = st
         L.k3moe_glu.argtypes = [P, P, P, P, i32, i32, P, i64, P, i64, i32, i32, f32, f32, P, i64, P, i64, i32, P]
+        size, sz = ctypes.POINTER(ctypes.c_size_t), ctypes.c_size_t
+        pages = ctypes.POINTER(Pages)
+        L.k3moe_qk_norm_rope.restype = st
+        L.k3moe_qk_norm_rope.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, i32, i32, P, P, f32, P, P, i32, i32,
+                                         P, i64, P, i64, pages, P, P]
+        L.k3moe_attention.restype = st
+        L.k3moe_attention.argtypes = [P, i64, P, i64, P, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, i32, P,
+                                      i64, P, P]
+        L.k3moe_tree_attention_workspace_size.restype = st
+        L.k3moe_tree_attention_workspace_size.argtypes = [i32, i32, i32, i32, size]
+        L.k3moe_tree_attention.restype = st
+        L.k3moe_tree_attention.argtypes = [P, i64, pages, P, i32, P, P, P, i32, i32, i32, i32, i32, i32, i32, f32, P,
+                                           i64, P, P, sz, P]
+        L.k3moe_logprobs_workspace_size.restype = st
+        L.k3moe_logprobs_workspace_size.argtypes = [i32, i32, i32, size]
+        L.k3moe_logprobs.restype = st
+        L.k3moe_logprobs.argtypes = [P, i32, i64, i32, i32, P, i32, P, P, P, P, i32, P, sz, P]
         _lib = L
     return _lib
 
@@ -633,4 +658,301 @@ def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=No
     status = lib().k3moe_glu(gp, gs, up, us, N, K, *tok, T, act, situ_b1, situ_b2, *res, _queue(dev, stream))
     if status:
         raise K3MoeError(status, "k3moe_glu")
+    _changed(written)
+
+
+# ---------------------------------------------------------------------------
+# Attention and what stands around it (k3moe_qk_norm_rope, k3moe_attention,
+# k3moe_tree_attention, k3moe_logprobs): functions over device tensors with the
+# dense operators' rules. Heads are [T][heads][dim] views, rows possibly part of
+# a wider projection; cache pages are [pages][heads][page][dim].
+_BF16_VALUES = (torch.bfloat16, torch.int16, torch.uint16)
+_I32, _I64 = (torch.int32,), (torch.int64,)
+
+
+def _heads(t, rows, heads, dim, name, dev):
+    """Refuse anything but a bf16 [rows][heads][dim] tensor on device number
+    `dev` whose rows are contiguous. Returns its address and row stride."""
+    if t.shape != (rows, heads, dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, heads, dim)}")
+    if t.dtype not in _BF16_VALUES:
+        raise ValueError(f"{name}: {t.dtype}, expected torch.bfloat16")
+    width = heads * dim
+    if rows >> 31 or width >> 31:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, rows and columns are counted in 32 bits")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{dev}" if dev >= 0 else "a GPU"))
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    st, head, unit = t.stride()
+    if (unit != 1 and dim > 1) or (head != dim and heads > 1):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    if rows < 2:
+        return t.data_ptr(), width
+    if st < width:
+        raise ValueError(f"{name}: rows overlap (stride {st}, width {width})")
+    return t.data_ptr(), st
+
+
+def _flat(t, shape, dtypes, name, dev):
+    """The address of a contiguous tensor of this shape and one of these types on device number `dev`."""
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous "
+                         f"{' or '.join(str(d) for d in dtypes)} {tuple(shape)}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{dev}" if dev >= 0 else "a GPU"))
+    return t.data_ptr()
+
+
+def _cache(kc, vc, ks, vs, dim, v_dim, dev):
+    """(Pages, heads) of cache tensors [pages][heads][page][dim], MXFP8 with ks and vs."""
+    if kc.dim() != 4 or vc.dim() != 4:
+        raise ValueError(f"kc, vc: shapes {tuple(kc.shape)} and {tuple(vc.shape)}, expected [pages][heads][page][dim]")
+    n, heads, page = kc.shape[:3]
+    if n >> 31 or page >> 31 or heads >> 31:
+        raise ValueError(f"kc: shape {tuple(kc.shape)}, pages and rows are counted in 32 bits")
+    if (ks is None) != (vs is None):
+        raise ValueError("ks and vs go together")
+    types = _BF16_VALUES if ks is None else _E4M3
+    k = _flat(kc, (n, heads, page, dim), types, "kc", dev)
+    v = _flat(vc, (n, heads, page, v_dim), types, "vc", dev)
+    if ks is None:
+        return Pages(k, v, None, None, n, page), heads
+    if dim % 32 or v_dim % 32:
+        raise ValueError(f"kc, vc: head widths {dim} and {v_dim}, an MXFP8 cache takes multiples of 32")
+    return Pages(k, v, _flat(ks, (n, heads, page, dim // 32), _E8M0, "ks", dev),
+                 _flat(vs, (n, heads, page, v_dim // 32), _E8M0, "vs", dev), n, page), heads
+
+
+def _scratch_ok(workspace, dev):
+    """Refuse a workspace that is no contiguous byte tensor on device number `dev`."""
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
+                                  or workspace.get_device() != dev):
+        raise ValueError(f"workspace: {workspace.dtype} on {workspace.device}, expected contiguous torch.uint8 on cuda:{dev}")
+
+
+def _scratch(workspace, size, device, stream):
+    """Address and bytes of the caller's workspace, or of a new one (256-byte aligned) marked as used on `stream`."""
+    if workspace is None:
+        workspace = torch.empty(size() + 256, dtype=torch.uint8, device=device)
+        if stream is not None and stream != torch.cuda.current_stream(device):
+            workspace.record_stream(stream)
+    base = workspace.data_ptr()
+    off = -base % 256
+    return base + off, max(workspace.numel() - off, 0)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, gamma_q=None, gamma_k=None, eps=1e-6, rot=ROT_HALVES, q_out=None, k_out=None,
+                 v=None, kc=None, vc=None, ks=None, vs=None, slots=None, stream=None):
+    """k3moe_qk_norm_rope: RMS norm of every head of q bf16 [T][Hq][D] and k bf16
+    [T][Hkv][D] (gamma_q, gamma_k fp32 [D], None: no norm), rotation of the first
+    2 * len(inv_freq) dimensions by positions int32 [T] times inv_freq fp32 (None:
+    none), to q_out, k_out (bf16, None: not written; may be q and k). With a cache
+    (kc [pages][Hkv][page][D], vc [pages][Hkv][page][Dv]; bf16, or e4m3 with E8M0
+    bytes ks, vs) the keys and v bf16 [T][Hkv][Dv] go to the places slots int64 [T]
+    (page * page size + row; outside the cache: not written)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q, k: shapes {tuple(q.shape)} and {tuple(k.shape)}, expected [T][heads][dim]")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    dev = q.get_device()
+    qp, qst = _heads(q, T, Hq, D, "q", dev)
+    kp, kst = _heads(k, T, Hkv, D, "k", dev)
+    gqp = None if gamma_q is None else _vec(gamma_q, D, "gamma_q", dev)
+    gkp = None if gamma_k is None else _vec(gamma_k, D, "gamma_k", dev)
+    pp = fp = None
+    R = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError(f"inv_freq: shape {tuple(inv_freq.shape)}, expected [rot_dim / 2]")
+        R = 2 * inv_freq.shape[0]
+        fp = _vec(inv_freq, R // 2, "inv_freq", dev) if R else None
+        pp = _flat(positions, (T,), _I32, "positions", dev) if R else None
+    op = kop = None
+    ost = kost = 0
+    written = ()
+    if q_out is not None:
+        op, ost = _heads(q_out, T, Hq, D, "q_out", dev)
+        written += (q_out,)
+    if k_out is not None:
+        kop, kost = _heads(k_out, T, Hkv, D, "k_out", dev)
+        written += (k_out,)
+    vp = sp = cache = None
+    vst = Dv = 0
+    given = [x is not None for x in (kc, vc, v, slots)]
+    if any(given) or ks is not None or vs is not None:
+        if not all(given):
+            raise ValueError("kc, vc, v and slots go together")
+        if v.dim() != 3:
+            raise ValueError(f"v: shape {tuple(v.shape)}, expected [T][heads][dim]")
+        Dv = v.shape[2]
+        vp, vst = _heads(v, T, Hkv, Dv, "v", dev)
+        cache, heads = _cache(kc, vc, ks, vs, D, Dv, dev)
+        if heads != Hkv:
+            raise ValueError(f"kc: {heads} heads, k has {Hkv}")
+        sp = _flat(slots, (T,), _I64, "slots", dev)
+        written += (kc, vc) if ks is None else (kc, vc, ks, vs)
+    if _grad_enabled():
+        _untracked(written)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return qk_norm_rope(q, k, positions, inv_freq, gamma_q, gamma_k, eps, rot, q_out, k_out, v, kc, vc, ks, vs,
+                                slots, stream)
+    status = lib().k3moe_qk_norm_rope(qp, qst, kp, kst, vp, vst, T, Hq, Hkv, D, Dv, gqp, gkp, eps, pp, fp, R, rot, op, ost,
+                                      kop, kost, cache, sp, _queue(dev, stream))
+    if status:
+        raise K3MoeError(status, "k3moe_qk_norm_rope")
+    _changed(written)
+
+
+def _group(Hq, Hkv):
+    if Hkv == 0 or Hq == 0 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads over {Hkv} key heads")
+
+
+def attention(q, k, v, cu_q, out, cu_k=None, scale=None, causal=True, lse=None, stream=None):
+    """k3moe_attention: out bf16 [Tq][Hq][Dv] of packed sequences. q bf16
+    [Tq][Hq][D], k bf16 [Tk][Hkv][D], v bf16 [Tk][Hkv][Dv]; cu_q int32 [seqs + 1]
+    offsets of the sequences, cu_k those of their keys (None: cu_q); scale None:
+    D ** -0.5; lse fp32 [Tq][Hq] (None: not written)."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v: expected [T][heads][dim]")
+    Tq, Hq, D = q.shape
+    Tk, Hkv, Dv = v.shape
+    dev = q.get_device()
+    qp, qst = _heads(q, Tq, Hq, D, "q", dev)
+    kp, kst = _heads(k, Tk, Hkv, D, "k", dev)
+    vp, vst = _heads(v, Tk, Hkv, Dv, "v", dev)
+    _group(Hq, Hkv)
+    op, ost = _heads(out, Tq, Hq, Dv, "out", dev)
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError(f"cu_q: shape {tuple(cu_q.shape)}, expected [sequences + 1]")
+    cqp = _flat(cu_q, cu_q.shape, _I32, "cu_q", dev)
+    ckp = None if cu_k is None else _flat(cu_k, cu_q.shape, _I32, "cu_k", dev)
+    lp = None if lse is None else _flat(lse, (Tq, Hq), _F32, "lse", dev)
+    written = (out,) if lse is None else (out, lse)
+    if _grad_enabled():
+        _untracked(written)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return attention(q, k, v, cu_q, out, cu_k, scale, causal, lse, stream)
+    status = lib().k3moe_attention(qp, qst, kp, kst, vp, vst, cqp, ckp, cu_q.shape[0] - 1, Tq, Tk, Hq, Hkv, D, Dv,
+                                   D ** -0.5 if scale is None else scale, 1 if causal else 0, op, ost, lp,
+                                   _queue(dev, stream))
+    if status:
+        raise K3MoeError(status, "k3moe_attention")
+    _changed(written)
+
+
+def _tree_bytes(q_heads, kv_heads, v_dim, max_q):
+    n = ctypes.c_size_t()
+    _check(lib().k3moe_tree_attention_workspace_size(q_heads, kv_heads, v_dim, max_q, ctypes.byref(n)),
+           "k3moe_tree_attention_workspace_size")
+    return n.value
+
+
+def tree_attention_workspace(q_heads, kv_heads, v_dim, max_q=1, device=None):
+    """A device byte tensor for ``tree_attention``, whatever the cached lengths and the number of sequences."""
+    return torch.empty(_tree_bytes(q_heads, kv_heads, v_dim, max_q) + 256, dtype=torch.uint8, device=device or "cuda")
+
+
+def tree_attention(q, kc, vc, pages, lens, out, ks=None, vs=None, cu_q=None, max_q=None, tree=None, scale=None, lse=None,
+                   workspace=None, stream=None):
+    """k3moe_tree_attention: out bf16 [Tq][Hq][Dv] of drafted tokens q bf16
+    [Tq][Hq][D] over the cache kc, vc (ks, vs) as in ``qk_norm_rope``. pages int32
+    [seqs][width] are the sequences' pages, lens int32 [seqs] their context; the
+    drafted tokens' keys and values stand behind it. cu_q int32 [seqs + 1] offsets
+    of the sequences' drafted tokens, at most max_q (1 to 64) each; cu_q None: the
+    same number each. tree int64 [Tq]: bit j of a token's word says whether it
+    sees its sequence's j-th drafted token (None: a chain). scale, lse as in
+    ``attention``; workspace from ``tree_attention_workspace`` (None: a new one)."""
+    if q.dim() != 3 or kc.dim() != 4 or vc.dim() != 4 or pages.dim() != 2:
+        raise ValueError("expected q [T][heads][dim], kc and vc [pages][heads][page][dim], pages [sequences][width]")
+    Tq, Hq, D = q.shape
+    Dv = vc.shape[3]
+    B, width = pages.shape
+    dev = q.get_device()
+    qp, qst = _heads(q, Tq, Hq, D, "q", dev)
+    cache, Hkv = _cache(kc, vc, ks, vs, D, Dv, dev)
+    _group(Hq, Hkv)
+    op, ost = _heads(out, Tq, Hq, Dv, "out", dev)
+    if B >> 31 or width >> 31:
+        raise ValueError(f"pages: shape {tuple(pages.shape)}, rows and columns are counted in 32 bits")
+    pp = _flat(pages, (B, width), _I32, "pages", dev)
+    np_ = _flat(lens, (B,), _I32, "lens", dev)
+    cqp = None if cu_q is None else _flat(cu_q, (B + 1,), _I32, "cu_q", dev)
+    if max_q is None:
+        if cu_q is not None:
+            raise ValueError("max_q: with cu_q the most drafted tokens of a sequence must be given")
+        max_q = max(Tq // B, 1) if B else 1
+    tp = None if tree is None else _flat(tree, (Tq,), _I64, "tree", dev)
+    lp = None if lse is None else _flat(lse, (Tq, Hq), _F32, "lse", dev)
+    _scratch_ok(workspace, dev)
+    written = (out,) if lse is None else (out, lse)
+    if _grad_enabled():
+        _untracked(written)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return tree_attention(q, kc, vc, pages, lens, out, ks, vs, cu_q, max_q, tree, scale, lse, workspace, stream)
+    wp, wn = _scratch(workspace, lambda: _tree_bytes(Hq, Hkv, Dv, max_q), q.device, stream)
+    status = lib().k3moe_tree_attention(qp, qst, cache, pp, width, np_, cqp, tp, B, Tq, max_q, Hq, Hkv, D, Dv,
+                                        D ** -0.5 if scale is None else scale, op, ost, lp, wp, wn, _queue(dev, stream))
+    if status:
+        raise K3MoeError(status, "k3moe_tree_attention")
+    _changed(written)
+
+
+def _logprobs_bytes(T, V, k):
+    n = ctypes.c_size_t()
+    _check(lib().k3moe_logprobs_workspace_size(T, V, k, ctypes.byref(n)), "k3moe_logprobs_workspace_size")
+    return n.value
+
+
+def logprobs_workspace(T, V, k=0, device=None):
+    """A device byte tensor for ``logprobs`` on T rows of V logits with k alternatives."""
+    return torch.empty(_logprobs_bytes(T, V, k) + 256, dtype=torch.uint8, device=device or "cuda")
+
+
+def logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=None, workspace=None, stream=None):
+    """k3moe_logprobs: of logits fp32 or bf16 [T][V], lp fp32 [T][M] the log
+    probabilities of the tokens ids int32 [T][M], entropy fp32 [T], top_ids int32
+    [T][k] and top_lp fp32 [T][k] the k (up to 64) likeliest tokens and their log
+    probabilities, each optional; workspace from ``logprobs_workspace`` (None: a
+    new one)."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected [T][V]")
+    T, V = logits.shape
+    dev = logits.get_device()
+    xp, xst = _mat(logits, T, V, _F32 + _BF16, "logits", dev)
+    if (ids is None) != (lp is None) or (top_ids is None) != (top_lp is None):
+        raise ValueError("ids and lp, and top_ids and top_lp, go together")
+    ip = op = ep = tip = tlp = None
+    M = k = 0
+    written = ()
+    if ids is not None:
+        if ids.dim() != 2:
+            raise ValueError(f"ids: shape {tuple(ids.shape)}, expected [T][M]")
+        M = ids.shape[1]
+        ip, op = _flat(ids, (T, M), _I32, "ids", dev), _flat(lp, (T, M), _F32, "lp", dev)
+        written += (lp,)
+    if entropy is not None:
+        ep = _flat(entropy, (T,), _F32, "entropy", dev)
+        written += (entropy,)
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError(f"top_ids: shape {tuple(top_ids.shape)}, expected [T][k]")
+        k = top_ids.shape[1]
+        tip, tlp = _flat(top_ids, (T, k), _I32, "top_ids", dev), _flat(top_lp, (T, k), _F32, "top_lp", dev)
+        written += (top_ids, top_lp)
+    _scratch_ok(workspace, dev)
+    if _grad_enabled():
+        _untracked(written)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return logprobs(logits, ids, lp, entropy, top_ids, top_lp, workspace, stream)
+    wp, wn = _scratch(workspace, lambda: _logprobs_bytes(T, V, k), logits.device, stream)
+    status = lib().k3moe_logprobs(xp, 1 if logits.dtype == torch.float32 else 0, xst, T, V, ip, M, op, ep, tip, tlp, k, wp,
+                                  wn, _queue(dev, stream))
+    if status:
+        raise K3MoeError(status, "k3moe_logprobs")
     _changed(written)

@@ -14,9 +14,10 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libk3moe.so")
 SOURCES = [os.path.join(CSRC, f) for f in (
     "k3moe_api.cpp", "k3moe_kernels.hip", "k3moe_decode.hip", "k3moe_grouped.hip", "k3moe_stream.hip",
-    "k3moe_latent.hip", "k3moe_step.hip", "k3moe_cache.hip", "k3moe_norm.hip", "k3moe_linear.hip")]
+    "k3moe_latent.hip", "k3moe_step.hip", "k3moe_cache.hip", "k3moe_norm.hip", "k3moe_linear.hip",
+    "k3moe_heads.hip", "k3moe_attention.hip", "k3moe_tree.hip", "k3moe_logprobs.hip")]
 HEADERS = [os.path.join(CSRC, "k3moe_internal.h"), os.path.join(CSRC, "k3moe_device.h"),
-           os.path.join(CSRC, "k3moe_mx8.h"),
+           os.path.join(CSRC, "k3moe_mx8.h"), os.path.join(CSRC, "k3moe_attn.h"),
            os.path.join(ROOT, "include", "k3moe.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

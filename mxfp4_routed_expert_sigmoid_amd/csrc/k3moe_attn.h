@@ -1,0 +1,249 @@
+// What the attention kernels share: the inner loop over tiles of 64 keys for a
+// wave's 32 rows of queries, and the small pieces around it.
+//
+// Scores are computed transposed, S^T = K Q^T (32x32x16 MFMAs, keys on the
+// rows), so that a lane holds scores of one query only: the running maximum
+// and sum of a row stay in its two lanes (l and l ^ 32), and the registers
+// that hold P^T are, in the order they have, the B operand of O^T = V^T P^T.
+// Its A operand V^T comes from the row-major V tile through the LDS transpose
+// reads. The order of the 16 keys of one product is free as long as both
+// operands agree; it is the score layout's: slot 8h + j of lane half h is key
+// 4h + j for j < 4 and key 8 + 4h + j - 4 behind that.
+//
+// P is rounded to bf16 for the second product (2^-9 of each weight, whose
+// errors average out over the keys); the sums l are taken of the fp32 values.
+#pragma once
+
+#include "k3moe_device.h"
+#include "k3moe_internal.h"
+
+namespace k3moe {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+constexpr int kAtKeys = 64;                // keys per tile
+constexpr int kAtRows = 32;                // rows of queries per wave
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// The running maximum is raised only when a tile exceeds it by more than this (in powers of two): the weights then
+// stay below 2^8 of what they would be, which neither fp32 sums nor the bf16 weights, rounded relatively, notice.
+constexpr float kAtSlack = 8.0f;
+// An offset behind every tile's bytes (63 rows of 2^24 elements at most): read as zeros.
+constexpr uint32_t kAtOut = 0xff000000u;
+
+__device__ __forceinline__ uint32_t at_bf16(float f) { return f != f ? 0x7fc0u : bf16_rne_u32(f); }
+
+// Two fp32 -> packed bf16, to nearest even.
+__device__ __forceinline__ uint32_t at_pack(float a, float b)
+{
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const bf2 p = __builtin_convertvector((f2){a, b}, bf2);
+    uint32_t r;
+    __builtin_memcpy(&r, &p, 4);
+    return r;
+}
+
+// Position of 16-byte slot s of row r in a tile of D-wide bf16 rows. K tiles are read one slot of 32 rows at a
+// time: 16 neighbouring rows touch every bank once. V tiles are read 64 bytes of four neighbouring rows at a time.
+template <int D>
+__device__ __forceinline__ int k_slot(int r, int s)
+{
+    return r * (D / 8) + (D == 128 ? s ^ (r & 15) : s ^ ((r >> 1) & 7));
+}
+template <int D>
+__device__ __forceinline__ int v_slot(int r, int s)
+{
+    static_assert(D == 64 || D == 128, "value widths");
+    return r * (D / 8) + (D == 128 ? s ^ ((r & 3) << 2) : s ^ (((r >> 1) & 1) << 2));
+}
+
+__device__ __forceinline__ v16f mfma32(const bf8 &a, const bf8 &b, v16f c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float swap_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
+
+// LDS transpose read: the 16 lanes of a quarter wave read 4 rows of 16 values (lane i: 4 values of row i / 4), and
+// lane i gets column i of the four rows.
+__device__ __forceinline__ s4 lds_tr(const uint8_t *at)
+{
+    typedef __attribute__((address_space(3))) s4 lds_s4;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)at);
+}
+
+// The lowest n bits (n <= 0: none, n >= 64: all).
+__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; }
+
+// Waits for this wave's loads and LDS operations, then for the block.
+__device__ __forceinline__ void at_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A wave's 32 rows: the queries as B operands, running maximum (of the raw scores) and sum, O^T.
+template <int DK, int DV>
+struct AttRows {
+    bf8 q[DK / 16];
+    v16f o[DV / 32];
+    float m, l;      // m: the same in both lanes of a row; l: each lane's own keys
+    __device__ __forceinline__ void clear()
+    {
+        m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+    }
+};
+
+// Whether a V tile in LDS holds a value that is not finite, for the whole wave.
+template <int DV>
+__device__ __forceinline__ bool v_not_finite(const uint8_t *vt)
+{
+    const int lane = threadIdx.x & 63;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kAtKeys * DV * 2 / 1024; ++i) {
+        const u4 w = *reinterpret_cast<const u4 *>(vt + 1024 * i + 16 * lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            bad |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+    }
+    return __ballot(bad) != 0;
+}
+
+// Zeros in the place of values that are not finite.
+__device__ __forceinline__ bf8 only_finite(const bf8 &a)
+{
+    u4 w;
+    __builtin_memcpy(&w, &a, 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = (w[i] & 0x7f80u) == 0x7f80u ? w[i] & 0xffff0000u : w[i];
+        w[i] = (w[i] & 0x7f800000u) == 0x7f800000u ? w[i] & 0xffffu : w[i];
+    }
+    return as_bf8(w);
+}
+
+// Keeps the compiler from holding what follows from v in registers across the loop over tiles (a tile's addresses
+// are a few operations on one register, or fifty registers that the accumulators need).
+__device__ __forceinline__ uint32_t fresh(uint32_t v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// One tile of 64 keys. kt, vt: the tiles in LDS; c: scale * log2(e). MASKED: bit j of `seen`
+// says whether this lane's row sees key j of the tile; what it does not see takes no part, whatever its key and value
+// hold.
+template <bool MASKED, int DK, int DV>
+__device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, const uint8_t *kt, const uint8_t *vt, float c, uint64_t seen)
+{
+    const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
+    // k_slot(32 t + l32, 2 k + h) = row part + (slot of k = 0, exchanged with 2 k), v_slot(row, slot) likewise
+    const uint32_t krow = fresh((uint32_t)(l32 * DK * 2)), kx = fresh(16u * (uint32_t)(k_slot<DK>(l32, h) - l32 * (DK / 8)));
+    v16f s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+            const u4 a = *reinterpret_cast<const u4 *>(kt + (krow + (kx ^ (32u * k))) + 64 * t * DK);
+            s[t] = mfma32(as_bf8(a), r.q[k], s[t]);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // or the fragments of both halves are held at once
+    }
+    if constexpr (MASKED) {
+        const uint64_t mine = seen >> (4 * h);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[t][i] = (uint32_t)(mine >> (32 * t)) & (1u << (8 * (i >> 2) + (i & 3))) ? s[t][i] : -INFINITY;
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
+    mx = swap_max(mx);
+    // (mx - m) is NaN where both are -inf: nothing to raise
+    if (__ballot((mx - r.m) * c > kAtSlack)) {
+        const float mn = fmaxf(r.m, mx);
+        const float a = r.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.m - mn) * c);
+        r.m = mn, r.l *= a;
+#pragma unroll
+        for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r.o[d][i] *= a;
+    }
+    const float mc = r.m == -INFINITY ? 0.0f : r.m * c;
+    bf8 p[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -mc));
+            r.l += s[t][i];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            p[2 * t + j] = as_bf8(u4{at_pack(s[t][8 * j], s[t][8 * j + 1]), at_pack(s[t][8 * j + 2], s[t][8 * j + 3]),
+                                     at_pack(s[t][8 * j + 4], s[t][8 * j + 5]), at_pack(s[t][8 * j + 6], s[t][8 * j + 7])});
+    }
+    // A weight of zero does not hide an infinity or a NaN in a product: where the tile holds one, the products are
+    // taken without such values, and the rows that see them get them afterwards, one by one.
+    bool bad = false;
+    if constexpr (MASKED) bad = v_not_finite<DV>(vt);
+    const int vr = 4 * h + ((lane & 15) >> 2), vc = (lane & 16) + 4 * (lane & 3);   // row and column of k = d = 0
+    const uint32_t vrow = fresh((uint32_t)(vr * DV * 2 + 2 * vc)), vx = fresh(16u * (uint32_t)(v_slot<DV>(vr, 0) - vr * (DV / 8)));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int d = 0; d < DV / 32; ++d) {
+            const uint8_t *at = vt + (vrow + (vx ^ (64u * d))) + 32 * k * DV;
+            const s4 a0 = lds_tr(at), a1 = lds_tr(at + 16 * DV);
+            bf8 a;
+            __builtin_memcpy(&a, &a0, 8);
+            __builtin_memcpy(reinterpret_cast<char *>(&a) + 8, &a1, 8);
+            if constexpr (MASKED)
+                if (bad) a = only_finite(a);
+            r.o[d] = mfma32(a, p[k], r.o[d]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (MASKED) {
+        if (!bad) return;
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j) {
+            float own = s[0][0];
+#pragma unroll
+            for (int i = 1; i < 32; ++i) own = j == i ? s[i >> 4][i & 15] : own;
+            own = bf16f(at_bf16(own));
+            const float other = __shfl_xor(own, 32);
+#pragma unroll 1
+            for (int hh = 0; hh < 2; ++hh) {
+                const int key = 32 * (j >> 4) + 8 * ((j & 15) >> 2) + 4 * hh + (j & 3);
+                const float w = hh == h ? own : other;
+                const bool sees = seen >> key & 1;
+#pragma unroll
+                for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const int col = 32 * d + 2 * i + 4 * h;
+                        const uint2 v = *reinterpret_cast<const uint2 *>(vt + 16 * v_slot<DV>(key, col >> 3) + 2 * (col & 7));
+                        const float f[4] = {bf16f(v.x & 0xffffu), bf16f(v.x >> 16), bf16f(v.y & 0xffffu), bf16f(v.y >> 16)};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            r.o[d][i + e] = sees && !(fabsf(f[e]) < INFINITY) ? fmaf(w, f[e], r.o[d][i + e]) : r.o[d][i + e];
+                    }
+            }
+        }
+    }
+}
+
+}  // namespace k3moe
