@@ -13,6 +13,7 @@ namespace k3moe {
 namespace {
 
 constexpr int kPrWaves = 4, kPrRows = kPrWaves * kAtRows;
+constexpr unsigned kPrCus = 256;
 
 struct PromptParams {
     const uint16_t *q, *k, *v;
@@ -25,34 +26,54 @@ struct PromptParams {
 };
 
 #ifdef __HIP_DEVICE_COMPILE__
-typedef __attribute__((address_space(3))) void lds_void;
+// Direct loads of 64 rows of one head into an LDS tile laid out by k_slot or v_slot; every wave loads 16 rows.
+// The places that a load fills are 1 KB in order, so each lane fetches the slot that belongs into its own. With row =
+// 16 wave + 8 a + r the exchange of slots is the same for a = 0 and 1 but for one bit of the slot's number (k_slot), or at all
+// (v_slot); so a load's offset is a lane constant, exchanged, and a wave constant.
+template <int D, bool K>
+struct TileStage {
+    static constexpr int SL = D / 8, L = D / 32;          // slots per row, loads of a wave
+    static constexpr int J = D == 192 ? 3 : L / 2;        // loads of 8 rows
+    uint32_t x[J], at[J];                                  // 16 * the slot, bytes of the row r
 
-// Direct loads of rows row0 .. row0 + 63 of one head into an LDS tile, the places by `slot`. src: the head's first
-// row of the sequence; rows from `end` on read as zeros.
-template <int D, class Slot>
-__device__ __forceinline__ void stage(const uint16_t *src, int64_t stride, int row0, int end, const uint8_t *lds, Slot slot)
-{
-    constexpr int SL = D / 8, N = kAtKeys * SL / (64 * kPrWaves);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t *>(src + (int64_t)row0 * stride), 0, kAtOut, 0x00020000);
+    __device__ __forceinline__ static int row(int j) { return (64 * j + (int)(threadIdx.x & 63)) / SL; }
+    int wave;
+
+    __device__ __forceinline__ void init(int64_t stride, int w)
+    {
+        wave = w;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = (wave * N + i) * 64 + lane, row = at / SL;   // place at holds slot s of row: slot(row, s) == at
-        const int s = slot(row, at % SL) - row * SL;                 // (the exchange of slots is its own inverse)
-        const uint32_t o = row0 + row < end ? (uint32_t)row * (uint32_t)stride * 2u + 16u * s : kAtOut;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + (wave * N + i) * 1024), 16, (int)o, 0, 0, 0);
+        for (int j = 0; j < J; ++j) {
+            const int r = row(j), pos = (64 * j + (int)(threadIdx.x & 63)) % SL;
+            x[j] = 16u * (uint32_t)((K ? k_slot<D>(r, pos) : v_slot<D == 192 ? 128 : D>(r, pos)) - r * SL);
+            at[j] = (uint32_t)r * (uint32_t)stride * 2u;
+        }
     }
-}
+    // rows row0 .. row0 + 63 behind src (the head's first row of the sequence); those from `end` on read as zeros
+    __device__ __forceinline__ void load(const uint16_t *src, int64_t stride, int row0, int end, const uint8_t *lds) const
+    {
+        const bool whole = row0 + kAtKeys <= end;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int a = i / J, j = i % J, base = 16 * wave + 8 * a;
+            uint32_t o = (x[j] ^ (K ? (D == 128 ? 128u : 64u) * a : 0u)) + at[j];
+            if (!whole) o = row0 + base + row(j) < end ? o : kAtOut;
+            lds_load16(src + (int64_t)row0 * stride, o, (uint32_t)base * (uint32_t)stride * 2u, lds + (wave * L + i) * 1024);
+        }
+    }
+};
 #endif
 
-template <int DK, int DV>
-__global__ __launch_bounds__(64 * kPrWaves, 2) void k_attention(PromptParams p)
+// SPLIT: four more waves take the second half of the keys, with buffers of their own.
+template <int DK, int DV, bool SPLIT>
+__global__ __launch_bounds__(64 * kPrWaves * (SPLIT ? 2 : 1), 2) void k_attention(PromptParams p)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    constexpr int KB = kAtKeys * DK * 2, BUF = kAtKeys * (DK + DV) * 2;
+    constexpr int KB = kAtKeys * DK * 2, VB = kAtKeys * DV * 2;
     extern __shared__ __align__(16) uint8_t lds[];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, l32 = lane & 31;
+    const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kPrWaves;
+    const int part = SPLIT ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kPrWaves : 0;
     const int head = blockIdx.x % p.Hq;
     int tile = blockIdx.x / p.Hq;
 
@@ -77,7 +98,7 @@ __global__ __launch_bounds__(64 * kPrWaves, 2) void k_attention(PromptParams p)
             b = b0 + at;
             q0 = __builtin_amdgcn_readlane(lo, at);
             n = __builtin_amdgcn_readlane(hi, at) - q0;
-            tile = __builtin_amdgcn_readlane(mine, at) - 1 - (tile - __builtin_amdgcn_readlane(upto - mine, at));   // the longest first
+            tile = __builtin_amdgcn_readlane(upto, at) - 1 - tile;   // the longest first
         } else {
             tile -= __builtin_amdgcn_readlane(upto, 63);
         }
@@ -101,26 +122,74 @@ __global__ __launch_bounds__(64 * kPrWaves, 2) void k_attention(PromptParams p)
     const int wsee = wfirst >= n ? 0 : p.causal ? wlast + 1 + N - n : N;
     const int wall = wfirst >= n ? 0 : p.causal ? wfirst + 1 + N - n : N;      // every row of the wave sees these
     const int bsee = p.causal ? min(kPrRows * (tile + 1), n) + N - n : N;
-    const int tiles = (max(bsee, 0) + kAtKeys - 1) / kAtKeys;
+    const int all = (max(bsee, 0) + kAtKeys - 1) / kAtKeys, steps = SPLIT ? (all + 1) / 2 : all;
+    const int t0 = part * steps, t1 = min(t0 + steps, all);                    // this part's tiles
 
     const int kvh = head / p.group;
     const uint16_t *kp = p.k + (int64_t)k0 * p.ks + (int64_t)kvh * DK, *vp = p.v + (int64_t)k0 * p.vs + (int64_t)kvh * DV;
-    auto load = [&](int t, int buf) {
-        stage<DK>(kp, p.ks, t * kAtKeys, N, lds + buf * BUF, k_slot<DK>);
-        stage<DV>(vp, p.vs, t * kAtKeys, N, lds + buf * BUF + KB, v_slot<DV>);
-    };
+    // Keys run a tile ahead of the values: tile t's scores are computed beside the weights of tile t - 1. i counts a
+    // part's tiles.
+    const uint8_t *buf = lds + part * 2 * (KB + VB);
+    TileStage<DK, true> sk;
+    TileStage<DV, false> sv;
+    sk.init(p.ks, wave), sv.init(p.vs, wave);
+    auto ktile = [&](int i) { return buf + (i & 1) * KB; };
+    auto vtile = [&](int i) { return buf + 2 * KB + (i & 1) * VB; };
+    auto load_k = [&](int i) { if (t0 + i < t1) sk.load(kp, p.ks, (t0 + i) * kAtKeys, N, ktile(i)); };
+    auto load_v = [&](int i) { if (t0 + i < t1) sv.load(vp, p.vs, (t0 + i) * kAtKeys, N, vtile(i)); };
     const float c = p.scale * kLog2e;
-    if (tiles > 0) load(0, 0);
-    for (int t = 0; t < tiles; ++t) {
+    if (steps > 0) {
+        load_k(0), load_k(1), load_v(0);
         at_barrier();
-        const int buf = t & 1, first = t * kAtKeys;
-        if (t + 1 < tiles) load(t + 1, buf ^ 1);
-        const uint8_t *kt = lds + buf * BUF;
-        if (first + kAtKeys <= wall) att_tile<false>(r, kt, kt + KB, c, ~0ull);
-        else if (first < wsee) att_tile<true>(r, kt, kt + KB, c, low_bits(see - first));
+        v16f s[2];
+        att_scores(s, r, ktile(0));
+        // every wave passes the same number of barriers, in whichever of the two loops
+        const int pairs = max(min(wall / kAtKeys, t1) - t0, 0) / 2;
+        int i = 0;
+        float mx = pairs > 0 ? att_max(s) : 0.0f;
+        for (; i < 2 * pairs; i += 2) {
+            v16f o[2];
+            at_barrier();
+            load_k(i + 2), load_v(i + 1);
+            att_tile(r, s, mx, o, buf + KB, vtile(0), c);
+            at_barrier();
+            load_k(i + 3), load_v(i + 2);
+            att_tile(r, o, mx, s, buf, vtile(1), c);
+        }
+        for (; i < steps; ++i) {
+            at_barrier();
+            load_k(i + 2), load_v(i + 1);
+            const int first = (t0 + i) * kAtKeys;
+            if (t0 + i < t1 && first < wsee) att_tile_masked(r, s, ktile(i + 1), vtile(i), c, low_bits(see - first));
+        }
     }
 
-    const float l = r.l + __shfl_xor(r.l, 32), inv = l == 0.0f ? 0.0f : 1.0f / l;
+    float l = r.l + __shfl_xor(r.l, 32);
+    if constexpr (SPLIT) {
+        // the second half's rows join the first's through LDS, in the lanes' own order
+        at_barrier();
+        float *x = reinterpret_cast<float *>(lds) + wave * 64 * (16 * (DV / 32) + 2) + lane;
+        if (part == 1) {
+            x[0] = r.m, x[64] = l;
+#pragma unroll
+            for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[64 * (2 + 16 * d + e)] = r.o[d][e];
+        }
+        at_barrier();
+        if (part == 1) return;
+        const float m1 = x[0], mn = fmaxf(r.m, m1);
+        const float f0 = r.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.m - mn) * c);
+        const float f1 = m1 == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m1 - mn) * c);
+        // (a part whose scores were all -inf has neither sum nor values; one with NaN has, whatever its maximum)
+        l = (r.m == -INFINITY ? l : l * f0) + (m1 == -INFINITY ? x[64] : x[64] * f1);
+        r.m = mn;
+#pragma unroll
+        for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r.o[d][e] = r.o[d][e] * f0 + x[64 * (2 + 16 * d + e)] * f1;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if (!have) return;
     if (p.lse && h == 0)
         p.lse[(int64_t)(q0 + row) * p.Hq + head] = l == 0.0f ? -INFINITY : fmaf(r.m, c, __log2f(l)) * kLn2;
@@ -135,15 +204,23 @@ __global__ __launch_bounds__(64 * kPrWaves, 2) void k_attention(PromptParams p)
 #endif
 }
 
+template <int DK, int DV, bool SPLIT>
+k3moe_status launch(const PromptParams &p, unsigned grid, hipStream_t s)
+{
+    constexpr int lds = 2 * kAtKeys * (DK + DV) * 2 * (SPLIT ? 2 : 1);
+    static_assert(!SPLIT || lds >= kPrWaves * 64 * (DV / 2 + 2) * 4, "the halves' join fits the tiles");
+    static const hipError_t allowed =
+        hipFuncSetAttribute(reinterpret_cast<const void *>(k_attention<DK, DV, SPLIT>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (allowed != hipSuccess) return K3MOE_E_HIP;
+    k_attention<DK, DV, SPLIT><<<grid, 64 * kPrWaves * (SPLIT ? 2 : 1), lds, s>>>(p);
+    return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
+}
+
 template <int DK, int DV>
 k3moe_status launch(const PromptParams &p, unsigned grid, hipStream_t s)
 {
-    constexpr int lds = 2 * kAtKeys * (DK + DV) * 2;
-    static const hipError_t allowed =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(k_attention<DK, DV>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (allowed != hipSuccess) return K3MOE_E_HIP;
-    k_attention<DK, DV><<<grid, 64 * kPrWaves, lds, s>>>(p);
-    return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
+    // no more tiles than CUs: a CU takes the waves of two blocks, so a tile gets them all
+    return grid <= kPrCus ? launch<DK, DV, true>(p, grid, s) : launch<DK, DV, false>(p, grid, s);
 }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }

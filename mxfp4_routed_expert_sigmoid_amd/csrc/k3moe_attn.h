@@ -62,7 +62,16 @@ __device__ __forceinline__ v16f mfma32(const bf8 &a, const bf8 &b, v16f c)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ float swap_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
+// The maximum of lanes l and l ^ 32.
+__device__ __forceinline__ float swap_max(float v)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#else
+    return v;
+#endif
+}
 
 // LDS transpose read: the 16 lanes of a quarter wave read 4 rows of 16 values (lane i: 4 values of row i / 4), and
 // lane i gets column i of the four rows.
@@ -74,6 +83,23 @@ __device__ __forceinline__ s4 lds_tr(const uint8_t *at)
 
 // The lowest n bits (n <= 0: none, n >= 64: all).
 __device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; }
+
+#ifdef __HIP_DEVICE_COMPILE__
+// 16 bytes per lane from a buffer into LDS at `lds` (the wave's first byte) on, in the lanes' order. Written as an
+// instruction: of the builtin the compiler believes that it may write what the transpose reads read, and waits for every
+// load in flight in front of them. at_barrier() waits for these loads.
+__device__ __forceinline__ void lds_load16(const void *base, uint32_t offset, uint32_t soffset, const uint8_t *lds)
+{
+    typedef int v4i __attribute__((ext_vector_type(4)));
+    const uint64_t a = (uint64_t)base;
+    const v4i rsrc = {__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                      __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)), (int)kAtOut, 0x00020000};
+    const uint32_t at = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(offset), "s"(rsrc),
+                 "s"(__builtin_amdgcn_readfirstlane((int)soffset))
+                 : "memory");   // m0 is no register that the compiler keeps anything in here
+}
+#endif
 
 // Waits for this wave's loads and LDS operations, then for the block.
 __device__ __forceinline__ void at_barrier()
@@ -103,16 +129,21 @@ struct AttRows {
 template <int DV>
 __device__ __forceinline__ bool v_not_finite(const uint8_t *vt)
 {
+    typedef unsigned short h2 __attribute__((ext_vector_type(2)));
     const int lane = threadIdx.x & 63;
-    bool bad = false;
+    h2 most = h2{0, 0};
 #pragma unroll
     for (int i = 0; i < kAtKeys * DV * 2 / 1024; ++i) {
         const u4 w = *reinterpret_cast<const u4 *>(vt + 1024 * i + 16 * lane);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            bad |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t e = w[j] & 0x7f807f80u;   // the exponents
+            h2 x;
+            __builtin_memcpy(&x, &e, 4);
+            most = __builtin_elementwise_max(most, x);
+        }
     }
-    return __ballot(bad) != 0;
+    return __ballot(most[0] == 0x7f80u || most[1] == 0x7f80u) != 0;
 }
 
 // Zeros in the place of values that are not finite.
@@ -136,16 +167,15 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v)
     return v;
 }
 
-// One tile of 64 keys. kt, vt: the tiles in LDS; c: scale * log2(e). MASKED: bit j of `seen`
-// says whether this lane's row sees key j of the tile; what it does not see takes no part, whatever its key and value
-// hold.
-template <bool MASKED, int DK, int DV>
-__device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, const uint8_t *kt, const uint8_t *vt, float c, uint64_t seen)
+// The parts of a tile's work. c: scale * log2(e).
+//
+// Scores of 64 keys: element i of s[t] is key 32 t + 8 (i / 4) + 4 h + i % 4.
+template <int DK, int DV>
+__device__ __forceinline__ void att_scores(v16f (&s)[2], const AttRows<DK, DV> &r, const uint8_t *kt)
 {
     const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
-    // k_slot(32 t + l32, 2 k + h) = row part + (slot of k = 0, exchanged with 2 k), v_slot(row, slot) likewise
+    // k_slot(32 t + l32, 2 k + h) = row part + (slot of k = 0, exchanged with 2 k)
     const uint32_t krow = fresh((uint32_t)(l32 * DK * 2)), kx = fresh(16u * (uint32_t)(k_slot<DK>(l32, h) - l32 * (DK / 8)));
-    v16f s[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -155,22 +185,34 @@ __device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, const uint8_t *kt, 
             const u4 a = *reinterpret_cast<const u4 *>(kt + (krow + (kx ^ (32u * k))) + 64 * t * DK);
             s[t] = mfma32(as_bf8(a), r.q[k], s[t]);
         }
-        __builtin_amdgcn_sched_barrier(0);   // or the fragments of both halves are held at once
     }
-    if constexpr (MASKED) {
-        const uint64_t mine = seen >> (4 * h);
+}
+
+// -inf for the keys whose bits are not in `seen`.
+__device__ __forceinline__ void att_mask(v16f (&s)[2], uint64_t seen)
+{
+    const uint64_t mine = seen >> (4 * ((threadIdx.x & 63) >> 5));
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[t][i] = (uint32_t)(mine >> (32 * t)) & (1u << (8 * (i >> 2) + (i & 3))) ? s[t][i] : -INFINITY;
-    }
+        for (int i = 0; i < 16; ++i)
+            s[t][i] = (uint32_t)(mine >> (32 * t)) & (1u << (8 * (i >> 2) + (i & 3))) ? s[t][i] : -INFINITY;
+}
+
+__device__ __forceinline__ float att_max(const v16f (&s)[2])
+{
     float mx = s[0][0];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
-    mx = swap_max(mx);
+    return swap_max(mx);
+}
+
+// Raises the running maximum where a score exceeds it by the slack.
+template <int DK, int DV>
+__device__ __forceinline__ void att_raise(AttRows<DK, DV> &r, float mx, float c)
+{
     // (mx - m) is NaN where both are -inf: nothing to raise
     if (__ballot((mx - r.m) * c > kAtSlack)) {
         const float mn = fmaxf(r.m, mx);
@@ -181,8 +223,13 @@ __device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, const uint8_t *kt, 
 #pragma unroll
             for (int i = 0; i < 16; ++i) r.o[d][i] *= a;
     }
+}
+
+// Scores to weights, their sum, and the weights as B operands of the four products with 16 values.
+template <int DK, int DV>
+__device__ __forceinline__ void att_weights(bf8 (&p)[4], AttRows<DK, DV> &r, v16f (&s)[2], float c)
+{
     const float mc = r.m == -INFINITY ? 0.0f : r.m * c;
-    bf8 p[4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -195,14 +242,17 @@ __device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, const uint8_t *kt, 
             p[2 * t + j] = as_bf8(u4{at_pack(s[t][8 * j], s[t][8 * j + 1]), at_pack(s[t][8 * j + 2], s[t][8 * j + 3]),
                                      at_pack(s[t][8 * j + 4], s[t][8 * j + 5]), at_pack(s[t][8 * j + 6], s[t][8 * j + 7])});
     }
-    // A weight of zero does not hide an infinity or a NaN in a product: where the tile holds one, the products are
-    // taken without such values, and the rows that see them get them afterwards, one by one.
-    bool bad = false;
-    if constexpr (MASKED) bad = v_not_finite<DV>(vt);
+}
+
+// O^T += V^T P^T; FINITE: without the values that are not finite.
+template <bool FINITE, int DK, int DV>
+__device__ __forceinline__ void att_values(AttRows<DK, DV> &r, const bf8 (&p)[4], const uint8_t *vt)
+{
+    const int lane = threadIdx.x & 63, h = lane >> 5;
     const int vr = 4 * h + ((lane & 15) >> 2), vc = (lane & 16) + 4 * (lane & 3);   // row and column of k = d = 0
     const uint32_t vrow = fresh((uint32_t)(vr * DV * 2 + 2 * vc)), vx = fresh(16u * (uint32_t)(v_slot<DV>(vr, 0) - vr * (DV / 8)));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int d = 0; d < DV / 32; ++d) {
             const uint8_t *at = vt + (vrow + (vx ^ (64u * d))) + 32 * k * DV;
@@ -210,40 +260,134 @@ __device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, const uint8_t *kt, 
             bf8 a;
             __builtin_memcpy(&a, &a0, 8);
             __builtin_memcpy(reinterpret_cast<char *>(&a) + 8, &a1, 8);
-            if constexpr (MASKED)
-                if (bad) a = only_finite(a);
+            if constexpr (FINITE) a = only_finite(a);
             r.o[d] = mfma32(a, p[k], r.o[d]);
         }
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (MASKED) {
-        if (!bad) return;
+}
+
+// A weight of zero does not hide an infinity or a NaN in a product. Where a tile that not every row sees holds one, the
+// products are taken without such values (att_values<true>), and this adds them to the rows that see them, one by one.
+// s: the weights.
+template <int DK, int DV>
+__device__ __forceinline__ void att_not_finite(AttRows<DK, DV> &r, const v16f (&s)[2], const uint8_t *vt, uint64_t seen)
+{
+    const int lane = threadIdx.x & 63, h = lane >> 5;
 #pragma unroll 1
-        for (int j = 0; j < 32; ++j) {
-            float own = s[0][0];
+    for (int j = 0; j < 32; ++j) {
+        float own = s[0][0];
 #pragma unroll
-            for (int i = 1; i < 32; ++i) own = j == i ? s[i >> 4][i & 15] : own;
-            own = bf16f(at_bf16(own));
-            const float other = __shfl_xor(own, 32);
+        for (int i = 1; i < 32; ++i) own = j == i ? s[i >> 4][i & 15] : own;
+        own = bf16f(at_bf16(own));
+        const float other = __shfl_xor(own, 32);
 #pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-                const int key = 32 * (j >> 4) + 8 * ((j & 15) >> 2) + 4 * hh + (j & 3);
-                const float w = hh == h ? own : other;
-                const bool sees = seen >> key & 1;
+        for (int hh = 0; hh < 2; ++hh) {
+            const int key = 32 * (j >> 4) + 8 * ((j & 15) >> 2) + 4 * hh + (j & 3);
+            const float w = hh == h ? own : other;
+            const bool sees = seen >> key & 1;
 #pragma unroll
-                for (int d = 0; d < DV / 32; ++d)
+            for (int d = 0; d < DV / 32; ++d)
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const int col = 32 * d + 2 * i + 4 * h;
-                        const uint2 v = *reinterpret_cast<const uint2 *>(vt + 16 * v_slot<DV>(key, col >> 3) + 2 * (col & 7));
-                        const float f[4] = {bf16f(v.x & 0xffffu), bf16f(v.x >> 16), bf16f(v.y & 0xffffu), bf16f(v.y >> 16)};
+                for (int i = 0; i < 16; i += 4) {
+                    const int col = 32 * d + 2 * i + 4 * h;
+                    const uint2 v = *reinterpret_cast<const uint2 *>(vt + 16 * v_slot<DV>(key, col >> 3) + 2 * (col & 7));
+                    const float f[4] = {bf16f(v.x & 0xffffu), bf16f(v.x >> 16), bf16f(v.y & 0xffffu), bf16f(v.y >> 16)};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            r.o[d][i + e] = sees && !(fabsf(f[e]) < INFINITY) ? fmaf(w, f[e], r.o[d][i + e]) : r.o[d][i + e];
-                    }
-            }
+                    for (int e = 0; e < 4; ++e)
+                        r.o[d][i + e] = sees && !(fabsf(f[e]) < INFINITY) ? fmaf(w, f[e], r.o[d][i + e]) : r.o[d][i + e];
+                }
         }
     }
+}
+
+// One tile whose scores s are there with their maximum mx, on a wave's rows, and the scores of the next tile (nk: its
+// keys) with theirs. Every row sees the whole tile. The products of the next scores, which do not depend on this tile's
+// weights, carry the exponentials in their shadow, and the products with the values the next maximum; fragments are read
+// some steps ahead. The steps are kept in this order: left to itself the compiler takes all exponentials first, then the
+// products.
+template <int DK, int DV>
+__device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, v16f (&s)[2], float &mx, v16f (&next)[2], const uint8_t *nk,
+                                         const uint8_t *vt, float c)
+{
+    constexpr int QS = DK / 8, VS = DV / 8;                 // steps: one product each
+    constexpr int QP = (16 + QS - 1) / QS, VP = 16 / VS;    // pairs of scores per step
+    constexpr int QA = 4, VA = 3;                           // steps that fragments are read ahead
+    const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
+    const uint32_t krow = fresh((uint32_t)(l32 * DK * 2)), kx = fresh(16u * (uint32_t)(k_slot<DK>(l32, h) - l32 * (DK / 8)));
+    const int vr = 4 * h + ((lane & 15) >> 2), vc = (lane & 16) + 4 * (lane & 3);
+    const uint32_t vrow = fresh((uint32_t)(vr * DV * 2 + 2 * vc)), vx = fresh(16u * (uint32_t)(v_slot<DV>(vr, 0) - vr * (DV / 8)));
+    u4 ka[QS];
+    s4 va[VS][2];
+    auto kread = [&](int i) {
+        ka[i] = *reinterpret_cast<const u4 *>(nk + (krow + (kx ^ (32u * (i % (DK / 16))))) + 64 * (i / (DK / 16)) * DK);
+    };
+    auto vread = [&](int i) {
+        const uint8_t *at = vt + (vrow + (vx ^ (64u * (i % (DV / 32))))) + 32 * (i / (DV / 32)) * DV;
+        va[i][0] = lds_tr(at), va[i][1] = lds_tr(at + 16 * DV);
+    };
+#pragma unroll
+    for (int i = 0; i < QA; ++i) kread(i);
+    att_raise(r, mx, c);
+    const float mc = r.m == -INFINITY ? 0.0f : r.m * c;
+    uint32_t p[16];
+    float l[2] = {r.l, 0.0f};
+#pragma unroll
+    for (int i = 0; i < QS; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + QA < QS) kread(i + QA);
+        else if (i + QA - QS < VA) vread(i + QA - QS);
+        constexpr int KS = DK / 16;
+        const int t = i / KS, k = i % KS;
+        if (k == 0)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) next[t][e] = 0.0f;
+        next[t] = mfma32(as_bf8(ka[i]), r.q[k], next[t]);
+#pragma unroll
+        for (int w = QP * i; w < QP * i + QP && w < 16; ++w) {
+            float e[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                e[x] = __builtin_amdgcn_exp2f(fmaf(s[w / 8][2 * (w % 8) + x], c, -mc));
+                l[x] += e[x];
+            }
+            p[w] = at_pack(e[0], e[1]);
+        }
+    }
+    r.l = l[0] + l[1];
+    asm volatile("" : "+v"(r.l));   // or the sum is put off to the next tile, and with it all weights are held
+    float nm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VS; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + VA < VS) vread(i + VA);
+        const int k = i / (DV / 32), d = i % (DV / 32);
+        bf8 v;
+        __builtin_memcpy(&v, &va[i][0], 8);
+        __builtin_memcpy(reinterpret_cast<char *>(&v) + 8, &va[i][1], 8);
+        r.o[d] = mfma32(v, as_bf8(u4{p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]}), r.o[d]);
+#pragma unroll
+        for (int w = VP * i; w < VP * i + VP; ++w) nm = fmaxf(fmaxf(nm, next[w / 8][2 * (w % 8)]), next[w / 8][2 * (w % 8) + 1]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    mx = swap_max(nm);
+}
+
+// The same where bit j of `seen` says whether this lane's row sees key j of the tile: what it does not see takes no part,
+// whatever its key and value hold. The next scores take the place of this tile's.
+template <int DK, int DV>
+__device__ __forceinline__ void att_tile_masked(AttRows<DK, DV> &r, v16f (&s)[2], const uint8_t *nk, const uint8_t *vt, float c,
+                                                uint64_t seen)
+{
+    att_mask(s, seen);
+    att_raise(r, att_max(s), c);
+    bf8 p[4];
+    att_weights(p, r, s, c);
+    if (v_not_finite<DV>(vt)) {
+        att_values<true>(r, p, vt);
+        att_not_finite(r, s, vt, seen);
+    } else {
+        att_values<false>(r, p, vt);
+    }
+    att_scores(s, r, nk);
 }
 
 }  // namespace k3moe

@@ -51,201 +51,292 @@ __device__ __forceinline__ float lp_logit(const LpParams &p, bool f32, int t, in
     return f32 ? static_cast<const float *>(p.x)[o] : bf16f(static_cast<const uint16_t *>(p.x)[o]);
 }
 
-// e^d for d <= 0, to about an ulp: the product with log2(e) is held in two parts.
-__device__ __forceinline__ float lp_exp(float d)
+// e^d for d <= 0: d log2(e) is rounded once, 2^-24 of |d| relative in the result.
+__device__ __forceinline__ float lp_exp(float d) { return __builtin_amdgcn_exp2f(d * 1.44269502f); }
+
+// Wave reductions through DPP, the result in every lane (read back from lane 63).
+template <class T, class F>
+__device__ __forceinline__ T lp_wave(T v, T none, F f)
 {
-    const float t = d * 1.44269502f, e = fmaf(d, 1.44269502f, -t) + d * 1.92596299e-8f;
-    const float x = __builtin_amdgcn_exp2f(t);
-    return d < -126.0f * 0.69314718f ? x : fmaf(x, e * 0.69314718f, x);
+    auto step = [&](auto ctrl, auto rows) {
+        constexpr int kCtrl = decltype(ctrl)::value, kRows = decltype(rows)::value;
+        uint32_t w[sizeof(T) / 4], n[sizeof(T) / 4];
+        __builtin_memcpy(w, &v, sizeof(T));
+        __builtin_memcpy(n, &none, sizeof(T));
+#pragma unroll
+        for (unsigned i = 0; i < sizeof(T) / 4; ++i)
+            w[i] = (uint32_t)__builtin_amdgcn_update_dpp((int)n[i], (int)w[i], kCtrl, kRows, 0xf, false);
+        T x;
+        __builtin_memcpy(&x, w, sizeof(T));
+        v = f(v, x);
+    };
+    typedef std::integral_constant<int, 0xf> all;
+    step(std::integral_constant<int, 0xb1>{}, all{});                                   // neighbours
+    step(std::integral_constant<int, 0x4e>{}, all{});                                   // pairs
+    step(std::integral_constant<int, 0x141>{}, all{});                                  // half rows
+    step(std::integral_constant<int, 0x140>{}, all{});                                  // rows
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});     // row 0 into 1, 2 into 3
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});     // row 1 into 2 and 3
+    uint32_t w[sizeof(T) / 4];
+    __builtin_memcpy(w, &v, sizeof(T));
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 4; ++i) w[i] = (uint32_t)__builtin_amdgcn_readlane((int)w[i], 63);
+    T r;
+    __builtin_memcpy(&r, w, sizeof(T));
+    return r;
 }
 
-template <class T, class F>
-__device__ __forceinline__ T block_reduce(T v, T *red, F f)
+struct LpMax {
+    template <class T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a > b ? a : b; }
+};
+struct LpFmax {   // passes over NaN
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct LpAdd {
+    template <class T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+
+// Joins a block's waves; red: one place per wave. W waves.
+template <int W, class T, class F>
+__device__ __forceinline__ T lp_block(T v, T none, T *red, F f)
 {
+    v = lp_wave(v, none, f);
+    if constexpr (W > 1) {
+        __syncthreads();             // what was in red is read
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = f(v, __shfl_xor(v, o));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < kLpWaves; ++w) v = f(v, red[w]);
+        for (int w = 1; w < W; ++w) v = f(v, red[w]);
+    }
     return v;
 }
 
-// The k largest of the keys that the block's threads hold. best: this thread's largest (0: none); each(f): calls
-// f(key) for all of its keys; put(rank, key). Every thread of the block calls it.
-template <class Each, class Put>
-__device__ __forceinline__ void block_top(uint64_t best, int k, uint64_t *list, int *count, uint64_t *red, Each each, Put put)
+// A bound that at least k of the wave's elements reach, as the key of a logit: the k-th largest of the lanes' maxima,
+// rounded down to its first 22 bits. 0 where fewer than k lanes hold any.
+__device__ __forceinline__ uint32_t lp_bound(uint32_t best, int k)
 {
-    const int tid = threadIdx.x;
-    // the k-th largest of the wave's 64 maxima (0 where fewer lanes hold any)
-    const uint32_t mine = (uint32_t)(best >> 32);
     uint32_t tau = 0u;
 #pragma unroll
-    for (int b = 31; b >= 0; --b) {
+    for (int b = 31; b >= 10; --b) {
         const uint32_t c = tau | (1u << b);
-        if (__popcll(__ballot(mine >= c)) >= k) tau = c;
+        if (__popcll(__ballot(best >= c)) >= k) tau = c;
     }
-    if (tid == 0) *count = 0;
-    const uint64_t bound = block_reduce<uint64_t>((uint64_t)tau << 32, red, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-    each([&](uint64_t key) {
-        if (key >= bound && key) {
-            const int at = atomicAdd(count, 1);   // the order of the list does not matter: every key has its own rank
-            if (at < kLpCand) list[at] = key;
-        }
-    });
-    __syncthreads();
-    const int n = *count;
+    return tau;
+}
+
+struct LpTop {
+    uint64_t list[kLpCand], red[kLpWaves];
+    int count;
+};
+
+// The k largest of the keys that a block's threads hold, all that reach a bound (which k of them do) being in L.list,
+// L.count of them. each(f): calls f(key) for all of this thread's keys; put(rank, key), key 0: there is none. Every
+// thread of the block calls it. W waves.
+template <int W, class Each, class Put>
+__device__ __forceinline__ void lp_rank(LpTop &L, int k, Each each, Put put)
+{
+    const int tid = threadIdx.x, n = L.count;
     if (n <= kLpCand) {
-        for (int i = tid; i < n; i += kLpThreads) {
-            const uint64_t key = list[i];
+        for (int i = tid; i < n; i += 64 * W) {
+            const uint64_t key = L.list[i];
             int rank = 0;
-            for (int j = 0; j < n; ++j) rank += list[j] > key ? 1 : 0;
+            for (int j = 0; j < n; ++j) rank += L.list[j] > key ? 1 : 0;
             if (rank < k) put(rank, key);
         }
-        for (int i = n + tid; i < k; i += kLpThreads) put(i, 0ull);
+        for (int i = n + tid; i < k; i += 64 * W) put(i, 0ull);
     } else {
         uint64_t last = ~0ull;
         for (int r = 0; r < k; ++r) {
             uint64_t next = 0ull;
             each([&](uint64_t key) { next = key < last && key > next ? key : next; });
-            next = block_reduce<uint64_t>(next, red, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+            next = lp_block<W, uint64_t>(next, 0ull, L.red, LpMax());
             if (tid == 0) put(r, next);
             last = next;
         }
     }
 }
 
+__device__ __forceinline__ void lp_collect(LpTop &L, uint64_t key)
+{
+    const int at = atomicAdd(&L.count, 1);   // the order of the list does not matter: every key has its own rank
+    if (at < kLpCand) L.list[at] = key;
+}
+
 // One chunk of VPT * 256 logits of a row. W: neighbouring elements per load.
 template <int VPT, bool F32, int W>
-__global__ __launch_bounds__(kLpThreads) void k_lp_chunk(LpParams p)
+__global__ __launch_bounds__(kLpThreads, 4) void k_lp_chunk(LpParams p)
 {
-    __shared__ uint64_t list[kLpCand], red[kLpWaves];
-    __shared__ int count;
-    const int tid = threadIdx.x;
+    __shared__ LpTop L;
+    __shared__ float wmax[kLpWaves];
+    __shared__ LpStats wsum[kLpWaves];
+    __shared__ uint32_t wbound[kLpWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int t = blockIdx.x / p.chunks, c = blockIdx.x - t * p.chunks;
     const int base = c * VPT * kLpThreads;
     auto index = [&](int j) { return base + ((j / W) * kLpThreads + tid) * W + j % W; };
 
     float v[VPT];
     const int64_t row = (int64_t)t * p.stride;
+    const bool whole = base + VPT * kLpThreads <= p.V;
 #pragma unroll
     for (int j = 0; j < VPT; j += W) {
-        const int i = min(index(j), p.V - 1) / W * W;   // a last load that ends behind the row is shortened below
-        if constexpr (W == 1) {
-            v[j] = F32 ? static_cast<const float *>(p.x)[row + i] : bf16f(static_cast<const uint16_t *>(p.x)[row + i]);
-        } else if constexpr (F32) {
-            if (i + W <= p.V) {
+        const int i = whole ? index(j) : min(index(j), p.V - 1) / W * W;
+        if (W > 1 && (whole || i + W <= p.V)) {
+            if constexpr (F32) {
                 const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + row + i);
                 v[j] = a.x, v[j + 1] = a.y, v[j + 2] = a.z, v[j + 3] = a.w;
             } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[j + e] = static_cast<const float *>(p.x)[row + min(i + e, p.V - 1)];
-            }
-        } else {
-            if (i + W <= p.V) {
                 const u4 a = *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(p.x) + row + i);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[j + 2 * e] = bf16f(a[e] & 0xffffu), v[j + 2 * e + 1] = bf16f(a[e] >> 16);
-            } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[j + e] = bf16f(static_cast<const uint16_t *>(p.x)[row + min(i + e, p.V - 1)]);
             }
+        } else {   // single elements, or the row's last ones
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                v[j + e] = F32 ? static_cast<const float *>(p.x)[row + min(i + e, p.V - 1)]
+                               : bf16f(static_cast<const uint16_t *>(p.x)[row + min(i + e, p.V - 1)]);
         }
     }
-    float m = -INFINITY;
+    float mine = -INFINITY;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        if (index(j) >= p.V) v[j] = -INFINITY;
-        m = fmaxf(m, v[j]);          // passes over NaN
+        if (!whole && index(j) >= p.V) v[j] = -INFINITY;
+        mine = fmaxf(mine, v[j]);          // passes over NaN
     }
-    m = block_reduce<float>(m, reinterpret_cast<float *>(red), [](float a, float b) { return fmaxf(a, b); });
+    // lanes without an element hold none of the chunk's largest
+    const float wm = lp_wave(mine, -INFINITY, LpFmax());
+    const uint32_t key = index(0) < p.V ? order_key(mine + 0.0f) : 0u;
+    if (lane == 0) wmax[wave] = wm;
+    if (p.k > 0) {
+        const uint32_t bound = lp_bound(key, p.k);
+        if (lane == 0) wbound[wave] = bound;
+    }
+    if (tid == 0) L.count = 0;
+    __syncthreads();
+    float m = wmax[0];
+#pragma unroll
+    for (int w = 1; w < kLpWaves; ++w) m = fmaxf(m, wmax[w]);
     const float use = m == -INFINITY ? 0.0f : m;
     float rest = 0.0f, dev = 0.0f;
     int top = 0;
+    // -inf: e is 0, and so is its term of the deviation; +inf: d is NaN and stays
+    if (wm == m && m < INFINITY) {         // the wave that holds the maximum counts it apart
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const float d = v[j] - use, e = lp_exp(d);
-        const bool peak = v[j] == m && m != -INFINITY;
-        top += peak && m < INFINITY ? 1 : 0;
-        rest += peak && m < INFINITY ? 0.0f : e;       // +inf: d is NaN and stays
-        dev -= e == 0.0f ? 0.0f : d * e;
+        for (int j = 0; j < VPT; ++j) {
+            const float d = v[j] - use, e = lp_exp(d);
+            const bool peak = v[j] == m;
+            top += peak ? 1 : 0;
+            rest += peak ? 0.0f : e;
+            dev = fmaf(-fmaxf(d, -256.0f), e, dev);
+        }
+        if (m == -INFINITY) top = 0, rest = rest != rest ? rest : 0.0f;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const float d = v[j] - use, e = lp_exp(d);
+            rest += e;
+            dev = fmaf(-fmaxf(d, -256.0f), e, dev);
+        }
     }
-    const double R = block_reduce<double>(rest, reinterpret_cast<double *>(red), [](double a, double b) { return a + b; });
-    const double Dv = block_reduce<double>(dev, reinterpret_cast<double *>(red), [](double a, double b) { return a + b; });
-    const int N = block_reduce<int>(top, reinterpret_cast<int *>(red), [](int a, int b) { return a + b; });
-    if (tid == 0) p.stats[(int64_t)t * p.chunks + c] = LpStats{R, Dv, m, N};
+    {
+        const double R = lp_wave<double>(rest, 0.0, LpAdd()), D = lp_wave<double>(dev, 0.0, LpAdd());
+        const int N = lp_wave<int>(top, 0, LpAdd());
+        if (lane == 0) wsum[wave] = LpStats{R, D, m, N};
+    }
+    if (p.k > 0) {
+        uint32_t bound = wbound[0];
+#pragma unroll
+        for (int w = 1; w < kLpWaves; ++w) bound = max(bound, wbound[w]);
+        if (__ballot(key >= bound && key)) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const uint32_t x = order_key(v[j] + 0.0f);
+                if (__ballot(x >= bound)) {
+                    const int i = index(j);
+                    if (x >= bound && i < p.V) lp_collect(L, ((uint64_t)x << 32) | (uint32_t)~(uint32_t)i);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        LpStats s = wsum[0];
+#pragma unroll
+        for (int w = 1; w < kLpWaves; ++w) s.rest += wsum[w].rest, s.dev += wsum[w].dev, s.top += wsum[w].top;
+        p.stats[(int64_t)t * p.chunks + c] = s;
+    }
     if (p.k == 0) return;
-
-    uint64_t best = 0ull;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int i = index(j);
-        const uint64_t key = i < p.V ? lp_key(v[j], i) : 0ull;
-        best = key > best ? key : best;
-    }
     uint64_t *out = p.cand + ((int64_t)t * p.chunks + c) * p.k;
-    block_top(best, p.k, list, &count, red,
-              [&](auto f) {
+    lp_rank<kLpWaves>(L, p.k,
+                      [&](auto f) {
 #pragma unroll
-                  for (int j = 0; j < VPT; ++j) {
-                      const int i = index(j);
-                      if (i < p.V) f(lp_key(v[j], i));
-                  }
-              },
-              [&](int rank, uint64_t key) { out[rank] = key; });
+                          for (int j = 0; j < VPT; ++j) {
+                              const int i = index(j);
+                              if (i < p.V) f(lp_key(v[j], i));
+                          }
+                      },
+                      [&](int rank, uint64_t key) { out[rank] = key; });
 }
 
-// Joins a row's chunks: one block per row.
-template <bool F32>
-__global__ __launch_bounds__(kLpThreads) void k_lp_join(LpParams p)
+// Joins a row's chunks: one block of W waves per row.
+template <bool F32, int W>
+__global__ __launch_bounds__(64 * W) void k_lp_join(LpParams p)
 {
-    __shared__ uint64_t list[kLpCand], red[kLpWaves];
-    __shared__ int count;
+    __shared__ LpTop L;
     const int tid = threadIdx.x, t = blockIdx.x;
     const LpStats *st = p.stats + (int64_t)t * p.chunks;
+    const uint64_t *cand = p.cand + (int64_t)t * p.chunks * p.k;
+    const int n = p.chunks * p.k;
+    uint64_t best = 0ull;
+    for (int i = tid; i < n; i += 64 * W) best = cand[i] > best ? cand[i] : best;
     float m = -INFINITY;
-    for (int c = tid; c < p.chunks; c += kLpThreads) m = fmaxf(m, st[c].m);
-    m = block_reduce<float>(m, reinterpret_cast<float *>(red), [](float a, float b) { return fmaxf(a, b); });
+    for (int c = tid; c < p.chunks; c += 64 * W) m = fmaxf(m, st[c].m);
+    m = lp_block<W, float>(m, -INFINITY, reinterpret_cast<float *>(L.red), LpFmax());
     double s = 0.0, dev = 0.0;
-    for (int c = tid; c < p.chunks; c += kLpThreads) {
+    int top = 0;
+    for (int c = tid; c < p.chunks; c += 64 * W) {
         const LpStats x = st[c];
         const double part = x.rest + x.top;
-        if (part == 0.0) continue;       // nothing but -inf
-        const double f = x.m == m ? 1.0 : exp((double)x.m - (double)m);
-        s += x.m == m ? x.rest : part * f;
-        dev += f * (x.dev + (x.m == m ? 0.0 : ((double)m - (double)x.m) * part));
+        if (x.m == m) {
+            s += x.rest, dev += x.dev, top += x.top;
+        } else if (part != 0.0) {          // else nothing but -inf
+            const double f = exp((double)x.m - (double)m);
+            s += part * f, dev += f * (x.dev + ((double)m - (double)x.m) * part);
+        }
     }
-    int top = 0;
-    for (int c = tid; c < p.chunks; c += kLpThreads) top += st[c].m == m ? st[c].top : 0;
-    s = block_reduce<double>(s, reinterpret_cast<double *>(red), [](double a, double b) { return a + b; });
-    dev = block_reduce<double>(dev, reinterpret_cast<double *>(red), [](double a, double b) { return a + b; });
-    top = block_reduce<int>(top, reinterpret_cast<int *>(red), [](int a, int b) { return a + b; });
+    s = lp_block<W, double>(s, 0.0, reinterpret_cast<double *>(L.red), LpAdd());
+    dev = lp_block<W, double>(dev, 0.0, reinterpret_cast<double *>(L.red), LpAdd());
+    top = lp_block<W, int>(top, 0, reinterpret_cast<int *>(L.red), LpAdd());
     // no maximum that counts: a row of -inf, of NaN, or with +inf
     const double log_s = top > 0 ? log1p(s + (top - 1)) : (double)NAN;
     const double peak = (double)m;
     if (p.ent && tid == 0) p.ent[t] = (float)(log_s + dev / (s + top));
-    for (int j = tid; j < p.n_ids; j += kLpThreads) {
+    for (int j = tid; j < p.n_ids; j += 64 * W) {
         const int64_t o = (int64_t)t * p.n_ids + j;
         const int i = p.ids[o];
         p.lp[o] = i >= 0 && i < p.V ? (float)((double)lp_logit(p, F32, t, i) - peak - log_s) : NAN;
     }
     if (p.k == 0) return;
-    const uint64_t *cand = p.cand + (int64_t)t * p.chunks * p.k;
-    const int n = p.chunks * p.k;
-    uint64_t best = 0ull;
-    for (int i = tid; i < n; i += kLpThreads) best = cand[i] > best ? cand[i] : best;
-    block_top(best, p.k, list, &count, red,
-              [&](auto f) {
-                  for (int i = tid; i < n; i += kLpThreads) f(cand[i]);
-              },
-              [&](int rank, uint64_t key) {
-                  const int i = (int)~(uint32_t)key;
-                  const int64_t o = (int64_t)t * p.k + rank;
-                  p.top_ids[o] = i;
-                  p.top_lp[o] = (float)((double)lp_logit(p, F32, t, i) - peak - log_s);
-              });
+    if (tid == 0) L.count = 0;
+    const uint32_t bound = lp_block<W, uint32_t>(lp_bound((uint32_t)(best >> 32), p.k), 0u, reinterpret_cast<uint32_t *>(L.red), LpMax());
+    __syncthreads();
+    auto each = [&](auto f) {
+        for (int i = tid; i < n; i += 64 * W) f(cand[i]);
+    };
+    if ((uint32_t)(best >> 32) >= bound)
+        each([&](uint64_t key) {
+            if (key && (uint32_t)(key >> 32) >= bound) lp_collect(L, key);
+        });
+    __syncthreads();
+    lp_rank<W>(L, p.k, each, [&](int rank, uint64_t key) {
+        const int i = (int)~(uint32_t)key;
+        const int64_t o = (int64_t)t * p.k + rank;
+        p.top_ids[o] = i;
+        p.top_lp[o] = (float)((double)lp_logit(p, F32, t, i) - peak - log_s);
+    });
 }
 
 // Chunks of a row: long ones where they still give every CU some blocks (a chunk's ends, the top list first of all,
@@ -274,7 +365,8 @@ void launch_lp(const LpParams &p, bool vec, hipStream_t s)
         if (vec) k_lp_chunk<kLpShort, F32, W><<<grid, kLpThreads, 0, s>>>(p);
         else k_lp_chunk<kLpShort, F32, 1><<<grid, kLpThreads, 0, s>>>(p);
     }
-    k_lp_join<F32><<<(unsigned)p.T, kLpThreads, 0, s>>>(p);
+    if (p.chunks * (int64_t)p.k <= 4096) k_lp_join<F32, 1><<<(unsigned)p.T, 64, 0, s>>>(p);
+    else k_lp_join<F32, kLpWaves><<<(unsigned)p.T, kLpThreads, 0, s>>>(p);
 }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }

@@ -184,7 +184,7 @@ template <int DK, int DV, bool X8>
 __global__ __launch_bounds__(64 * kTrWaves, 2) void k_tree(TreeParams p)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    constexpr int KB = kAtKeys * DK * 2, BUF = kAtKeys * (DK + DV) * 2, EB = X8 ? 1 : 2;
+    constexpr int KB = kAtKeys * DK * 2, VB = kAtKeys * DV * 2, EB = X8 ? 1 : 2;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, l32 = lane & 31;
     const int64_t total = tree_total(p), per = run_length(total);
@@ -218,8 +218,7 @@ __global__ __launch_bounds__(64 * kTrWaves, 2) void k_tree(TreeParams p)
 
         // page numbers of a tile's four runs of 16 keys, and which of them are in the cache
         const int32_t *table = p.pages + (int64_t)b * p.width;
-        int own;            // the page of this wave's rows, -1: none
-        auto lookup = [&](int t) {
+        auto lookup = [&](int t, int &own) {   // own: the page of this wave's rows, -1: none
             uint32_t ok = 0;
             own = -1;
 #pragma unroll
@@ -234,44 +233,54 @@ __global__ __launch_bounds__(64 * kTrWaves, 2) void k_tree(TreeParams p)
         };
         PageStage<DK, X8> sk;
         PageStage<DV, X8> sv;
-        auto issue = [&](int t, int buf) {
-            const int pos = t * kAtKeys + 16 * wave, rows = own < 0 ? 0 : min(s.keys - pos, 16);
-            const int64_t row = ((int64_t)max(own, 0) * p.Hkv + kvh) * page + (pos & (page - 1));
-            sk.issue(p.kc + row * DK * EB, X8 ? p.ks + row * (DK / 32) : nullptr, rows, lds + buf * BUF, k_slot<DK>);
-            sv.issue(p.vc + row * DV * EB, X8 ? p.vs + row * (DV / 32) : nullptr, rows, lds + buf * BUF + KB, v_slot<DV>);
+        // Keys run a tile ahead of the values: tile t's scores are there before its weights are taken. What goes through
+        // registers (8-bit pages) is written behind the tile's work, before the barrier in front of its use.
+        auto where = [&](int t, int own, int &rows) {
+            const int pos = t * kAtKeys + 16 * wave;
+            rows = own < 0 ? 0 : min(s.keys - pos, 16);
+            return ((int64_t)max(own, 0) * p.Hkv + kvh) * page + (pos & (page - 1));
         };
-        auto commit = [&](int buf) {
-            sk.commit(lds + buf * BUF, k_slot<DK>);
-            sv.commit(lds + buf * BUF + KB, v_slot<DV>);
+        auto issue_k = [&](int t, int own) {
+            int rows;
+            const int64_t row = where(t, own, rows);
+            sk.issue(p.kc + row * DK * EB, X8 ? p.ks + row * (DK / 32) : nullptr, rows, lds + ((t - t0) & 1) * KB, k_slot<DK>);
         };
+        auto issue_v = [&](int t, int own) {
+            int rows;
+            const int64_t row = where(t, own, rows);
+            sv.issue(p.vc + row * DV * EB, X8 ? p.vs + row * (DV / 32) : nullptr, rows, lds + 2 * KB + ((t - t0) & 1) * VB, v_slot<DV>);
+        };
+        auto commit_k = [&](int t) { sk.commit(lds + ((t - t0) & 1) * KB, k_slot<DK>); };
+        auto commit_v = [&](int t) { sv.commit(lds + 2 * KB + ((t - t0) & 1) * VB, v_slot<DV>); };
 
         at_barrier();       // the last segment's tiles are read
-        uint32_t ok = lookup(t0);
-        issue(t0, 0);
-        commit(0);
+        int own0, own1 = -1, own2 = -1;            // this wave's pages of tiles t, t + 1, t + 2
+        uint32_t ok = lookup(t0, own0), ok1 = 0;
+        if (t0 + 1 < t1) ok1 = lookup(t0 + 1, own1);
+        issue_k(t0, own0), issue_v(t0, own0);
+        commit_k(t0), commit_v(t0);
+        if (t0 + 1 < t1) issue_k(t0 + 1, own1), commit_k(t0 + 1);
+        at_barrier();
+        v16f sc[2];
+        if (busy) att_scores(sc, r, lds);
         for (int t = t0; t < t1; ++t) {
-            const int buf = (t - t0) & 1, first = t * kAtKeys;
-            uint32_t next_ok = 0;
+            const int first = t * kAtKeys;
+            uint32_t ok2 = 0;
             at_barrier();
-            if (t + 1 < t1) {
-                next_ok = lookup(t + 1);
-                issue(t + 1, buf ^ 1);
-            }
-            const uint8_t *kt = lds + buf * BUF;
+            if (t + 2 < t1) ok2 = lookup(t + 2, own2), issue_k(t + 2, own2);
+            if (t + 1 < t1) issue_v(t + 1, own1);
             if (busy) {
+                const uint8_t *nk = lds + ((t + 1 - t0) & 1) * KB, *vt = lds + 2 * KB + ((t - t0) & 1) * VB;
                 const int a = s.ctx - first;   // the tile's keys in front of the drafted ones
-                if (a >= kAtKeys && ok == 15u) {
-                    att_tile<false>(r, kt, kt + KB, c, ~0ull);
-                } else {
-                    uint64_t seen = low_bits(a) | (a >= 64 || a <= -64 ? 0ull : a >= 0 ? word << a : word >> -a);
-                    seen &= low_bits(s.keys - first);
+                uint64_t seen = low_bits(a) | (a >= 64 || a <= -64 ? 0ull : a >= 0 ? word << a : word >> -a);
+                seen &= low_bits(s.keys - first);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) seen &= ok >> g & 1 ? ~0ull : ~(0xffffull << (16 * g));
-                    att_tile<true>(r, kt, kt + KB, c, seen);
-                }
+                for (int g = 0; g < 4; ++g) seen &= ok >> g & 1 ? ~0ull : ~(0xffffull << (16 * g));
+                att_tile_masked(r, sc, nk, vt, c, seen);
             }
-            ok = next_ok;
-            if (t + 1 < t1) commit(buf ^ 1);
+            if (t + 2 < t1) commit_k(t + 2);
+            if (t + 1 < t1) commit_v(t + 1);
+            ok = ok1, ok1 = ok2, own1 = own2;
         }
 
         const float l = r.l + __shfl_xor(r.l, 32);

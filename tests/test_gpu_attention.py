@@ -69,6 +69,13 @@ def test_packed(D, Dv, causal):
     _case([1, 70, 0, 33, 129, 2, 64], [1, 70, 0, 33, 129, 2, 64], 4, 2, D, Dv, causal, tail=3, pad=8)
 
 
+@pytest.mark.parametrize("D,Dv", DIMS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_tiles_than_cus(D, Dv, causal):
+    """Whole tiles per block; with few of them, as in most tests here, two halves of a block share a tile's keys."""
+    _case([257, 1, 130, 64], [257, 40, 700, 64], 96, 8, D, Dv, causal, heads=[0, 37, 95], tail=2)
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (8, 1), (6, 2), (12, 4)])
 def test_groups(Hq, Hkv):
     _case([40, 90], [40, 90], Hq, Hkv, 64, 64, pad=16)
@@ -103,12 +110,13 @@ def test_rising_scores_raise_the_maximum_in_every_tile():
 
 
 @pytest.mark.parametrize("D,Dv", DIMS)
-def test_what_is_not_seen_has_no_influence(D, Dv):
+@pytest.mark.parametrize("Hq", [2, 80])
+def test_what_is_not_seen_has_no_influence(D, Dv, Hq):
     """NaN and infinities in keys and values behind a query, and in the other sequences' rows."""
     nq = [100, 3, 140]
-    q, k, v = _inputs(nq, nq, 2, 1, D, Dv)
+    q, k, v = _inputs(nq, nq, Hq, 1, D, Dv)
     bad = [float("nan"), float("inf"), float("-inf")]
-    clean, lse = torch.empty((sum(nq), 2, Dv), dtype=BF, device=DEV), torch.empty((sum(nq), 2), device=DEV)
+    clean, lse = torch.empty((sum(nq), Hq, Dv), dtype=BF, device=DEV), torch.empty((sum(nq), Hq), device=DEV)
     k3.attention(q, k, v, _cu(nq), clean, lse=lse)
     for b in bad:
         k2, v2 = k.clone(), v.clone()
