@@ -553,8 +553,10 @@ k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, const uint16_t
  *          max_q of a sequence, and rows of no sequence, are left as they were.
  *   tree   uint64 [Tq] (optional)
  *   q bf16 [Tq][q_heads][k_dim], out bf16 [Tq][q_heads][v_dim], lse fp32 [Tq][q_heads] (optional)
- * (k_dim, v_dim) and alignment as in k3moe_attention. The workspace's size
- * depends on neither lens nor the number of sequences. */
+ * (k_dim, v_dim) and alignment as in k3moe_attention; page * pages_width up to
+ * 2^30, and the tiles of 64 keys of all heads, blocks of 32 rows and sequences up
+ * to 2^30 if every table were full (K3MOE_E_UNSUPPORTED_SHAPE above). The
+ * workspace's size depends on neither lens nor the number of sequences. */
 k3moe_status k3moe_tree_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t v_dim,
                                                  int32_t max_q, size_t *bytes);
 k3moe_status k3moe_tree_attention(const uint16_t *q, int64_t q_stride, const k3moe_pages *cache,

@@ -25,45 +25,6 @@ struct PromptParams {
     float scale;
 };
 
-#ifdef __HIP_DEVICE_COMPILE__
-// Direct loads of 64 rows of one head into an LDS tile laid out by k_slot or v_slot; every wave loads 16 rows.
-// The places that a load fills are 1 KB in order, so each lane fetches the slot that belongs into its own. With row =
-// 16 wave + 8 a + r the exchange of slots is the same for a = 0 and 1 but for one bit of the slot's number (k_slot), or at all
-// (v_slot); so a load's offset is a lane constant, exchanged, and a wave constant.
-template <int D, bool K>
-struct TileStage {
-    static constexpr int SL = D / 8, L = D / 32;          // slots per row, loads of a wave
-    static constexpr int J = D == 192 ? 3 : L / 2;        // loads of 8 rows
-    uint32_t x[J], at[J];                                  // 16 * the slot, bytes of the row r
-
-    __device__ __forceinline__ static int row(int j) { return (64 * j + (int)(threadIdx.x & 63)) / SL; }
-    int wave;
-
-    __device__ __forceinline__ void init(int64_t stride, int w)
-    {
-        wave = w;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int r = row(j), pos = (64 * j + (int)(threadIdx.x & 63)) % SL;
-            x[j] = 16u * (uint32_t)((K ? k_slot<D>(r, pos) : v_slot<D == 192 ? 128 : D>(r, pos)) - r * SL);
-            at[j] = (uint32_t)r * (uint32_t)stride * 2u;
-        }
-    }
-    // rows row0 .. row0 + 63 behind src (the head's first row of the sequence); those from `end` on read as zeros
-    __device__ __forceinline__ void load(const uint16_t *src, int64_t stride, int row0, int end, const uint8_t *lds) const
-    {
-        const bool whole = row0 + kAtKeys <= end;
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int a = i / J, j = i % J, base = 16 * wave + 8 * a;
-            uint32_t o = (x[j] ^ (K ? (D == 128 ? 128u : 64u) * a : 0u)) + at[j];
-            if (!whole) o = row0 + base + row(j) < end ? o : kAtOut;
-            lds_load16(src + (int64_t)row0 * stride, o, (uint32_t)base * (uint32_t)stride * 2u, lds + (wave * L + i) * 1024);
-        }
-    }
-};
-#endif
-
 // SPLIT: four more waves take the second half of the keys, with buffers of their own.
 template <int DK, int DV, bool SPLIT>
 __global__ __launch_bounds__(64 * kPrWaves * (SPLIT ? 2 : 1), 2) void k_attention(PromptParams p)
@@ -130,13 +91,20 @@ __global__ __launch_bounds__(64 * kPrWaves * (SPLIT ? 2 : 1), 2) void k_attentio
     // Keys run a tile ahead of the values: tile t's scores are computed beside the weights of tile t - 1. i counts a
     // part's tiles.
     const uint8_t *buf = lds + part * 2 * (KB + VB);
-    TileStage<DK, true> sk;
-    TileStage<DV, false> sv;
-    sk.init(p.ks, wave), sv.init(p.vs, wave);
+    RowStage<DK, true> sk;
+    RowStage<DV, false> sv;
+    sk.init(p.ks), sv.init(p.vs);
     auto ktile = [&](int i) { return buf + (i & 1) * KB; };
     auto vtile = [&](int i) { return buf + 2 * KB + (i & 1) * VB; };
-    auto load_k = [&](int i) { if (t0 + i < t1) sk.load(kp, p.ks, (t0 + i) * kAtKeys, N, ktile(i)); };
-    auto load_v = [&](int i) { if (t0 + i < t1) sv.load(vp, p.vs, (t0 + i) * kAtKeys, N, vtile(i)); };
+    // a wave loads 16 of a tile's rows; those behind the last key read as zeros
+    auto load_k = [&](int i) {
+        const int at = (t0 + i) * kAtKeys + 16 * wave;
+        if (t0 + i < t1) sk.load(kp + (int64_t)at * p.ks, p.ks, N - at, ktile(i) + 16 * wave * DK * 2);
+    };
+    auto load_v = [&](int i) {
+        const int at = (t0 + i) * kAtKeys + 16 * wave;
+        if (t0 + i < t1) sv.load(vp + (int64_t)at * p.vs, p.vs, N - at, vtile(i) + 16 * wave * DV * 2);
+    };
     const float c = p.scale * kLog2e;
     if (steps > 0) {
         load_k(0), load_k(1), load_v(0);

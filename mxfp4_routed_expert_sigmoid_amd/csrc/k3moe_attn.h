@@ -28,7 +28,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The running maximum is raised only when a tile exceeds it by more than this (in powers of two): the weights then
 // stay below 2^8 of what they would be, which neither fp32 sums nor the bf16 weights, rounded relatively, notice.
 constexpr float kAtSlack = 8.0f;
-// An offset behind every tile's bytes (63 rows of 2^24 elements at most): read as zeros.
+// An offset behind the bytes of 16 rows of 2^24 elements at most: read as zeros.
 constexpr uint32_t kAtOut = 0xff000000u;
 
 __device__ __forceinline__ uint32_t at_bf16(float f) { return f != f ? 0x7fc0u : bf16_rne_u32(f); }
@@ -99,6 +99,41 @@ __device__ __forceinline__ void lds_load16(const void *base, uint32_t offset, ui
                  "s"(__builtin_amdgcn_readfirstlane((int)soffset))
                  : "memory");   // m0 is no register that the compiler keeps anything in here
 }
+
+// Direct loads of 16 rows of one head into their places of an LDS tile laid out by k_slot (K) or v_slot. The places that
+// a load fills are 1 KB in order, so each lane fetches the slot that belongs into its own. With row = 8 a + r the
+// exchange of slots is the same for a = 0 and 1 but for one bit of the slot's number (k_slot), or at all (v_slot); so a
+// load's offset is a lane constant, exchanged, and a wave constant.
+template <int D, bool K>
+struct RowStage {
+    static constexpr int SL = D / 8, L = D / 32;          // slots per row, loads
+    static constexpr int J = D == 192 ? 3 : L / 2;        // loads of 8 rows
+    uint32_t x[J], at[J];                                  // 16 * the slot, bytes of the row r
+
+    __device__ __forceinline__ static int row(int j) { return (64 * j + (int)(threadIdx.x & 63)) / SL; }
+    // stride: elements between rows, at most 2^24
+    __device__ __forceinline__ void init(int64_t stride)
+    {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int r = row(j), pos = (64 * j + (int)(threadIdx.x & 63)) % SL;
+            x[j] = 16u * (uint32_t)((K ? k_slot<D>(r, pos) : v_slot<D == 192 ? 128 : D>(r, pos)) - r * SL);
+            at[j] = (uint32_t)r * (uint32_t)stride * 2u;
+        }
+    }
+    // src: the first of the 16 rows; those from `have` on read as zeros. lds: their first place.
+    __device__ __forceinline__ void load(const uint16_t *src, int64_t stride, int have, const uint8_t *lds) const
+    {
+        const bool whole = have >= 16;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int a = i / J, j = i % J;
+            uint32_t o = (x[j] ^ (K ? (D == 128 ? 128u : 64u) * a : 0u)) + at[j];
+            if (!whole) o = 8 * a + row(j) < have ? o : kAtOut;
+            lds_load16(src, o, 8u * a * (uint32_t)stride * 2u, lds + i * 1024);
+        }
+    }
+};
 #endif
 
 // Waits for this wave's loads and LDS operations, then for the block.
@@ -125,15 +160,15 @@ struct AttRows {
     }
 };
 
-// Whether a V tile in LDS holds a value that is not finite, for the whole wave.
-template <int DV>
+// Whether KEYS rows of a V tile in LDS hold a value that is not finite, for the whole wave.
+template <int DV, int KEYS>
 __device__ __forceinline__ bool v_not_finite(const uint8_t *vt)
 {
     typedef unsigned short h2 __attribute__((ext_vector_type(2)));
     const int lane = threadIdx.x & 63;
     h2 most = h2{0, 0};
 #pragma unroll
-    for (int i = 0; i < kAtKeys * DV * 2 / 1024; ++i) {
+    for (int i = 0; i < KEYS * DV * 2 / 1024; ++i) {
         const u4 w = *reinterpret_cast<const u4 *>(vt + 1024 * i + 16 * lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -266,22 +301,22 @@ __device__ __forceinline__ void att_values(AttRows<DK, DV> &r, const bf8 (&p)[4]
 }
 
 // A weight of zero does not hide an infinity or a NaN in a product. Where a tile that not every row sees holds one, the
-// products are taken without such values (att_values<true>), and this adds them to the rows that see them, one by one.
-// s: the weights.
-template <int DK, int DV>
-__device__ __forceinline__ void att_not_finite(AttRows<DK, DV> &r, const v16f (&s)[2], const uint8_t *vt, uint64_t seen)
+// products are taken without such values (only_finite), and this adds them to the rows that see them, one by one.
+// s: the weights of 32 keys from `key0` of the tile on, bit j of `seen`: whether this lane's row sees the j-th of them.
+template <int DV>
+__device__ __forceinline__ void att_not_finite(v16f (&o)[DV / 32], const v16f &s, const uint8_t *vt, int key0, uint32_t seen)
 {
     const int lane = threadIdx.x & 63, h = lane >> 5;
 #pragma unroll 1
-    for (int j = 0; j < 32; ++j) {
-        float own = s[0][0];
+    for (int j = 0; j < 16; ++j) {
+        float own = s[0];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) own = j == i ? s[i >> 4][i & 15] : own;
+        for (int i = 1; i < 16; ++i) own = j == i ? s[i] : own;
         own = bf16f(at_bf16(own));
         const float other = __shfl_xor(own, 32);
 #pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
-            const int key = 32 * (j >> 4) + 8 * ((j & 15) >> 2) + 4 * hh + (j & 3);
+            const int key = 8 * (j >> 2) + 4 * hh + (j & 3);
             const float w = hh == h ? own : other;
             const bool sees = seen >> key & 1;
 #pragma unroll
@@ -289,11 +324,11 @@ __device__ __forceinline__ void att_not_finite(AttRows<DK, DV> &r, const v16f (&
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
                     const int col = 32 * d + 2 * i + 4 * h;
-                    const uint2 v = *reinterpret_cast<const uint2 *>(vt + 16 * v_slot<DV>(key, col >> 3) + 2 * (col & 7));
+                    const uint2 v = *reinterpret_cast<const uint2 *>(vt + 16 * v_slot<DV>(key0 + key, col >> 3) + 2 * (col & 7));
                     const float f[4] = {bf16f(v.x & 0xffffu), bf16f(v.x >> 16), bf16f(v.y & 0xffffu), bf16f(v.y >> 16)};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        r.o[d][i + e] = sees && !(fabsf(f[e]) < INFINITY) ? fmaf(w, f[e], r.o[d][i + e]) : r.o[d][i + e];
+                        o[d][i + e] = sees && !(fabsf(f[e]) < INFINITY) ? fmaf(w, f[e], o[d][i + e]) : o[d][i + e];
                 }
         }
     }
@@ -381,9 +416,10 @@ __device__ __forceinline__ void att_tile_masked(AttRows<DK, DV> &r, v16f (&s)[2]
     att_raise(r, att_max(s), c);
     bf8 p[4];
     att_weights(p, r, s, c);
-    if (v_not_finite<DV>(vt)) {
+    if (v_not_finite<DV, kAtKeys>(vt)) {
         att_values<true>(r, p, vt);
-        att_not_finite(r, s, vt, seen);
+        att_not_finite<DV>(r.o, s[0], vt, 0, (uint32_t)seen);
+        att_not_finite<DV>(r.o, s[1], vt, 32, (uint32_t)(seen >> 32));
     } else {
         att_values<false>(r, p, vt);
     }

@@ -4,21 +4,26 @@
 // over the context and the drafted tokens whose bits are set in i's word.
 //
 // The rows that share a key/value head, (token, head of the group), are one
-// matrix: 128 of them per block. The work is a line of units, a unit being 64
-// keys of one (sequence, key/value head, 128 rows), cut into equal runs, one
-// per block, so that sequences of any lengths fill the card alike. What a run
+// matrix: 32 or 64 of them per block. The work is a line of units, a unit being
+// 64 keys of one (sequence, key/value head, block of rows), cut into equal runs,
+// one per block, so that sequences of any lengths fill the card alike. What a run
 // holds whole is written at once; cut ends (two per block at most) go to the
 // workspace as unnormalised sums with their maximum, and a second kernel joins
 // them in their order.
+//
+// Bound by the cache's bytes: every wave holds all rows of its block and reads
+// tiles of 32 keys of its own, every fourth of the run, through its own part of
+// the LDS, so nothing waits for another wave until a segment ends and the four
+// waves' sums are added.
 #include "k3moe_attn.h"
 
 namespace k3moe {
 namespace {
 
-constexpr int kTrWaves = 4, kTrRows = kTrWaves * kAtRows;
-constexpr int kTrBlocks = 512;   // runs: two blocks of 80 KB of LDS or less per CU
-constexpr int kTrLeast = 2;      // units of a run at least
-constexpr int kTrMaxDraft = 64;  // bits of a word
+constexpr int kTrWaves = 4, kTrTile = 32;   // keys of a wave's tile
+constexpr int kTrLeast = 2;                 // units of a run at least: a tile for each wave
+constexpr int kTrMaxDraft = 64;             // bits of a word
+constexpr int kTrMaxRuns = 512, kTrMaxRows = 64;
 
 struct TreeParams {
     const uint16_t *q;
@@ -26,16 +31,17 @@ struct TreeParams {
     const int32_t *pages, *lens, *cu;
     const uint64_t *tree;
     uint16_t *out;
-    float *lse, *part, *ml;   // part [2 kTrBlocks][rows][DV], ml [2 kTrBlocks][rows][2]
+    float *lse, *part, *ml;   // part [2 runs][rows][DV], ml [2 runs][rows][2]
     int64_t qs, os;
     int seqs, Tq, maxq, Hq, Hkv, group, n_pages, lpage, width;
+    int runs, rows;           // blocks, rows of a block
     float scale;
 };
 
 // What a sequence has to do.
 struct TreeSeq {
-    int q0, n, ctx, keys, kt, rt;   // first row, drafted tokens, context, keys, tiles of keys and of rows
-    int64_t units;
+    int q0, n, ctx, keys, kt, rt;   // first row, drafted tokens, context, keys, tiles of keys and blocks of rows
+    int units;
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b)
@@ -54,71 +60,65 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b)
     s.ctx = max(p.lens[b], 0);
     s.keys = (int)min((int64_t)s.ctx + s.n, (int64_t)p.width << p.lpage);
     s.kt = max(1, (s.keys + kAtKeys - 1) / kAtKeys);   // a row without a key is written too
-    s.rt = (s.n * p.group + kTrRows - 1) / kTrRows;
-    s.units = (int64_t)p.Hkv * s.rt * s.kt;
+    s.rt = (s.n * p.group + p.rows - 1) / p.rows;
+    s.units = p.Hkv * s.rt * s.kt;                     // the host has checked that their sum fits
     return s;
 }
 
-__device__ __forceinline__ int64_t shfl_up64(int64_t v, int o)
+// The sum over the lanes up to and with this one.
+__device__ __forceinline__ int wave_scan(int v)
 {
-    const uint32_t lo = __shfl_up((uint32_t)v, o), hi = __shfl_up((uint32_t)(v >> 32), o);
-    return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-__device__ __forceinline__ int64_t lane64(int64_t v, int l)
-{
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, l);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), l);
-    return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
-// Units of the sequences b0 .. b0 + 63 up to and with this lane's.
-__device__ __forceinline__ int64_t tree_scan(const TreeSeq &s)
-{
-    const int lane = threadIdx.x & 63;
-    int64_t upto = s.units;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int64_t x = shfl_up64(upto, o);
-        if (lane >= o) upto += x;
-    }
-    return upto;
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // one lane to the right, within a row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row 0 into 1, 2 into 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row 1 into 2 and 3
+    return v;
 }
 
-__device__ __forceinline__ int64_t run_length(int64_t units)
+__device__ __forceinline__ int run_length(const TreeParams &p, int units)
 {
-    const int64_t r = (units + kTrBlocks - 1) / kTrBlocks;
-    return r < kTrLeast ? kTrLeast : r;
+    return max((units + p.runs - 1) / p.runs, kTrLeast);
 }
 
-// The sum over all sequences, and (find >= 0) the sequence that holds unit `find` with the units in front of it.
-__device__ __forceinline__ int64_t tree_total(const TreeParams &p)
+// The line of units: its length, the length of a run, and for unit run * number the sequence that holds it with the
+// units in front of that sequence (b < 0: the line is shorter). 64 sequences at a time; up to 64 are looked at once.
+struct TreePlan {
+    int total, per, b, front;
+};
+__device__ __forceinline__ TreePlan tree_plan(const TreeParams &p, int number)
 {
     const int lane = threadIdx.x & 63;
-    int64_t total = 0;
-    for (int b0 = 0; b0 < p.seqs; b0 += 64) total += lane64(tree_scan(tree_seq(p, b0 + lane)), 63);
-    return total;
-}
-__device__ __forceinline__ int tree_find(const TreeParams &p, int64_t unit, int64_t &front)
-{
-    const int lane = threadIdx.x & 63;
-    front = 0;
+    TreePlan r{0, 0, -1, 0};
+    int units = 0, upto = 0;
     for (int b0 = 0; b0 < p.seqs; b0 += 64) {
-        const TreeSeq s = tree_seq(p, b0 + lane);
-        const int64_t upto = tree_scan(s) + front;
+        units = tree_seq(p, b0 + lane).units;
+        upto = wave_scan(units) + r.total;
+        r.total = __builtin_amdgcn_readlane(upto, 63);
+    }
+    r.per = run_length(p, r.total);
+    const int64_t unit = (int64_t)r.per * number;
+    if (unit >= r.total) return r;
+    int before = 0;
+    for (int b0 = 0; b0 < p.seqs; b0 += 64) {
+        if (p.seqs > 64) {
+            units = tree_seq(p, b0 + lane).units;
+            upto = wave_scan(units) + before;
+        }
         const uint64_t past = __ballot(upto > unit);
         if (past) {
             const int at = __builtin_ctzll(past);
-            front = lane64(upto - s.units, at);
-            return b0 + at;
+            r.b = b0 + at;
+            r.front = __builtin_amdgcn_readlane(upto - units, at);
+            return r;
         }
-        front = lane64(upto, 63);
+        before = __builtin_amdgcn_readlane(upto, 63);
     }
-    return -1;
+    return r;
 }
 
 #ifdef __HIP_DEVICE_COMPILE__
-typedef __attribute__((address_space(3))) void lds_void;
-
 __device__ __forceinline__ u4 expand_pair(uint32_t lo, uint32_t hi, float f)
 {
     const bf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, true);
@@ -129,189 +129,317 @@ __device__ __forceinline__ u4 expand_pair(uint32_t lo, uint32_t hi, float f)
     return r;
 }
 
-// One side (keys or values) of the cache: a wave stages its 16 rows of a tile, all in one page.
-template <int D, bool X8>
-struct PageStage {
-    u4 w[X8 ? D / 64 : 1];
-    uint32_t sc[X8 ? D / 64 : 1];
+// 16 rows of MXFP8 values on their way through registers: 16 codes and their group's byte per lane and load.
+template <int D>
+struct ByteStage {
+    static constexpr int L = D / 64;
+    u4 w[L];
+    uint32_t sc[L];
 
-    // base: the head's rows of the page from this wave's first on; rows: how many of the 16 exist
-    template <class Slot>
-    __device__ __forceinline__ void issue(const uint8_t *base, const uint8_t *sbase, int rows, const uint8_t *lds, Slot slot)
+    __device__ __forceinline__ void load(const uint8_t *rows, const uint8_t *bytes, int have)
     {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, kAtOut, 0x00020000);
-        if constexpr (!X8) {
-            constexpr int SL = D / 8, N = 16 * SL / 64;
+        const int lane = threadIdx.x & 63;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(rows), 0, kAtOut, 0x00020000);
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(bytes), 0, kAtOut, 0x00020000);
+        typedef unsigned u4v __attribute__((ext_vector_type(4)));
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = (wave * N + i) * 64 + lane, row = at / SL, s = slot(row, at % SL) - row * SL, r16 = row - 16 * wave;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + (wave * N + i) * 1024), 16,
-                                                         (int)(r16 < rows ? (uint32_t)(r16 * D * 2 + 16 * s) : kAtOut), 0, 0, 0);
-            }
-        } else {
-            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(sbase), 0, kAtOut, 0x00020000);
-            typedef unsigned u4v __attribute__((ext_vector_type(4)));
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const int at = 64 * i + lane, row = at / (D / 16), sub = at % (D / 16);
-                const u4v x = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(row < rows ? (uint32_t)(16 * at) : kAtOut), 0, 0);
-                w[i] = u4{x[0], x[1], x[2], x[3]};
-                sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(row < rows ? (uint32_t)(row * (D / 32) + sub / 2) : kAtOut), 0, 0);
-            }
+        for (int i = 0; i < L; ++i) {
+            const int at = 64 * i + lane, row = at / (D / 16), sub = at % (D / 16);
+            const u4v x = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(row < have ? (uint32_t)(16 * at) : kAtOut), 0, 0);
+            w[i] = u4{x[0], x[1], x[2], x[3]};
+            sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(row < have ? (uint32_t)(row * (D / 32) + sub / 2) : kAtOut), 0, 0);
         }
     }
+    // As bf16 into rows row0 .. row0 + 15 of a tile.
     template <class Slot>
-    __device__ __forceinline__ void commit(uint8_t *lds, Slot slot)
+    __device__ __forceinline__ void store(uint8_t *tile, int row0, Slot slot) const
     {
-        if constexpr (X8) {
-            const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int lane = threadIdx.x & 63;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const int at = 64 * i + lane, row = 16 * wave + at / (D / 16), sub = at % (D / 16);
-                const bool drop = sc[i] == 255u;   // such a group is zero, whatever its codes
-                const float f = e8m0_to_f32(sc[i]);
-                const u4 x = drop ? u4{0u, 0u, 0u, 0u} : w[i];
-                *reinterpret_cast<u4 *>(lds + 16 * slot(row, 2 * sub)) = expand_pair(x.x, x.y, f);
-                *reinterpret_cast<u4 *>(lds + 16 * slot(row, 2 * sub + 1)) = expand_pair(x.z, x.w, f);
-            }
+        for (int i = 0; i < L; ++i) {
+            const int at = 64 * i + lane, row = row0 + at / (D / 16), sub = at % (D / 16);
+            const bool drop = sc[i] == 255u;   // such a group is zero, whatever its codes
+            const float f = e8m0_to_f32(sc[i]);
+            const u4 x = drop ? u4{0u, 0u, 0u, 0u} : w[i];
+            *reinterpret_cast<u4 *>(tile + 16 * slot(row, 2 * sub)) = expand_pair(x.x, x.y, f);
+            *reinterpret_cast<u4 *>(tile + 16 * slot(row, 2 * sub + 1)) = expand_pair(x.z, x.w, f);
         }
     }
 };
+
+template <int N>
+__device__ __forceinline__ void wait_loads()   // all but the last N loads
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 #endif
 
-template <int DK, int DV, bool X8>
-__global__ __launch_bounds__(64 * kTrWaves, 2) void k_tree(TreeParams p)
+// NC * 32 rows per block.
+template <int DK, int DV, bool X8, int NC>
+struct TreeShape {
+    static constexpr int KB = kTrTile * DK * 2, VB = kTrTile * DV * 2;   // a wave's tile
+    static constexpr int kBufs = X8 ? 1 : 2;
+    static constexpr int kTiles = kTrWaves * kBufs * (KB + VB), kSums = kTrWaves * (DV / 2 + 1) * 64 * 4;
+    static constexpr int kLds = kTiles > kSums ? kTiles : kSums;          // the waves' sums take the tiles' place
+    // blocks that fit a CU: by LDS, and by registers where the accumulators leave room for a second wave per SIMD
+    static constexpr int kPerCu = kLds <= 80 * 1024 && NC == 1 ? 2 : 1;
+};
+
+template <int DK, int DV, bool X8, int NC>
+__global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8, NC>::kPerCu)) void k_tree(TreeParams p)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    constexpr int KB = kAtKeys * DK * 2, VB = kAtKeys * DV * 2, EB = X8 ? 1 : 2;
+    typedef TreeShape<DK, DV, X8, NC> S;
+    constexpr int KB = S::KB, VB = S::VB, EB = X8 ? 1 : 2;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, l32 = lane & 31;
-    const int64_t total = tree_total(p), per = run_length(total);
-    int64_t u = per * blockIdx.x;
-    const int64_t end = min(u + per, total);
-    if (u >= end) return;
-    int64_t front;
-    int b = tree_find(p, u, front);
+    const TreePlan plan = tree_plan(p, (int)blockIdx.x);
+    if (plan.b < 0) return;
+    int u = plan.per * (int)blockIdx.x, b = plan.b, front = plan.front;
+    const int end = min(u + plan.per, plan.total);
     TreeSeq s = tree_seq(p, b);
     const int page = 1 << p.lpage;
     const float c = p.scale * kLog2e;
+    uint8_t *mine = lds + wave * S::kBufs * (KB + VB);      // this wave's tiles
+
+    // lane parts of the fragments' addresses
+    const uint32_t krow = (uint32_t)(l32 * DK * 2), kx = 16u * (uint32_t)(k_slot<DK>(l32, h) - l32 * (DK / 8));
+    const int vr = 4 * h + ((lane & 15) >> 2), vcol = (lane & 16) + 4 * (lane & 3);
+    const uint32_t vrow = (uint32_t)(vr * DV * 2 + 2 * vcol), vx = 16u * (uint32_t)(v_slot<DV>(vr, 0) - vr * (DV / 8));
+    RowStage<DK, true> sk;
+    RowStage<DV, false> sv;
+    ByteStage<DK> bk[2];
+    ByteStage<DV> bv[2];
+    if constexpr (!X8) sk.init(DK), sv.init(DV);
 
     while (true) {
-        // the segment that holds unit u: tiles t0 .. t1 of (b, kvh, rows)
-        const int64_t in = u - front;
-        const int seg = (int)(in / s.kt), t0 = (int)(in - (int64_t)seg * s.kt);
-        const int kvh = seg / s.rt, rows0 = (seg - kvh * s.rt) * kTrRows;
-        const int t1 = (int)min((int64_t)s.kt, t0 + (end - u));
+        // the segment that holds unit u: tiles t0 .. t1 (of 64 keys) of (b, kvh, rows)
+        const int in = u - front, seg = in / s.kt, t0 = in - seg * s.kt;
+        const int kvh = seg / s.rt, rows0 = (seg - kvh * s.rt) * 32 * NC;
+        const int t1 = min(s.kt, t0 + (end - u));
+        const int j1 = min(2 * t1, (s.keys + kTrTile - 1) / kTrTile);   // tiles of 32 keys
 
-        const int m = rows0 + kAtRows * wave + l32;                 // (token, head of the group)
-        const int i = min(m / p.group, s.n - 1), head = kvh * p.group + m % p.group;
-        const bool have = m < s.n * p.group, busy = rows0 + kAtRows * wave < s.n * p.group;
-        const uint64_t word = (p.tree ? p.tree[s.q0 + i] : low_bits(i + 1)) & low_bits(s.n);
-        AttRows<DK, DV> r;
-        {
-            const uint16_t *qp = p.q + (int64_t)(s.q0 + i) * p.qs + (int64_t)head * DK + 8 * h;
+        // this lane's rows: (token, head of the group)
+        int tok[NC], head[NC];
+        bool have[NC];
+        uint64_t word[NC];
+        bf8 q[NC][DK / 16];
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k) r.q[k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
+        for (int n = 0; n < NC; ++n) {
+            const int m = rows0 + 32 * n + l32;
+            have[n] = m < s.n * p.group;
+            tok[n] = min(m / p.group, s.n - 1), head[n] = kvh * p.group + m % p.group;
+            const uint16_t *qp = p.q + (int64_t)(s.q0 + tok[n]) * p.qs + (int64_t)head[n] * DK + 8 * h;
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) q[n][k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
+            word[n] = (p.tree ? p.tree[s.q0 + tok[n]] : low_bits(tok[n] + 1)) & low_bits(s.n);
         }
-        r.clear();
-
-        // page numbers of a tile's four runs of 16 keys, and which of them are in the cache
-        const int32_t *table = p.pages + (int64_t)b * p.width;
-        auto lookup = [&](int t, int &own) {   // own: the page of this wave's rows, -1: none
-            uint32_t ok = 0;
-            own = -1;
+        v16f o[NC][DV / 32];
+        float mx[NC], l[NC];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int pos = t * kAtKeys + 16 * g;
-                const int id = pos < s.keys ? __builtin_amdgcn_readfirstlane(table[pos >> p.lpage]) : -1;
-                const bool in_cache = id >= 0 && id < p.n_pages;
-                ok |= in_cache ? 1u << g : 0u;
-                if (g == wave) own = in_cache ? id : -1;
-            }
-            return ok;
-        };
-        PageStage<DK, X8> sk;
-        PageStage<DV, X8> sv;
-        // Keys run a tile ahead of the values: tile t's scores are there before its weights are taken. What goes through
-        // registers (8-bit pages) is written behind the tile's work, before the barrier in front of its use.
-        auto where = [&](int t, int own, int &rows) {
-            const int pos = t * kAtKeys + 16 * wave;
-            rows = own < 0 ? 0 : min(s.keys - pos, 16);
-            return ((int64_t)max(own, 0) * p.Hkv + kvh) * page + (pos & (page - 1));
-        };
-        auto issue_k = [&](int t, int own) {
-            int rows;
-            const int64_t row = where(t, own, rows);
-            sk.issue(p.kc + row * DK * EB, X8 ? p.ks + row * (DK / 32) : nullptr, rows, lds + ((t - t0) & 1) * KB, k_slot<DK>);
-        };
-        auto issue_v = [&](int t, int own) {
-            int rows;
-            const int64_t row = where(t, own, rows);
-            sv.issue(p.vc + row * DV * EB, X8 ? p.vs + row * (DV / 32) : nullptr, rows, lds + 2 * KB + ((t - t0) & 1) * VB, v_slot<DV>);
-        };
-        auto commit_k = [&](int t) { sk.commit(lds + ((t - t0) & 1) * KB, k_slot<DK>); };
-        auto commit_v = [&](int t) { sv.commit(lds + 2 * KB + ((t - t0) & 1) * VB, v_slot<DV>); };
-
-        at_barrier();       // the last segment's tiles are read
-        int own0, own1 = -1, own2 = -1;            // this wave's pages of tiles t, t + 1, t + 2
-        uint32_t ok = lookup(t0, own0), ok1 = 0;
-        if (t0 + 1 < t1) ok1 = lookup(t0 + 1, own1);
-        issue_k(t0, own0), issue_v(t0, own0);
-        commit_k(t0), commit_v(t0);
-        if (t0 + 1 < t1) issue_k(t0 + 1, own1), commit_k(t0 + 1);
-        at_barrier();
-        v16f sc[2];
-        if (busy) att_scores(sc, r, lds);
-        for (int t = t0; t < t1; ++t) {
-            const int first = t * kAtKeys;
-            uint32_t ok2 = 0;
-            at_barrier();
-            if (t + 2 < t1) ok2 = lookup(t + 2, own2), issue_k(t + 2, own2);
-            if (t + 1 < t1) issue_v(t + 1, own1);
-            if (busy) {
-                const uint8_t *nk = lds + ((t + 1 - t0) & 1) * KB, *vt = lds + 2 * KB + ((t - t0) & 1) * VB;
-                const int a = s.ctx - first;   // the tile's keys in front of the drafted ones
-                uint64_t seen = low_bits(a) | (a >= 64 || a <= -64 ? 0ull : a >= 0 ? word << a : word >> -a);
-                seen &= low_bits(s.keys - first);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) seen &= ok >> g & 1 ? ~0ull : ~(0xffffull << (16 * g));
-                att_tile_masked(r, sc, nk, vt, c, seen);
-            }
-            if (t + 2 < t1) commit_k(t + 2);
-            if (t + 1 < t1) commit_v(t + 1);
-            ok = ok1, ok1 = ok2, own1 = own2;
-        }
-
-        const float l = r.l + __shfl_xor(r.l, 32);
-        if (t0 == 0 && t1 == s.kt) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (have) {
-                if (p.lse && h == 0)
-                    p.lse[(int64_t)(s.q0 + i) * p.Hq + head] = l == 0.0f ? -INFINITY : fmaf(r.m, c, __log2f(l)) * kLn2;
-                uint16_t *op = p.out + (int64_t)(s.q0 + i) * p.os + (int64_t)head * DV + 4 * h;
-#pragma unroll
-                for (int d = 0; d < DV / 32; ++d)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *reinterpret_cast<uint2 *>(op + 32 * d + 2 * e) = uint2{
-                            at_bf16(r.o[d][e] * inv) | (at_bf16(r.o[d][e + 1] * inv) << 16),
-                            at_bf16(r.o[d][e + 2] * inv) | (at_bf16(r.o[d][e + 3] * inv) << 16)};
-            }
-        } else if (have) {
-            // a run cut in front goes to the block's first place, one cut behind only to its second
-            const int64_t at = (int64_t)(2 * blockIdx.x + (t0 == 0)) * kTrRows + (m - rows0);
-            float *op = p.part + at * DV + 4 * h;
+        for (int n = 0; n < NC; ++n) {
+            mx[n] = -INFINITY, l[n] = 0.0f;
 #pragma unroll
             for (int d = 0; d < DV / 32; ++d)
 #pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<float4 *>(op + 32 * d + 2 * e) = float4{r.o[d][e], r.o[d][e + 1], r.o[d][e + 2], r.o[d][e + 3]};
-            if (h == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = float2{r.m * c, l};   // c > 0: -inf stays
+                for (int i = 0; i < 16; ++i) o[n][d][i] = 0.0f;
+        }
+
+        // Page numbers of this wave's next 32 tiles, two (of 16 keys) each, a lane holds one; -1: no such key or page.
+        const int32_t *table = p.pages + (int64_t)b * p.width;
+        int ids = -1, ids_from = 0;
+        auto look = [&](int j) {
+            ids_from = j;
+            const int64_t pos = ((int64_t)j + kTrWaves * (lane >> 1)) * kTrTile + 16 * (lane & 1);
+            ids = pos < s.keys ? table[pos >> p.lpage] : -1;
+            if (ids >= p.n_pages) ids = -1;
+        };
+        auto id_of = [&](int j, int g) { return __builtin_amdgcn_readlane(ids, 2 * ((j - ids_from) / kTrWaves) + g); };
+        uint32_t ok = 0, ok_next = 0;                      // which of a tile's two runs of 16 keys are in the cache
+        auto load = [&](int j, int buf) {
+            if (j >= ids_from + 32 * kTrWaves) look(j);
+            ok_next = 0;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int id = id_of(j, g), pos = j * kTrTile + 16 * g;
+                const int rows = id < 0 ? 0 : min(s.keys - pos, 16);
+                ok_next |= id < 0 ? 0u : 0xffffu << (16 * g);
+                const int64_t row = ((int64_t)max(id, 0) * p.Hkv + kvh) * page + (pos & (page - 1));
+                if constexpr (X8) {
+                    bk[g].load(p.kc + row * DK, p.ks + row * (DK / 32), rows);
+                    bv[g].load(p.vc + row * DV, p.vs + row * (DV / 32), rows);
+                } else {
+                    uint8_t *at = mine + buf * (KB + VB);
+                    sk.load(reinterpret_cast<const uint16_t *>(p.kc + row * DK * EB), DK, rows, at + 16 * g * DK * 2);
+                    sv.load(reinterpret_cast<const uint16_t *>(p.vc + row * DV * EB), DV, rows, at + KB + 16 * g * DV * 2);
+                }
+            }
+        };
+
+        int j = 2 * t0 + wave, buf = 0;
+        if (j < j1) {
+            look(j);
+            load(j, 0);
+        }
+        for (; j < j1; j += kTrWaves) {
+            const uint8_t *kt = mine + buf * (KB + VB), *vt = kt + KB;
+            ok = ok_next;
+            const bool more = j + kTrWaves < j1;
+            if constexpr (X8) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    bk[g].store(mine, 16 * g, k_slot<DK>);
+                    bv[g].store(mine + KB, 16 * g, v_slot<DV>);
+                }
+                if (more) load(j + kTrWaves, 0);
+                wave_lds_sync();
+            } else {
+                if (more) {
+                    wave_lds_sync();                        // the other buffer is read
+                    load(j + kTrWaves, buf ^ 1);
+                    wait_loads<2 * (DK + DV) / 32>();
+                } else {
+                    wait_loads<0>();
+                }
+                buf ^= 1;
+            }
+            // scores
+            v16f sc[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[n][i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) {
+                const bf8 a = as_bf8(*reinterpret_cast<const u4 *>(kt + krow + (kx ^ (32u * k))));
+#pragma unroll
+                for (int n = 0; n < NC; ++n) sc[n] = mfma32(a, q[n][k], sc[n]);
+            }
+            const int first = j * kTrTile, ahead = s.ctx - first;   // the tile's keys in front of the drafted ones
+            const bool whole = ahead >= kTrTile && ok == ~0u;
+            uint32_t seen[NC];
+            bool bad = false;
+            bf8 pw[NC][2];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                seen[n] = ~0u;
+                if (!whole) {
+                    uint64_t see = low_bits(ahead) | (ahead >= 64 || ahead <= -64 ? 0ull : ahead >= 0 ? word[n] << ahead : word[n] >> -ahead);
+                    see &= low_bits(s.keys - first);
+                    seen[n] = (uint32_t)see & ok;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sc[n][i] = (seen[n] >> (4 * h)) & (1u << (8 * (i >> 2) + (i & 3))) ? sc[n][i] : -INFINITY;
+                }
+                float m = sc[n][0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) m = fmaxf(m, sc[n][i]);
+                m = swap_max(m);
+                if (__ballot((m - mx[n]) * c > kAtSlack)) {
+                    const float mn = fmaxf(mx[n], m);
+                    const float f = mx[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx[n] - mn) * c);
+                    mx[n] = mn, l[n] *= f;
+#pragma unroll
+                    for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[n][d][i] *= f;
+                }
+                const float mc = mx[n] == -INFINITY ? 0.0f : mx[n] * c;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    sc[n][i] = __builtin_amdgcn_exp2f(fmaf(sc[n][i], c, -mc));
+                    l[n] += sc[n][i];
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    pw[n][k] = as_bf8(u4{at_pack(sc[n][8 * k], sc[n][8 * k + 1]), at_pack(sc[n][8 * k + 2], sc[n][8 * k + 3]),
+                                         at_pack(sc[n][8 * k + 4], sc[n][8 * k + 5]), at_pack(sc[n][8 * k + 6], sc[n][8 * k + 7])});
+            }
+            if (!whole) bad = v_not_finite<DV, kTrTile>(vt);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int d = 0; d < DV / 32; ++d) {
+                    const uint8_t *at = vt + (vrow + (vx ^ (64u * d))) + 32 * k * DV;
+                    const s4 a0 = lds_tr(at), a1 = lds_tr(at + 16 * DV);
+                    bf8 a;
+                    __builtin_memcpy(&a, &a0, 8);
+                    __builtin_memcpy(reinterpret_cast<char *>(&a) + 8, &a1, 8);
+                    if (bad) a = only_finite(a);
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) o[n][d] = mfma32(a, pw[n][k], o[n][d]);
+                }
+            if (bad) {
+#pragma unroll
+                for (int n = 0; n < NC; ++n) att_not_finite<DV>(o[n], sc[n], vt, 0, seen[n]);
+            }
+            if constexpr (X8) wave_lds_sync();   // the tile is read
+        }
+
+        // The four waves' sums: all rows' maxima first, then each wave adds a quarter of the dimensions.
+        const bool complete = t0 == 0 && t1 == s.kt;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            constexpr int R = DV / 2, RW = R / kTrWaves;   // a row's values per lane, and per wave
+            float *sums = reinterpret_cast<float *>(lds), *ml = sums + kTrWaves * R * 64;
+            const float lw = l[n] + __shfl_xor(l[n], 32);
+            at_barrier();                                  // the tiles, or the last sums, are read
+            if (h == 0) ml[wave * 64 + l32] = mx[n], ml[wave * 64 + 32 + l32] = lw;
+            at_barrier();
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kTrWaves; ++w) M = fmaxf(M, ml[w * 64 + l32]);
+            float L = 0.0f, f = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kTrWaves; ++w) {
+                const float m = ml[w * 64 + l32], x = ml[w * 64 + 32 + l32];
+                const float g = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - M) * c);
+                L += m == -INFINITY ? x : x * g;           // without a score above -inf: 0, or NaN
+                f = w == wave ? g : f;
+            }
+#pragma unroll
+            for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sums[(wave * R + 16 * d + i) * 64 + lane] = o[n][d][i] * f;
+            at_barrier();
+            float v[RW];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                v[i] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kTrWaves; ++w) v[i] += sums[(w * R + RW * wave + i) * 64 + lane];
+            }
+            // register e of a row holds dimension 32 (e / 16) + 8 (e % 16 / 4) + 4 h + e % 4
+            const int e0 = RW * wave;
+            if (have[n]) {
+                if (complete) {
+                    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                    if (p.lse && h == 0 && wave == 0)
+                        p.lse[(int64_t)(s.q0 + tok[n]) * p.Hq + head[n]] = L == 0.0f ? -INFINITY : fmaf(M, c, __log2f(L)) * kLn2;
+                    uint16_t *op = p.out + (int64_t)(s.q0 + tok[n]) * p.os + (int64_t)head[n] * DV + 4 * h;
+#pragma unroll
+                    for (int i = 0; i < RW; i += 4) {
+                        const int e = e0 + i;
+                        *reinterpret_cast<uint2 *>(op + 32 * (e >> 4) + 2 * (e & 15)) =
+                            uint2{at_bf16(v[i] * inv) | (at_bf16(v[i + 1] * inv) << 16), at_bf16(v[i + 2] * inv) | (at_bf16(v[i + 3] * inv) << 16)};
+                    }
+                } else {
+                    // a segment cut in front goes to the block's first place, one cut behind only to its second
+                    const int64_t at = (int64_t)(2 * (int)blockIdx.x + (t0 == 0)) * p.rows + 32 * n + l32;
+                    float *op = p.part + at * DV + 4 * h;
+#pragma unroll
+                    for (int i = 0; i < RW; i += 4) {
+                        const int e = e0 + i;
+                        *reinterpret_cast<float4 *>(op + 32 * (e >> 4) + 2 * (e & 15)) = float4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+                    }
+                    if (h == 0 && wave == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = float2{M * c, L};   // c > 0: -inf stays
+                }
+            }
         }
 
         u += t1 - t0;
         if (u >= end) return;
+        at_barrier();                                      // the sums are read
         while (u >= front + s.units) {
             front += s.units;
             s = tree_seq(p, ++b);
@@ -320,71 +448,73 @@ __global__ __launch_bounds__(64 * kTrWaves, 2) void k_tree(TreeParams p)
 #endif
 }
 
-// Joins the cut ends: one wave per (drafted token, head).
+// Joins the cut ends. Block (w, y): if the end of run w - 1 is the first one within its segment, the rows 16 y .. of
+// that segment, four dimensions per thread.
 template <int DV>
 __global__ __launch_bounds__(256) void k_tree_join(TreeParams p)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (item >= (int64_t)p.Tq * p.Hq) return;
-    const int t = (int)(item / p.Hq), head = (int)(item % p.Hq);
-
-    int64_t total = 0, front = -1;
-    TreeSeq s{};
-    for (int b0 = 0; b0 < p.seqs; b0 += 64) {
-        const TreeSeq x = tree_seq(p, b0 + lane);
-        const int64_t upto = tree_scan(x) + total;
-        const uint64_t mine = __ballot(t >= x.q0 && t < x.q0 + x.n);
-        if (mine && front < 0) {
-            const int at = __builtin_ctzll(mine);
-            front = lane64(upto - x.units, at);
-            s = tree_seq(p, b0 + at);
-        }
-        total = lane64(upto, 63);
-    }
-    if (front < 0) return;   // a row of no sequence
-    const int64_t per = run_length(total);
-    const int m = (t - s.q0) * p.group + head % p.group, rt = m / kTrRows;
-    const int64_t u0 = front + ((int64_t)(head / p.group) * s.rt + rt) * s.kt, u1 = u0 + s.kt;
-    const int w0 = (int)(u0 / per), w1 = (int)((u1 - 1) / per);
-    if (w0 == w1) return;    // written whole
-    auto place = [&](int w) { return ((int64_t)(2 * w + (w == w0)) * kTrRows + (m - rt * kTrRows)); };
-    // 64 runs at a time: their maxima and sums, then their sums of values
+    constexpr int TR = DV / 4, RB = 256 / TR;             // threads of a row, rows at a time
+    const int w = (int)blockIdx.x + 1;
+    const TreePlan plan = tree_plan(p, w);
+    if (plan.b < 0) return;
+    const int u = plan.per * w;
+    const TreeSeq s = tree_seq(p, plan.b);
+    const int seg = (u - plan.front) / s.kt, u0 = plan.front + seg * s.kt;
+    if (u == u0 || u - plan.per > u0) return;             // no cut, or not the segment's first
+    const int kvh = seg / s.rt, rows0 = (seg - kvh * s.rt) * p.rows;
+    const int w0 = w - 1, w1 = (u0 + s.kt - 1) / plan.per;
+    const int row = (int)blockIdx.y * RB + (int)threadIdx.x / TR, e = 4 * ((int)threadIdx.x % TR);
+    const int m = rows0 + row;
+    if (row >= p.rows || m >= s.n * p.group) return;
+    auto place = [&](int r) { return (int64_t)(2 * r + (r == w0 && u0 >= r * plan.per)) * p.rows + row; };
     float mx = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 64) mx = fmaxf(mx, p.ml[2 * place(w)]);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+    for (int r = w0; r <= w1; ++r) mx = fmaxf(mx, p.ml[2 * place(r)]);
     const float use = mx == -INFINITY ? 0.0f : mx;
-    float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-    for (int w = w0; w <= w1; ++w) {
-        const int64_t at = place(w);
-        const float f = __builtin_amdgcn_exp2f(p.ml[2 * at] - use);
-        l = fmaf(p.ml[2 * at + 1], f, l);
-        o0 = fmaf(p.part[at * DV + lane], f, o0);
-        if constexpr (DV == 128) o1 = fmaf(p.part[at * DV + 64 + lane], f, o1);
+    float l = 0.0f;
+    float4 o = float4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int r = w0; r <= w1; ++r) {
+        const int64_t at = place(r);
+        const float2 x = *reinterpret_cast<const float2 *>(p.ml + 2 * at);
+        const float4 v = *reinterpret_cast<const float4 *>(p.part + at * DV + e);
+        const float f = x.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x.x - use);
+        l += x.x == -INFINITY ? x.y : x.y * f;            // without a score above -inf: 0, or NaN
+        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *op = p.out + (int64_t)t * p.os + (int64_t)head * DV;
-    op[lane] = (uint16_t)at_bf16(o0 * inv);
-    if constexpr (DV == 128) op[64 + lane] = (uint16_t)at_bf16(o1 * inv);
-    if (p.lse && lane == 0) p.lse[(int64_t)t * p.Hq + head] = l == 0.0f ? -INFINITY : (use + __log2f(l)) * kLn2;
+    const int64_t t = s.q0 + m / p.group;
+    const int head = kvh * p.group + m % p.group;
+    *reinterpret_cast<uint2 *>(p.out + t * p.os + (int64_t)head * DV + e) =
+        uint2{at_bf16(o.x * inv) | (at_bf16(o.y * inv) << 16), at_bf16(o.z * inv) | (at_bf16(o.w * inv) << 16)};
+    if (p.lse && e == 0) p.lse[t * p.Hq + head] = l == 0.0f ? -INFINITY : (use + __log2f(l)) * kLn2;
 }
 
-template <int DK, int DV, bool X8>
-k3moe_status launch(const TreeParams &p, hipStream_t s)
+template <int DK, int DV, bool X8, int NC>
+k3moe_status launch(TreeParams p, hipStream_t s)
 {
-    constexpr int lds = 2 * kAtKeys * (DK + DV) * 2;
+    typedef TreeShape<DK, DV, X8, NC> S;
     static const hipError_t allowed =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(k_tree<DK, DV, X8>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        hipFuncSetAttribute(reinterpret_cast<const void *>(k_tree<DK, DV, X8, NC>), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
     if (allowed != hipSuccess) return K3MOE_E_HIP;
-    k_tree<DK, DV, X8><<<kTrBlocks, 64 * kTrWaves, lds, s>>>(p);
-    k_tree_join<DV><<<(unsigned)(((int64_t)p.Tq * p.Hq + 3) / 4), 256, 0, s>>>(p);
+    p.runs = 256 * S::kPerCu, p.rows = 32 * NC;
+    p.ml = p.part + (size_t)2 * p.runs * p.rows * DV;
+    k_tree<DK, DV, X8, NC><<<(unsigned)p.runs, 64 * kTrWaves, S::kLds, s>>>(p);
+    k_tree_join<DV><<<dim3((unsigned)p.runs - 1, (unsigned)(p.rows / (1024 / DV))), 256, 0, s>>>(p);
     return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
+}
+
+template <int DK, int DV>
+k3moe_status launch(const TreeParams &p, bool x8, hipStream_t s)
+{
+    const bool few = p.maxq * (int64_t)p.group <= 32;
+    if (x8) return few ? launch<DK, DV, true, 1>(p, s) : launch<DK, DV, true, 2>(p, s);
+    return few ? launch<DK, DV, false, 1>(p, s) : launch<DK, DV, false, 2>(p, s);
 }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-size_t ws_bytes(int v_dim) { return (size_t)2 * kTrBlocks * kTrRows * (size_t)(v_dim + 2) * 4; }
+// For the most runs and rows that any variant has.
+size_t ws_bytes(int v_dim) { return (size_t)2 * kTrMaxRuns * kTrMaxRows * (size_t)(v_dim + 2) * 4; }
 
 }  // namespace
 }  // namespace k3moe
@@ -423,7 +553,10 @@ extern "C" k3moe_status k3moe_tree_attention(const uint16_t *q, int64_t q_stride
     const int64_t qw = (int64_t)q_heads * k_dim, ow = (int64_t)q_heads * v_dim;
     if (Tq == 1) q_stride = qw, out_stride = ow;
     if (q_stride < qw || out_stride < ow) return K3MOE_E_INVALID_ARG;
-    if (((int64_t)Tq * q_heads + 3) / 4 >= (int64_t)1 << 24) return K3MOE_E_UNSUPPORTED_SHAPE;   // work-items are counted in 32 bits
+    // the line of units is counted in 32 bits; rows of a block: 32 at least
+    const int64_t tiles = ((int64_t)pages_width * page + kAtKeys - 1) / kAtKeys + 1;
+    const int64_t blocks = (int64_t)seqs * kv_heads * (((int64_t)max_q * (q_heads / kv_heads) + 31) / 32);
+    if (blocks > INT32_MAX / 2 || tiles * blocks > INT32_MAX / 2) return K3MOE_E_UNSUPPORTED_SHAPE;
     if (!at(q, 16) || !at(out, 16) || q_stride % 8 || out_stride % 8 || !at(cache->k, 16) || !at(cache->v, 16) || !at(pages, 4) ||
         !at(lens, 4) || !at(cu_q, 4) || !at(tree, 8) || !at(lse, 4))
         return K3MOE_E_ALIGNMENT;
@@ -432,12 +565,9 @@ extern "C" k3moe_status k3moe_tree_attention(const uint16_t *q, int64_t q_stride
     p.q = q, p.kc = static_cast<const uint8_t *>(cache->k), p.vc = static_cast<const uint8_t *>(cache->v);
     p.ks = cache->ks, p.vs = cache->vs, p.pages = pages, p.lens = lens, p.cu = cu_q, p.tree = tree, p.out = out, p.lse = lse;
     p.part = static_cast<float *>(workspace);
-    p.ml = p.part + (size_t)2 * kTrBlocks * kTrRows * (size_t)v_dim;
     p.qs = q_stride, p.os = out_stride, p.seqs = seqs, p.Tq = Tq, p.maxq = max_q, p.Hq = q_heads, p.Hkv = kv_heads;
     p.group = q_heads / kv_heads, p.n_pages = cache->pages, p.lpage = __builtin_ctz((unsigned)page), p.width = pages_width;
     p.scale = scale;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (k_dim == 64) return x8 ? launch<64, 64, true>(p, s) : launch<64, 64, false>(p, s);
-    if (k_dim == 128) return x8 ? launch<128, 128, true>(p, s) : launch<128, 128, false>(p, s);
-    return x8 ? launch<192, 128, true>(p, s) : launch<192, 128, false>(p, s);
+    return k_dim == 64 ? launch<64, 64>(p, x8, s) : k_dim == 128 ? launch<128, 128>(p, x8, s) : launch<192, 128>(p, x8, s);
 }

@@ -93,8 +93,8 @@ def _tree(**kw):
     (dict(cache=_pages(k=None)), INVALID), (dict(cache=_pages(v=None)), INVALID), (dict(qst=504), INVALID),
     (dict(ost=504), INVALID), (dict(D=96, Dv=96), SHAPE), (dict(D=128), SHAPE), (dict(maxq=65), SHAPE),
     (dict(cache=_pages(page=8)), SHAPE), (dict(cache=_pages(page=40)), SHAPE), (dict(cache=_pages(page=2 ** 21)), SHAPE),
-    (dict(width=2 ** 26 + 1), SHAPE), (dict(Tq=2 ** 24), SHAPE), (dict(q=A + 8), ALIGN), (dict(out=A + 8), ALIGN),
-    (dict(qst=516), ALIGN), (dict(ost=516), ALIGN), (dict(pages=A + 2), ALIGN), (dict(lens=A + 2), ALIGN),
+    (dict(width=2 ** 26 + 1), SHAPE), (dict(seqs=2 ** 30, Tq=2 ** 30), SHAPE), (dict(seqs=2 ** 20, Tq=2 ** 20, width=2 ** 20), SHAPE),
+    (dict(q=A + 8), ALIGN), (dict(out=A + 8), ALIGN), (dict(qst=516), ALIGN), (dict(ost=516), ALIGN), (dict(pages=A + 2), ALIGN), (dict(lens=A + 2), ALIGN),
     (dict(cq=A + 2), ALIGN), (dict(tree=A + 4), ALIGN), (dict(lse=A + 2), ALIGN), (dict(cache=_pages(k=A + 8)), ALIGN),
     (dict(cache=_pages(v=A + 8)), ALIGN), (dict(ws=None), WORKSPACE), (dict(ws=A + 128), WORKSPACE), (dict(n=0), WORKSPACE),
     (dict(n="short"), WORKSPACE), (dict(seqs=0), OK), (dict(Tq=0, q=None, out=None), OK),
