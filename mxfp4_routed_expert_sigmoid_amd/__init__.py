@@ -732,14 +732,15 @@ def _scratch_ok(workspace, dev):
 
 
 def _scratch(workspace, size, device, stream):
-    """Address and bytes of the caller's workspace, or of a new one (256-byte aligned) marked as used on `stream`."""
+    """The caller's workspace or a new one (marked as used on `stream`), with its address and bytes from the first
+    256-byte boundary on. The caller holds it until its call is queued: freed before, it could be given out again."""
     if workspace is None:
         workspace = torch.empty(size() + 256, dtype=torch.uint8, device=device)
         if stream is not None and stream != torch.cuda.current_stream(device):
             workspace.record_stream(stream)
     base = workspace.data_ptr()
     off = -base % 256
-    return base + off, max(workspace.numel() - off, 0)
+    return workspace, base + off, max(workspace.numel() - off, 0)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, gamma_q=None, gamma_k=None, eps=1e-6, rot=ROT_HALVES, q_out=None, k_out=None,
@@ -894,7 +895,7 @@ def tree_attention(q, kc, vc, pages, lens, out, ks=None, vs=None, cu_q=None, max
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return tree_attention(q, kc, vc, pages, lens, out, ks, vs, cu_q, max_q, tree, scale, lse, workspace, stream)
-    wp, wn = _scratch(workspace, lambda: _tree_bytes(Hq, Hkv, Dv, max_q), q.device, stream)
+    workspace, wp, wn = _scratch(workspace, lambda: _tree_bytes(Hq, Hkv, Dv, max_q), q.device, stream)
     status = lib().k3moe_tree_attention(qp, qst, cache, pp, width, np_, cqp, tp, B, Tq, max_q, Hq, Hkv, D, Dv,
                                         D ** -0.5 if scale is None else scale, op, ost, lp, wp, wn, _queue(dev, stream))
     if status:
@@ -950,7 +951,7 @@ def logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=None,
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return logprobs(logits, ids, lp, entropy, top_ids, top_lp, workspace, stream)
-    wp, wn = _scratch(workspace, lambda: _logprobs_bytes(T, V, k), logits.device, stream)
+    workspace, wp, wn = _scratch(workspace, lambda: _logprobs_bytes(T, V, k), logits.device, stream)
     status = lib().k3moe_logprobs(xp, 1 if logits.dtype == torch.float32 else 0, xst, T, V, ip, M, op, ep, tip, tlp, k, wp,
                                   wn, _queue(dev, stream))
     if status:

@@ -4,17 +4,18 @@
 // over the context and the drafted tokens whose bits are set in i's word.
 //
 // The rows that share a key/value head, (token, head of the group), are one
-// matrix: 32 or 64 of them per block. The work is a line of units, a unit being
+// matrix: 32 or 128 of them per block. The work is a line of units, a unit being
 // 64 keys of one (sequence, key/value head, block of rows), cut into equal runs,
 // one per block, so that sequences of any lengths fill the card alike. What a run
 // holds whole is written at once; cut ends (two per block at most) go to the
 // workspace as unnormalised sums with their maximum, and a second kernel joins
 // them in their order.
 //
-// Bound by the cache's bytes: every wave holds all rows of its block and reads
-// tiles of 32 keys of its own, every fourth of the run, through its own part of
-// the LDS, so nothing waits for another wave until a segment ends and the four
-// waves' sums are added.
+// Up to 32 rows (k_tree_few) are bound by the cache's bytes: every wave holds all
+// rows of its block and reads tiles of 32 keys of its own, every fourth of the
+// run, through its own part of the LDS, so nothing waits for another wave until a
+// segment ends and the four waves' sums are added. More rows (k_tree_wide) are
+// split over the waves, which share tiles of 64 keys as the prompts' kernel does.
 #include "k3moe_attn.h"
 
 namespace k3moe {
@@ -23,7 +24,7 @@ namespace {
 constexpr int kTrWaves = 4, kTrTile = 32;   // keys of a wave's tile
 constexpr int kTrLeast = 2;                 // units of a run at least: a tile for each wave
 constexpr int kTrMaxDraft = 64;             // bits of a word
-constexpr int kTrMaxRuns = 512, kTrMaxRows = 64;
+constexpr int kTrMaxRuns = 512, kTrMaxRows = 128, kTrFew = 32;
 
 struct TreeParams {
     const uint16_t *q;
@@ -77,40 +78,67 @@ __device__ __forceinline__ int wave_scan(int v)
     return v;
 }
 
-__device__ __forceinline__ int run_length(const TreeParams &p, int units)
+// The line of units and a block's run of it. Runs of `per` units follow each other regardless of segments (a segment:
+// the units of one sequence, head and block of rows), or, where the runs of segments cut on their own fit the blocks
+// too, begin with the segments: a block then has one segment instead of up to two ends, one after the other.
+struct TreePlan {
+    int total, per, own;        // own: runs begin with segments
+    int b, seg, tile, last;     // where the run begins: sequence, segment in it, tile; units of the run (0: none)
+    TreeSeq s;
+};
+
+__device__ __forceinline__ TreeSeq tree_pick(const TreeSeq &s, int l)
 {
-    return max((units + p.runs - 1) / p.runs, kTrLeast);
+    TreeSeq r;
+    r.q0 = __builtin_amdgcn_readlane(s.q0, l), r.n = __builtin_amdgcn_readlane(s.n, l);
+    r.ctx = __builtin_amdgcn_readlane(s.ctx, l), r.keys = __builtin_amdgcn_readlane(s.keys, l);
+    r.kt = __builtin_amdgcn_readlane(s.kt, l), r.rt = __builtin_amdgcn_readlane(s.rt, l);
+    r.units = __builtin_amdgcn_readlane(s.units, l);
+    return r;
 }
 
-// The line of units: its length, the length of a run, and for unit run * number the sequence that holds it with the
-// units in front of that sequence (b < 0: the line is shorter). 64 sequences at a time; up to 64 are looked at once.
-struct TreePlan {
-    int total, per, b, front;
-};
 __device__ __forceinline__ TreePlan tree_plan(const TreeParams &p, int number)
 {
     const int lane = threadIdx.x & 63;
-    TreePlan r{0, 0, -1, 0};
-    int units = 0, upto = 0;
+    TreePlan r{};
+    TreeSeq s{};
+    int upto = 0;
     for (int b0 = 0; b0 < p.seqs; b0 += 64) {
-        units = tree_seq(p, b0 + lane).units;
-        upto = wave_scan(units) + r.total;
+        s = tree_seq(p, b0 + lane);
+        upto = wave_scan(s.units) + r.total;
         r.total = __builtin_amdgcn_readlane(upto, 63);
     }
-    r.per = run_length(p, r.total);
+    r.per = max((r.total + p.runs - 1) / p.runs, kTrLeast);
+    if (p.seqs <= 64) {
+        // the smallest length, of the first few, with which every segment's own runs fit
+        const int segs = s.units > 0 ? p.Hkv * s.rt : 0;
+        for (int more = 0; more < 4 && !r.own; ++more) {
+            const int per = r.per + more, runs = segs > 0 ? (s.kt + per - 1) / per : 0;
+            const int sum = wave_scan(segs * runs), all = __builtin_amdgcn_readlane(sum, 63);
+            // (at most one run per unit, so that the sum fits 32 bits too)
+            if (all > p.runs) continue;
+            r.own = 1, r.per = per;
+            if (number >= all) return r;
+            const int at = __builtin_ctzll(__ballot(sum > number));
+            const int in = number - __builtin_amdgcn_readlane(sum - segs * runs, at), each = __builtin_amdgcn_readlane(runs, at);
+            r.b = at, r.s = tree_pick(s, at), r.seg = in / each, r.tile = (in - r.seg * each) * per;
+            r.last = min(per, r.s.kt - r.tile);
+            return r;
+        }
+    }
     const int64_t unit = (int64_t)r.per * number;
     if (unit >= r.total) return r;
+    r.last = min(r.per, r.total - (int)unit);
     int before = 0;
     for (int b0 = 0; b0 < p.seqs; b0 += 64) {
         if (p.seqs > 64) {
-            units = tree_seq(p, b0 + lane).units;
-            upto = wave_scan(units) + before;
+            s = tree_seq(p, b0 + lane);
+            upto = wave_scan(s.units) + before;
         }
         const uint64_t past = __ballot(upto > unit);
         if (past) {
-            const int at = __builtin_ctzll(past);
-            r.b = b0 + at;
-            r.front = __builtin_amdgcn_readlane(upto - units, at);
+            const int at = __builtin_ctzll(past), in = (int)unit - __builtin_amdgcn_readlane(upto - s.units, at);
+            r.b = b0 + at, r.s = tree_pick(s, at), r.seg = in / r.s.kt, r.tile = in - r.seg * r.s.kt;
             return r;
         }
         before = __builtin_amdgcn_readlane(upto, 63);
@@ -150,6 +178,19 @@ struct ByteStage {
             sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(row < have ? (uint32_t)(row * (D / 32) + sub / 2) : kAtOut), 0, 0);
         }
     }
+    // Whether a group's byte is 255 in any lane; such a group is zero, whatever its codes.
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t m = sc[0];
+#pragma unroll
+        for (int i = 1; i < L; ++i) m = max(m, sc[i]);
+        return m;
+    }
+    __device__ __forceinline__ void drop()
+    {
+#pragma unroll
+        for (int i = 0; i < L; ++i) w[i] = sc[i] == 255u ? u4{0u, 0u, 0u, 0u} : w[i];
+    }
     // As bf16 into rows row0 .. row0 + 15 of a tile.
     template <class Slot>
     __device__ __forceinline__ void store(uint8_t *tile, int row0, Slot slot) const
@@ -158,9 +199,8 @@ struct ByteStage {
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             const int at = 64 * i + lane, row = row0 + at / (D / 16), sub = at % (D / 16);
-            const bool drop = sc[i] == 255u;   // such a group is zero, whatever its codes
             const float f = e8m0_to_f32(sc[i]);
-            const u4 x = drop ? u4{0u, 0u, 0u, 0u} : w[i];
+            const u4 x = w[i];
             *reinterpret_cast<u4 *>(tile + 16 * slot(row, 2 * sub)) = expand_pair(x.x, x.y, f);
             *reinterpret_cast<u4 *>(tile + 16 * slot(row, 2 * sub + 1)) = expand_pair(x.z, x.w, f);
         }
@@ -174,30 +214,81 @@ __device__ __forceinline__ void wait_loads()   // all but the last N loads
 }
 #endif
 
-// NC * 32 rows per block.
-template <int DK, int DV, bool X8, int NC>
+// A lane's row of a block: (token, head of the group), with what it sees.
+struct TreeRow {
+    int64_t token;
+    int head;
+    bool have;
+    uint64_t word;
+
+    __device__ __forceinline__ TreeRow(const TreeParams &p, const TreeSeq &s, int kvh, int m)
+    {
+        have = m < s.n * p.group;
+        const int i = min(m / p.group, s.n - 1);
+        token = s.q0 + i, head = kvh * p.group + m % p.group;
+        word = (p.tree ? p.tree[token] : low_bits(i + 1)) & low_bits(s.n);
+    }
+    // which of the 64 keys from `first` on it sees, whatever their pages
+    __device__ __forceinline__ uint64_t seen(const TreeSeq &s, int first) const
+    {
+        const int a = s.ctx - first;   // those in front of the drafted ones
+        const uint64_t drafted = a >= 64 || a <= -64 ? 0ull : a >= 0 ? word << a : word >> -a;
+        return (low_bits(a) | drafted) & low_bits(s.keys - first);
+    }
+    // Stores N values of the row from register e0 of its lane on (register e: dimension 32 (e / 16) + 8 (e % 16 / 4) +
+    // 4 h + e % 4), or leaves them in the workspace where tiles t0 .. t1 are not all of the segment's. M: the maximum,
+    // in powers of two; L: the sum; at: the row's place in the block.
+    template <int DV, int N>
+    __device__ __forceinline__ void store(const TreeParams &p, const TreeSeq &s, const float (&v)[N], int e0, float M, float L,
+                                          int t0, int t1, int at) const
+    {
+        const int h = (threadIdx.x & 63) >> 5;
+        if (!have) return;
+        if (t0 == 0 && t1 == s.kt) {
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            if (p.lse && h == 0 && e0 == 0) p.lse[token * p.Hq + head] = L == 0.0f ? -INFINITY : (M + __log2f(L)) * kLn2;
+            uint16_t *op = p.out + token * p.os + (int64_t)head * DV + 4 * h;
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const int e = e0 + i;
+                *reinterpret_cast<uint2 *>(op + 32 * (e >> 4) + 2 * (e & 15)) =
+                    uint2{at_bf16(v[i] * inv) | (at_bf16(v[i + 1] * inv) << 16), at_bf16(v[i + 2] * inv) | (at_bf16(v[i + 3] * inv) << 16)};
+            }
+        } else {
+            // a segment cut in front goes to the block's first place, one cut behind only to its second
+            const int64_t to = (int64_t)(2 * (int)blockIdx.x + (t0 == 0)) * p.rows + at;
+            float *op = p.part + to * DV + 4 * h;
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const int e = e0 + i;
+                *reinterpret_cast<float4 *>(op + 32 * (e >> 4) + 2 * (e & 15)) = float4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+            }
+            if (h == 0 && e0 == 0) *reinterpret_cast<float2 *>(p.ml + 2 * to) = float2{M, L};
+        }
+    }
+};
+
+template <int DK, int DV, bool X8>
 struct TreeShape {
     static constexpr int KB = kTrTile * DK * 2, VB = kTrTile * DV * 2;   // a wave's tile
     static constexpr int kBufs = X8 ? 1 : 2;
     static constexpr int kTiles = kTrWaves * kBufs * (KB + VB), kSums = kTrWaves * (DV / 2 + 1) * 64 * 4;
     static constexpr int kLds = kTiles > kSums ? kTiles : kSums;          // the waves' sums take the tiles' place
-    // blocks that fit a CU: by LDS, and by registers where the accumulators leave room for a second wave per SIMD
-    static constexpr int kPerCu = kLds <= 80 * 1024 && NC == 1 ? 2 : 1;
+    static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;             // blocks that fit a CU
 };
 
-template <int DK, int DV, bool X8, int NC>
-__global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8, NC>::kPerCu)) void k_tree(TreeParams p)
+template <int DK, int DV, bool X8>
+__global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) void k_tree_few(TreeParams p)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    typedef TreeShape<DK, DV, X8, NC> S;
+    typedef TreeShape<DK, DV, X8> S;
     constexpr int KB = S::KB, VB = S::VB, EB = X8 ? 1 : 2;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, l32 = lane & 31;
     const TreePlan plan = tree_plan(p, (int)blockIdx.x);
-    if (plan.b < 0) return;
-    int u = plan.per * (int)blockIdx.x, b = plan.b, front = plan.front;
-    const int end = min(u + plan.per, plan.total);
-    TreeSeq s = tree_seq(p, b);
+    if (plan.last <= 0) return;
+    int left = plan.last, b = plan.b, seg = plan.seg, t0 = plan.tile;
+    TreeSeq s = plan.s;
     const int page = 1 << p.lpage;
     const float c = p.scale * kLog2e;
     uint8_t *mine = lds + wave * S::kBufs * (KB + VB);      // this wave's tiles
@@ -213,37 +304,24 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8, NC>::kPerCu))
     if constexpr (!X8) sk.init(DK), sv.init(DV);
 
     while (true) {
-        // the segment that holds unit u: tiles t0 .. t1 (of 64 keys) of (b, kvh, rows)
-        const int in = u - front, seg = in / s.kt, t0 = in - seg * s.kt;
-        const int kvh = seg / s.rt, rows0 = (seg - kvh * s.rt) * 32 * NC;
-        const int t1 = min(s.kt, t0 + (end - u));
+        // tiles t0 .. t1 (of 64 keys) of segment seg of sequence b
+        const int kvh = seg / s.rt, rows0 = (seg - kvh * s.rt) * kTrFew;
+        const int t1 = min(s.kt, t0 + left);
         const int j1 = min(2 * t1, (s.keys + kTrTile - 1) / kTrTile);   // tiles of 32 keys
 
-        // this lane's rows: (token, head of the group)
-        int tok[NC], head[NC];
-        bool have[NC];
-        uint64_t word[NC];
-        bf8 q[NC][DK / 16];
+        const TreeRow row(p, s, kvh, rows0 + l32);
+        bf8 q[DK / 16];
+        {
+            const uint16_t *qp = p.q + row.token * p.qs + (int64_t)row.head * DK + 8 * h;
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const int m = rows0 + 32 * n + l32;
-            have[n] = m < s.n * p.group;
-            tok[n] = min(m / p.group, s.n - 1), head[n] = kvh * p.group + m % p.group;
-            const uint16_t *qp = p.q + (int64_t)(s.q0 + tok[n]) * p.qs + (int64_t)head[n] * DK + 8 * h;
-#pragma unroll
-            for (int k = 0; k < DK / 16; ++k) q[n][k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
-            word[n] = (p.tree ? p.tree[s.q0 + tok[n]] : low_bits(tok[n] + 1)) & low_bits(s.n);
+            for (int k = 0; k < DK / 16; ++k) q[k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
         }
-        v16f o[NC][DV / 32];
-        float mx[NC], l[NC];
+        v16f o[DV / 32];
+        float mx = -INFINITY, l = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            mx[n] = -INFINITY, l[n] = 0.0f;
+        for (int d = 0; d < DV / 32; ++d)
 #pragma unroll
-            for (int d = 0; d < DV / 32; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[n][d][i] = 0.0f;
-        }
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
 
         // Page numbers of this wave's next 32 tiles, two (of 16 keys) each, a lane holds one; -1: no such key or page.
         const int32_t *table = p.pages + (int64_t)b * p.width;
@@ -277,15 +355,18 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8, NC>::kPerCu))
         };
 
         int j = 2 * t0 + wave, buf = 0;
-        if (j < j1) {
-            look(j);
-            load(j, 0);
-        }
-        for (; j < j1; j += kTrWaves) {
-            const uint8_t *kt = mine + buf * (KB + VB), *vt = kt + KB;
+        const uint8_t *kt = mine, *vt = mine + KB;
+        bool whole = false;                                // every row sees the whole tile
+        // Makes tile j ready at kt, vt and sends for the next one.
+        auto ready = [&]() {
             ok = ok_next;
             const bool more = j + kTrWaves < j1;
             if constexpr (X8) {
+                wave_lds_sync();                           // the last tile is read
+                if (__ballot(max(max(bk[0].top(), bk[1].top()), max(bv[0].top(), bv[1].top())) == 255u)) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) bk[g].drop(), bv[g].drop();
+                }
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     bk[g].store(mine, 16 * g, k_slot<DK>);
@@ -294,179 +375,310 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8, NC>::kPerCu))
                 if (more) load(j + kTrWaves, 0);
                 wave_lds_sync();
             } else {
+                kt = mine + buf * (KB + VB), vt = kt + KB;
+                buf ^= 1;
                 if (more) {
-                    wave_lds_sync();                        // the other buffer is read
-                    load(j + kTrWaves, buf ^ 1);
+                    wave_lds_sync();                       // the other buffer is read
+                    load(j + kTrWaves, buf);
                     wait_loads<2 * (DK + DV) / 32>();
                 } else {
                     wait_loads<0>();
                 }
-                buf ^= 1;
             }
-            // scores
-            v16f sc[NC];
+            whole = (j + 1) * kTrTile <= s.ctx && ok == ~0u;
+        };
+        v16f sc;
+        bf8 pw[2];
+        auto scores = [&]() {
+            const uint32_t at = fresh(krow), x = fresh(kx);
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
+            for (int i = 0; i < 16; ++i) sc[i] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc[n][i] = 0.0f;
+            for (int k = 0; k < DK / 16; ++k)
+                sc = mfma32(as_bf8(*reinterpret_cast<const u4 *>(kt + at + (x ^ (32u * k)))), q[k], sc);
+        };
+        auto weights = [&]() {
+            float m = sc[0];
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k) {
-                const bf8 a = as_bf8(*reinterpret_cast<const u4 *>(kt + krow + (kx ^ (32u * k))));
+            for (int i = 1; i < 16; ++i) m = fmaxf(m, sc[i]);
+            m = swap_max(m);
+            if (__ballot((m - mx) * c > kAtSlack)) {
+                const float mn = fmaxf(mx, m);
+                const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx - mn) * c);
+                mx = mn, l *= f;
 #pragma unroll
-                for (int n = 0; n < NC; ++n) sc[n] = mfma32(a, q[n][k], sc[n]);
+                for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[d][i] *= f;
             }
-            const int first = j * kTrTile, ahead = s.ctx - first;   // the tile's keys in front of the drafted ones
-            const bool whole = ahead >= kTrTile && ok == ~0u;
-            uint32_t seen[NC];
-            bool bad = false;
-            bf8 pw[NC][2];
+            const float mc = mx == -INFINITY ? 0.0f : mx * c;
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                seen[n] = ~0u;
-                if (!whole) {
-                    uint64_t see = low_bits(ahead) | (ahead >= 64 || ahead <= -64 ? 0ull : ahead >= 0 ? word[n] << ahead : word[n] >> -ahead);
-                    see &= low_bits(s.keys - first);
-                    seen[n] = (uint32_t)see & ok;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sc[n][i] = (seen[n] >> (4 * h)) & (1u << (8 * (i >> 2) + (i & 3))) ? sc[n][i] : -INFINITY;
-                }
-                float m = sc[n][0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) m = fmaxf(m, sc[n][i]);
-                m = swap_max(m);
-                if (__ballot((m - mx[n]) * c > kAtSlack)) {
-                    const float mn = fmaxf(mx[n], m);
-                    const float f = mx[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx[n] - mn) * c);
-                    mx[n] = mn, l[n] *= f;
-#pragma unroll
-                    for (int d = 0; d < DV / 32; ++d)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[n][d][i] *= f;
-                }
-                const float mc = mx[n] == -INFINITY ? 0.0f : mx[n] * c;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    sc[n][i] = __builtin_amdgcn_exp2f(fmaf(sc[n][i], c, -mc));
-                    l[n] += sc[n][i];
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    pw[n][k] = as_bf8(u4{at_pack(sc[n][8 * k], sc[n][8 * k + 1]), at_pack(sc[n][8 * k + 2], sc[n][8 * k + 3]),
-                                         at_pack(sc[n][8 * k + 4], sc[n][8 * k + 5]), at_pack(sc[n][8 * k + 6], sc[n][8 * k + 7])});
+            for (int i = 0; i < 16; ++i) {
+                sc[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], c, -mc));
+                l += sc[i];
             }
-            if (!whole) bad = v_not_finite<DV, kTrTile>(vt);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                pw[k] = as_bf8(u4{at_pack(sc[8 * k], sc[8 * k + 1]), at_pack(sc[8 * k + 2], sc[8 * k + 3]),
+                                  at_pack(sc[8 * k + 4], sc[8 * k + 5]), at_pack(sc[8 * k + 6], sc[8 * k + 7])});
+        };
+        auto values = [&](auto finite) {
+            const uint32_t from = fresh(vrow), x = fresh(vx);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int d = 0; d < DV / 32; ++d) {
-                    const uint8_t *at = vt + (vrow + (vx ^ (64u * d))) + 32 * k * DV;
+                    const uint8_t *at = vt + from + (x ^ (64u * d)) + 32 * k * DV;
                     const s4 a0 = lds_tr(at), a1 = lds_tr(at + 16 * DV);
                     bf8 a;
                     __builtin_memcpy(&a, &a0, 8);
                     __builtin_memcpy(reinterpret_cast<char *>(&a) + 8, &a1, 8);
-                    if (bad) a = only_finite(a);
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) o[n][d] = mfma32(a, pw[n][k], o[n][d]);
+                    if constexpr (decltype(finite)::value) a = only_finite(a);
+                    o[d] = mfma32(a, pw[k], o[d]);
                 }
-            if (bad) {
-#pragma unroll
-                for (int n = 0; n < NC; ++n) att_not_finite<DV>(o[n], sc[n], vt, 0, seen[n]);
+        };
+        if (j < j1) {
+            look(j);
+            load(j, 0);
+        }
+        while (j < j1) {
+            ready();
+            while (whole) {
+                scores();
+                weights();
+                values(std::false_type{});
+                j += kTrWaves;
+                if (j >= j1) break;
+                ready();
             }
-            if constexpr (X8) wave_lds_sync();   // the tile is read
+            if (j >= j1) break;
+            scores();
+            const uint32_t seen = (uint32_t)row.seen(s, j * kTrTile) & ok;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[i] = (seen >> (4 * h)) & (1u << (8 * (i >> 2) + (i & 3))) ? sc[i] : -INFINITY;
+            weights();
+            if (v_not_finite<DV, kTrTile>(vt)) {
+                values(std::true_type{});
+                att_not_finite<DV>(o, sc, vt, 0, seen);
+            } else {
+                values(std::false_type{});
+            }
+            j += kTrWaves;
         }
 
         // The four waves' sums: all rows' maxima first, then each wave adds a quarter of the dimensions.
-        const bool complete = t0 == 0 && t1 == s.kt;
+        constexpr int R = DV / 2, RW = R / kTrWaves;       // a row's values per lane, and per wave
+        float *sums = reinterpret_cast<float *>(lds), *ml = sums + kTrWaves * R * 64;
+        const float lw = l + __shfl_xor(l, 32);
+        at_barrier();                                      // the tiles are read
+        if (h == 0) ml[wave * 64 + l32] = mx, ml[wave * 64 + 32 + l32] = lw;
+        at_barrier();
+        float M = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            constexpr int R = DV / 2, RW = R / kTrWaves;   // a row's values per lane, and per wave
-            float *sums = reinterpret_cast<float *>(lds), *ml = sums + kTrWaves * R * 64;
-            const float lw = l[n] + __shfl_xor(l[n], 32);
-            at_barrier();                                  // the tiles, or the last sums, are read
-            if (h == 0) ml[wave * 64 + l32] = mx[n], ml[wave * 64 + 32 + l32] = lw;
-            at_barrier();
-            float M = -INFINITY;
+        for (int w = 0; w < kTrWaves; ++w) M = fmaxf(M, ml[w * 64 + l32]);
+        float L = 0.0f, f = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kTrWaves; ++w) M = fmaxf(M, ml[w * 64 + l32]);
-            float L = 0.0f, f = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kTrWaves; ++w) {
-                const float m = ml[w * 64 + l32], x = ml[w * 64 + 32 + l32];
-                const float g = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - M) * c);
-                L += m == -INFINITY ? x : x * g;           // without a score above -inf: 0, or NaN
-                f = w == wave ? g : f;
-            }
-#pragma unroll
-            for (int d = 0; d < DV / 32; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sums[(wave * R + 16 * d + i) * 64 + lane] = o[n][d][i] * f;
-            at_barrier();
-            float v[RW];
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                v[i] = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kTrWaves; ++w) v[i] += sums[(w * R + RW * wave + i) * 64 + lane];
-            }
-            // register e of a row holds dimension 32 (e / 16) + 8 (e % 16 / 4) + 4 h + e % 4
-            const int e0 = RW * wave;
-            if (have[n]) {
-                if (complete) {
-                    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                    if (p.lse && h == 0 && wave == 0)
-                        p.lse[(int64_t)(s.q0 + tok[n]) * p.Hq + head[n]] = L == 0.0f ? -INFINITY : fmaf(M, c, __log2f(L)) * kLn2;
-                    uint16_t *op = p.out + (int64_t)(s.q0 + tok[n]) * p.os + (int64_t)head[n] * DV + 4 * h;
-#pragma unroll
-                    for (int i = 0; i < RW; i += 4) {
-                        const int e = e0 + i;
-                        *reinterpret_cast<uint2 *>(op + 32 * (e >> 4) + 2 * (e & 15)) =
-                            uint2{at_bf16(v[i] * inv) | (at_bf16(v[i + 1] * inv) << 16), at_bf16(v[i + 2] * inv) | (at_bf16(v[i + 3] * inv) << 16)};
-                    }
-                } else {
-                    // a segment cut in front goes to the block's first place, one cut behind only to its second
-                    const int64_t at = (int64_t)(2 * (int)blockIdx.x + (t0 == 0)) * p.rows + 32 * n + l32;
-                    float *op = p.part + at * DV + 4 * h;
-#pragma unroll
-                    for (int i = 0; i < RW; i += 4) {
-                        const int e = e0 + i;
-                        *reinterpret_cast<float4 *>(op + 32 * (e >> 4) + 2 * (e & 15)) = float4{v[i], v[i + 1], v[i + 2], v[i + 3]};
-                    }
-                    if (h == 0 && wave == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = float2{M * c, L};   // c > 0: -inf stays
-                }
-            }
+        for (int w = 0; w < kTrWaves; ++w) {
+            const float m = ml[w * 64 + l32], x = ml[w * 64 + 32 + l32];
+            const float g = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - M) * c);
+            L += m == -INFINITY ? x : x * g;               // without a score above -inf: 0, or NaN
+            f = w == wave ? g : f;
         }
+#pragma unroll
+        for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sums[(wave * R + 16 * d + i) * 64 + lane] = o[d][i] * f;
+        at_barrier();
+        float v[RW];
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            v[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kTrWaves; ++w) v[i] += sums[(w * R + RW * wave + i) * 64 + lane];
+        }
+        row.store<DV, RW>(p, s, v, RW * wave, M * c, L, t0, t1, l32);
 
-        u += t1 - t0;
-        if (u >= end) return;
+        left -= t1 - t0;
+        if (left <= 0) return;
         at_barrier();                                      // the sums are read
-        while (u >= front + s.units) {
-            front += s.units;
-            s = tree_seq(p, ++b);
+        t0 = 0;
+        if (++seg == p.Hkv * s.rt) {
+            seg = 0;
+            do s = tree_seq(p, ++b);
+            while (s.units == 0);
         }
     }
 #endif
 }
 
-// Joins the cut ends. Block (w, y): if the end of run w - 1 is the first one within its segment, the rows 16 y .. of
-// that segment, four dimensions per thread.
+// More rows than 32: 128 per block, 32 per wave, over shared tiles of 64 keys; a wave fetches 16 keys of each.
+template <int DK, int DV, bool X8>
+struct WideShape {
+    static constexpr int kLds = 2 * kAtKeys * (DK + DV) * 2;
+    // 8-bit keys and values on their way take registers that two waves per SIMD do not have
+    static constexpr int kPerCu = X8 || kLds > 80 * 1024 ? 1 : 2;
+};
+
+template <int DK, int DV, bool X8>
+__global__ __launch_bounds__(64 * kTrWaves, (WideShape<DK, DV, X8>::kPerCu)) void k_tree_wide(TreeParams p)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    constexpr int KB = kAtKeys * DK * 2, VB = kAtKeys * DV * 2;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, l32 = lane & 31;
+    const TreePlan plan = tree_plan(p, (int)blockIdx.x);
+    if (plan.last <= 0) return;
+    int left = plan.last, b = plan.b, seg = plan.seg, t0 = plan.tile;
+    TreeSeq s = plan.s;
+    const int page = 1 << p.lpage;
+    const float c = p.scale * kLog2e;
+    RowStage<DK, true> sk;
+    RowStage<DV, false> sv;
+    ByteStage<DK> bk;
+    ByteStage<DV> bv;
+    if constexpr (!X8) sk.init(DK), sv.init(DV);
+
+    while (true) {
+        const int kvh = seg / s.rt, rows0 = (seg - kvh * s.rt) * kTrMaxRows;
+        const int n = min(s.kt - t0, left);                        // tiles of this segment here
+        const TreeRow row(p, s, kvh, rows0 + kAtRows * wave + l32);
+        const bool busy = rows0 + kAtRows * wave < s.n * p.group;
+        AttRows<DK, DV> r;
+        {
+            const uint16_t *qp = p.q + row.token * p.qs + (int64_t)row.head * DK + 8 * h;
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) r.q[k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
+        }
+        r.clear();
+
+        // Page numbers of 16 tiles, four (of 16 keys) each, a lane holds one; -1: no such key or page. i counts tiles from t0.
+        const int32_t *table = p.pages + (int64_t)b * p.width;
+        int ids = -1, ids_from = 0;
+        auto look = [&](int i) {
+            ids_from = i;
+            const int64_t pos = (int64_t)(t0 + i) * kAtKeys + 16 * lane;
+            ids = pos < s.keys ? table[pos >> p.lpage] : -1;
+            if (ids >= p.n_pages) ids = -1;
+        };
+        // where this wave's 16 rows of tile i lie, and how many there are
+        auto rows_of = [&](int i, int64_t &at) {
+            const int id = __builtin_amdgcn_readlane(ids, 4 * (i - ids_from) + wave), pos = (t0 + i) * kAtKeys + 16 * wave;
+            at = ((int64_t)max(id, 0) * p.Hkv + kvh) * page + (pos & (page - 1));
+            return id < 0 ? 0 : min(s.keys - pos, 16);
+        };
+        auto cached = [&](int i) {                                 // which of a tile's keys are in the cache
+            const uint64_t m = __ballot(ids >= 0) >> (4 * (i - ids_from));
+            uint64_t r16 = 0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) r16 |= m >> g & 1 ? 0xffffull << (16 * g) : 0ull;
+            return r16;
+        };
+        auto ktile = [&](int i) { return lds + (i & 1) * KB; };
+        auto vtile = [&](int i) { return lds + 2 * KB + (i & 1) * VB; };
+        int64_t vat = 0;
+        int vrows = 0;                                             // of the next tile whose values are fetched
+        uint64_t ok = 0, ok1 = 0, ok2 = 0;                         // cached keys of tiles i, i + 1, i + 2
+        // Keys run a tile ahead of the values. Fetches what tile i's step does: keys of tile i + 2, values of tile i + 1.
+        auto fetch = [&](int i) {
+            if (i + 1 < n) {
+                if constexpr (X8) bv.load(p.vc + vat * DV, p.vs + vat * (DV / 32), vrows);
+                else sv.load(reinterpret_cast<const uint16_t *>(p.vc) + vat * DV, DV, vrows, vtile(i + 1) + 16 * wave * DV * 2);
+            }
+            if (i + 2 < n) {
+                if (i + 2 >= ids_from + 16) look(i + 2);
+                ok2 = cached(i + 2);
+                vrows = rows_of(i + 2, vat);
+                if constexpr (X8) bk.load(p.kc + vat * DK, p.ks + vat * (DK / 32), vrows);
+                else sk.load(reinterpret_cast<const uint16_t *>(p.kc) + vat * DK, DK, vrows, ktile(i + 2) + 16 * wave * DK * 2);
+            }
+        };
+        // 8-bit rows go to their tiles behind the step's work, before the barrier in front of their use.
+        auto commit = [&](int i) {
+            if constexpr (X8) {
+                if (__ballot(max(bk.top(), bv.top()) == 255u)) bk.drop(), bv.drop();
+                if (i + 2 < n) bk.store(const_cast<uint8_t *>(ktile(i + 2)), 16 * wave, k_slot<DK>);
+                if (i + 1 < n) bv.store(const_cast<uint8_t *>(vtile(i + 1)), 16 * wave, v_slot<DV>);
+            }
+        };
+        look(0);
+        at_barrier();                                              // the last segment's tiles are read
+        // Fills up to the state of step 0: keys of tiles 0 and 1, values of tile 0. A step -2 fetches keys of tile 0, a step
+        // -1 those of tile 1 and values of tile 0.
+        ok2 = cached(0);
+        fetch(-2), commit(-2), ok1 = ok2;
+        fetch(-1), commit(-1), ok = ok1, ok1 = n > 1 ? ok2 : 0;
+        at_barrier();
+        v16f sc[2];
+        float mx = 0.0f;
+        if (busy) {
+            att_scores(sc, r, ktile(0));
+            mx = att_max(sc);
+        }
+        int i = 0;
+        auto whole = [&](int i, uint64_t in) { return (t0 + i + 1) * kAtKeys <= s.ctx && in == ~0ull; };
+        auto next = [&]() { ok = ok1, ok1 = ok2; };
+        while (i < n) {
+            while (i + 1 < n && whole(i, ok) && whole(i + 1, ok1)) {
+                v16f o[2];
+                at_barrier();
+                fetch(i);
+                if (busy) att_tile(r, sc, mx, o, ktile(i + 1), vtile(i), c);
+                commit(i), next();
+                at_barrier();
+                fetch(i + 1);
+                if (busy) att_tile(r, o, mx, sc, ktile(i), vtile(i + 1), c);
+                commit(i + 1), next();
+                i += 2;
+            }
+            if (i >= n) break;
+            at_barrier();
+            fetch(i);
+            if (busy) {
+                att_tile_masked(r, sc, ktile(i + 1), vtile(i), c, row.seen(s, (t0 + i) * kAtKeys) & ok);
+                mx = att_max(sc);
+            }
+            commit(i), next();
+            ++i;
+        }
+        const float l = r.l + __shfl_xor(r.l, 32);
+        if (busy) {
+            float v[DV / 2];
+#pragma unroll
+            for (int d = 0; d < DV / 32; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[16 * d + e] = r.o[d][e];
+            row.store<DV, DV / 2>(p, s, v, 0, r.m * c, l, t0, t0 + n, kAtRows * wave + l32);   // c > 0: -inf stays
+        }
+
+        left -= n;
+        if (left <= 0) return;
+        t0 = 0;
+        if (++seg == p.Hkv * s.rt) {
+            seg = 0;
+            do s = tree_seq(p, ++b);
+            while (s.units == 0);
+        }
+    }
+#endif
+}
+
+// Joins the cut ends. Block (w, y): if the end of run w - 1 is the first one within its segment, some rows of that
+// segment, four dimensions per thread.
 template <int DV>
 __global__ __launch_bounds__(256) void k_tree_join(TreeParams p)
 {
     constexpr int TR = DV / 4, RB = 256 / TR;             // threads of a row, rows at a time
     const int w = (int)blockIdx.x + 1;
     const TreePlan plan = tree_plan(p, w);
-    if (plan.b < 0) return;
-    const int u = plan.per * w;
-    const TreeSeq s = tree_seq(p, plan.b);
-    const int seg = (u - plan.front) / s.kt, u0 = plan.front + seg * s.kt;
-    if (u == u0 || u - plan.per > u0) return;             // no cut, or not the segment's first
-    const int kvh = seg / s.rt, rows0 = (seg - kvh * s.rt) * p.rows;
-    const int w0 = w - 1, w1 = (u0 + s.kt - 1) / plan.per;
+    // run w begins within a segment, and is the first that does
+    if (plan.last <= 0 || plan.tile == 0 || plan.tile > plan.per) return;
+    const TreeSeq s = plan.s;
+    const int kvh = plan.seg / s.rt, rows0 = (plan.seg - kvh * s.rt) * p.rows;
+    const int w0 = w - 1, w1 = w + (s.kt - plan.tile - 1) / plan.per;
     const int row = (int)blockIdx.y * RB + (int)threadIdx.x / TR, e = 4 * ((int)threadIdx.x % TR);
     const int m = rows0 + row;
     if (row >= p.rows || m >= s.n * p.group) return;
-    auto place = [&](int r) { return (int64_t)(2 * r + (r == w0 && u0 >= r * plan.per)) * p.rows + row; };
+    auto place = [&](int r) { return (int64_t)(2 * r + (r == w0)) * p.rows + row; };
     float mx = -INFINITY;
     for (int r = w0; r <= w1; ++r) mx = fmaxf(mx, p.ml[2 * place(r)]);
     const float use = mx == -INFINITY ? 0.0f : mx;
@@ -489,26 +701,33 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p)
     if (p.lse && e == 0) p.lse[t * p.Hq + head] = l == 0.0f ? -INFINITY : (use + __log2f(l)) * kLn2;
 }
 
-template <int DK, int DV, bool X8, int NC>
-k3moe_status launch(TreeParams p, hipStream_t s)
+template <int DV>
+k3moe_status launch(void (*kernel)(TreeParams), int lds, TreeParams p, int per_cu, int rows, hipStream_t s)
 {
-    typedef TreeShape<DK, DV, X8, NC> S;
-    static const hipError_t allowed =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(k_tree<DK, DV, X8, NC>), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
-    if (allowed != hipSuccess) return K3MOE_E_HIP;
-    p.runs = 256 * S::kPerCu, p.rows = 32 * NC;
+    p.runs = 256 * per_cu, p.rows = rows;
     p.ml = p.part + (size_t)2 * p.runs * p.rows * DV;
-    k_tree<DK, DV, X8, NC><<<(unsigned)p.runs, 64 * kTrWaves, S::kLds, s>>>(p);
+    kernel<<<(unsigned)p.runs, 64 * kTrWaves, lds, s>>>(p);
     k_tree_join<DV><<<dim3((unsigned)p.runs - 1, (unsigned)(p.rows / (1024 / DV))), 256, 0, s>>>(p);
     return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
+}
+
+template <int DK, int DV, bool X8>
+k3moe_status launch(const TreeParams &p, hipStream_t s)
+{
+    typedef TreeShape<DK, DV, X8> Few;
+    typedef WideShape<DK, DV, X8> Wide;
+    static const hipError_t allowed[2] = {
+        hipFuncSetAttribute(reinterpret_cast<const void *>(k_tree_few<DK, DV, X8>), hipFuncAttributeMaxDynamicSharedMemorySize, Few::kLds),
+        hipFuncSetAttribute(reinterpret_cast<const void *>(k_tree_wide<DK, DV, X8>), hipFuncAttributeMaxDynamicSharedMemorySize, Wide::kLds)};
+    if (allowed[0] != hipSuccess || allowed[1] != hipSuccess) return K3MOE_E_HIP;
+    return p.maxq * p.group <= kTrFew ? launch<DV>(k_tree_few<DK, DV, X8>, Few::kLds, p, Few::kPerCu, kTrFew, s)
+                                      : launch<DV>(k_tree_wide<DK, DV, X8>, Wide::kLds, p, Wide::kPerCu, kTrMaxRows, s);
 }
 
 template <int DK, int DV>
 k3moe_status launch(const TreeParams &p, bool x8, hipStream_t s)
 {
-    const bool few = p.maxq * (int64_t)p.group <= 32;
-    if (x8) return few ? launch<DK, DV, true, 1>(p, s) : launch<DK, DV, true, 2>(p, s);
-    return few ? launch<DK, DV, false, 1>(p, s) : launch<DK, DV, false, 2>(p, s);
+    return x8 ? launch<DK, DV, true>(p, s) : launch<DK, DV, false>(p, s);
 }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
