@@ -177,6 +177,7 @@ __device__ __forceinline__ bool v_not_finite(const uint8_t *vt)
             __builtin_memcpy(&x, &e, 4);
             most = __builtin_elementwise_max(most, x);
         }
+        if (i % 2) asm volatile("" ::: "memory");   // two loads at a time: the accumulators hold the registers
     }
     return __ballot(most[0] == 0x7f80u || most[1] == 0x7f80u) != 0;
 }
@@ -313,6 +314,7 @@ __device__ __forceinline__ void att_not_finite(v16f (&o)[DV / 32], const v16f &s
 #pragma unroll
         for (int i = 1; i < 16; ++i) own = j == i ? s[i] : own;
         own = bf16f(at_bf16(own));
+        asm volatile("" ::: "memory");
         const float other = __shfl_xor(own, 32);
 #pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
@@ -329,6 +331,7 @@ __device__ __forceinline__ void att_not_finite(v16f (&o)[DV / 32], const v16f &s
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         o[d][i + e] = sees && !(fabsf(f[e]) < INFINITY) ? fmaf(w, f[e], o[d][i + e]) : o[d][i + e];
+                    asm volatile("" ::: "memory");   // a few values at a time: this path sets no register's limit
                 }
         }
     }

@@ -26,6 +26,12 @@ constexpr int kTrLeast = 2;                 // units of a run at least: a tile f
 constexpr int kTrMaxDraft = 64;             // bits of a word
 constexpr int kTrMaxRuns = 512, kTrMaxRows = 128, kTrFew = 32;
 
+// A segment whose runs k_tree_join joins, left by the first run that begins within it (last < 0: no such run).
+struct TreeCut {
+    int first, last;            // its runs
+    int q0, n, kvh, rows0;      // its sequence's rows, its head, its first row (token, head of the group)
+};
+
 struct TreeParams {
     const uint16_t *q;
     const uint8_t *kc, *vc, *ks, *vs;
@@ -33,6 +39,7 @@ struct TreeParams {
     const uint64_t *tree;
     uint16_t *out;
     float *lse, *part, *ml;   // part [2 runs][rows][DV], ml [2 runs][rows][2]
+    TreeCut *cut;             // [runs]
     int64_t qs, os;
     int seqs, Tq, maxq, Hq, Hkv, group, n_pages, lpage, width;
     int runs, rows;           // blocks, rows of a block
@@ -144,6 +151,20 @@ __device__ __forceinline__ TreePlan tree_plan(const TreeParams &p, int number)
         before = __builtin_amdgcn_readlane(upto, 63);
     }
     return r;
+}
+
+// Run `number` begins within a segment, as the first of the segment's: what the join has to know.
+__device__ __forceinline__ void tree_cut(const TreeParams &p, const TreePlan &r, int number)
+{
+    if (threadIdx.x) return;
+    TreeCut c{};
+    if (r.last > 0 && r.tile > 0 && r.tile <= r.per) {
+        c.first = number - 1, c.last = number + (r.s.kt - r.tile - 1) / r.per;
+        c.q0 = r.s.q0, c.n = r.s.n, c.kvh = r.seg / r.s.rt, c.rows0 = (r.seg - c.kvh * r.s.rt) * p.rows;
+    } else {
+        c.last = -1;
+    }
+    p.cut[number] = c;
 }
 
 #ifdef __HIP_DEVICE_COMPILE__
@@ -286,6 +307,7 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, l32 = lane & 31;
     const TreePlan plan = tree_plan(p, (int)blockIdx.x);
+    tree_cut(p, plan, (int)blockIdx.x);
     if (plan.last <= 0) return;
     int left = plan.last, b = plan.b, seg = plan.seg, t0 = plan.tile;
     TreeSeq s = plan.s;
@@ -422,7 +444,7 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
                 pw[k] = as_bf8(u4{at_pack(sc[8 * k], sc[8 * k + 1]), at_pack(sc[8 * k + 2], sc[8 * k + 3]),
                                   at_pack(sc[8 * k + 4], sc[8 * k + 5]), at_pack(sc[8 * k + 6], sc[8 * k + 7])});
         };
-        auto values = [&](auto finite) {
+        auto values = [&]() {
             const uint32_t from = fresh(vrow), x = fresh(vx);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -433,7 +455,6 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
                     bf8 a;
                     __builtin_memcpy(&a, &a0, 8);
                     __builtin_memcpy(reinterpret_cast<char *>(&a) + 8, &a1, 8);
-                    if constexpr (decltype(finite)::value) a = only_finite(a);
                     o[d] = mfma32(a, pw[k], o[d]);
                 }
         };
@@ -446,7 +467,7 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
             while (whole) {
                 scores();
                 weights();
-                values(std::false_type{});
+                values();
                 j += kTrWaves;
                 if (j >= j1) break;
                 ready();
@@ -458,11 +479,17 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
             for (int i = 0; i < 16; ++i) sc[i] = (seen >> (4 * h)) & (1u << (8 * (i >> 2) + (i & 3))) ? sc[i] : -INFINITY;
             weights();
             if (v_not_finite<DV, kTrTile>(vt)) {
-                values(std::true_type{});
+                // the rows that see such values get them here; the tile, this wave's own, goes on without them
                 att_not_finite<DV>(o, sc, vt, 0, seen);
-            } else {
-                values(std::false_type{});
+#pragma unroll 1
+                for (int i = 0; i < VB / 1024; ++i) {
+                    u4 *at = reinterpret_cast<u4 *>(const_cast<uint8_t *>(vt) + 1024 * i + 16 * lane);
+                    const bf8 clean = only_finite(as_bf8(*at));
+                    __builtin_memcpy(at, &clean, 16);
+                }
+                wave_lds_sync();
             }
+            values();
             j += kTrWaves;
         }
 
@@ -511,22 +538,23 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
 #endif
 }
 
-// More rows than 32: 128 per block, 32 per wave, over shared tiles of 64 keys; a wave fetches 16 keys of each.
+// More rows than 32: 128 per block, 32 per wave, over shared tiles of 64 keys; a wave fetches 16 keys of each, two steps
+// before their use: bf16 by direct loads into three buffers, 8 bits through registers, a step in each.
 template <int DK, int DV, bool X8>
 struct WideShape {
-    static constexpr int kLds = 2 * kAtKeys * (DK + DV) * 2;
-    // 8-bit keys and values on their way take registers that two waves per SIMD do not have
-    static constexpr int kPerCu = X8 || kLds > 80 * 1024 ? 1 : 2;
+    static constexpr int kBufs = X8 ? 2 : 3;
+    static constexpr int kLds = kBufs * kAtKeys * (DK + DV) * 2;
 };
 
 template <int DK, int DV, bool X8>
-__global__ __launch_bounds__(64 * kTrWaves, (WideShape<DK, DV, X8>::kPerCu)) void k_tree_wide(TreeParams p)
+__global__ __launch_bounds__(64 * kTrWaves, 1) void k_tree_wide(TreeParams p)
 {
 #ifdef __HIP_DEVICE_COMPILE__
     constexpr int KB = kAtKeys * DK * 2, VB = kAtKeys * DV * 2;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, l32 = lane & 31;
     const TreePlan plan = tree_plan(p, (int)blockIdx.x);
+    tree_cut(p, plan, (int)blockIdx.x);
     if (plan.last <= 0) return;
     int left = plan.last, b = plan.b, seg = plan.seg, t0 = plan.tile;
     TreeSeq s = plan.s;
@@ -573,40 +601,50 @@ __global__ __launch_bounds__(64 * kTrWaves, (WideShape<DK, DV, X8>::kPerCu)) voi
             for (int g = 0; g < 4; ++g) r16 |= m >> g & 1 ? 0xffffull << (16 * g) : 0ull;
             return r16;
         };
-        auto ktile = [&](int i) { return lds + (i & 1) * KB; };
-        auto vtile = [&](int i) { return lds + 2 * KB + (i & 1) * VB; };
-        int64_t vat = 0;
-        int vrows = 0;                                             // of the next tile whose values are fetched
-        uint64_t ok = 0, ok1 = 0, ok2 = 0;                         // cached keys of tiles i, i + 1, i + 2
-        // Keys run a tile ahead of the values. Fetches what tile i's step does: keys of tile i + 2, values of tile i + 1.
+        constexpr int NB = WideShape<DK, DV, X8>::kBufs;
+        auto ktile = [&](int i) { return lds + (unsigned)(i + NB) % NB * KB; };
+        auto vtile = [&](int i) { return lds + NB * KB + (unsigned)(i + NB) % NB * VB; };
+        int64_t kat = 0;
+        int krows = 0;                                             // of the keys that were fetched last
+        uint64_t ok = 0, ok1 = 0, ok2 = 0, ok3 = 0;                // cached keys of the next three tiles, and of what is fetched
+        // Step i's fetches, behind its barrier: keys of tile i + 3, values of tile i + 2. Keys run a tile ahead of the
+        // values: step i computes the scores of tile i + 1.
         auto fetch = [&](int i) {
-            if (i + 1 < n) {
-                if constexpr (X8) bv.load(p.vc + vat * DV, p.vs + vat * (DV / 32), vrows);
-                else sv.load(reinterpret_cast<const uint16_t *>(p.vc) + vat * DV, DV, vrows, vtile(i + 1) + 16 * wave * DV * 2);
-            }
-            if (i + 2 < n) {
-                if (i + 2 >= ids_from + 16) look(i + 2);
-                ok2 = cached(i + 2);
-                vrows = rows_of(i + 2, vat);
-                if constexpr (X8) bk.load(p.kc + vat * DK, p.ks + vat * (DK / 32), vrows);
-                else sk.load(reinterpret_cast<const uint16_t *>(p.kc) + vat * DK, DK, vrows, ktile(i + 2) + 16 * wave * DK * 2);
-            }
-        };
-        // 8-bit rows go to their tiles behind the step's work, before the barrier in front of their use.
-        auto commit = [&](int i) {
-            if constexpr (X8) {
+            if constexpr (X8) {                                    // what the last step fetched
                 if (__ballot(max(bk.top(), bv.top()) == 255u)) bk.drop(), bv.drop();
-                if (i + 2 < n) bk.store(const_cast<uint8_t *>(ktile(i + 2)), 16 * wave, k_slot<DK>);
-                if (i + 1 < n) bv.store(const_cast<uint8_t *>(vtile(i + 1)), 16 * wave, v_slot<DV>);
+                if (i + 2 >= 0 && i + 2 < n) bk.store(ktile(i + 2), 16 * wave, k_slot<DK>);
+                if (i + 1 >= 0 && i + 1 < n) bv.store(vtile(i + 1), 16 * wave, v_slot<DV>);
+            }
+            if (i + 2 >= 0 && i + 2 < n) {
+                if constexpr (X8) bv.load(p.vc + kat * DV, p.vs + kat * (DV / 32), krows);
+                else sv.load(reinterpret_cast<const uint16_t *>(p.vc) + kat * DV, DV, krows, vtile(i + 2) + 16 * wave * DV * 2);
+            }
+            if (i + 3 < n) {
+                if (i + 3 >= ids_from + 16) look(i + 3);
+                ok3 = cached(i + 3);
+                krows = rows_of(i + 3, kat);
+                if constexpr (X8) bk.load(p.kc + kat * DK, p.ks + kat * (DK / 32), krows);
+                else sk.load(reinterpret_cast<const uint16_t *>(p.kc) + kat * DK, DK, krows, ktile(i + 3) + 16 * wave * DK * 2);
+            }
+            ok = ok1, ok1 = ok2, ok2 = ok3;                        // now of tiles i + 1 .. i + 3
+        };
+        // In front of step i: keys of tile i + 1 and values of tile i are there; what step i - 1 fetched may be on its way.
+        auto step_barrier = [&](int i) {
+            if (!X8 && i + 2 < n) {
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((DK + DV) / 32) : "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            } else if (X8) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            } else {
+                at_barrier();
             }
         };
         look(0);
         at_barrier();                                              // the last segment's tiles are read
-        // Fills up to the state of step 0: keys of tiles 0 and 1, values of tile 0. A step -2 fetches keys of tile 0, a step
-        // -1 those of tile 1 and values of tile 0.
-        ok2 = cached(0);
-        fetch(-2), commit(-2), ok1 = ok2;
-        fetch(-1), commit(-1), ok = ok1, ok1 = n > 1 ? ok2 : 0;
+        fetch(-3), fetch(-2), fetch(-1);                           // now ok: tile 0, ok1: tile 1, ok2: tile 2
         at_barrier();
         v16f sc[2];
         float mx = 0.0f;
@@ -616,28 +654,25 @@ __global__ __launch_bounds__(64 * kTrWaves, (WideShape<DK, DV, X8>::kPerCu)) voi
         }
         int i = 0;
         auto whole = [&](int i, uint64_t in) { return (t0 + i + 1) * kAtKeys <= s.ctx && in == ~0ull; };
-        auto next = [&]() { ok = ok1, ok1 = ok2; };
         while (i < n) {
             while (i + 1 < n && whole(i, ok) && whole(i + 1, ok1)) {
                 v16f o[2];
-                at_barrier();
+                step_barrier(i);
                 fetch(i);
                 if (busy) att_tile(r, sc, mx, o, ktile(i + 1), vtile(i), c);
-                commit(i), next();
-                at_barrier();
+                step_barrier(i + 1);
                 fetch(i + 1);
-                if (busy) att_tile(r, o, mx, sc, ktile(i), vtile(i + 1), c);
-                commit(i + 1), next();
+                if (busy) att_tile(r, o, mx, sc, ktile(i + 2), vtile(i + 1), c);
                 i += 2;
             }
             if (i >= n) break;
-            at_barrier();
+            const uint64_t in = ok;
+            step_barrier(i);
             fetch(i);
             if (busy) {
-                att_tile_masked(r, sc, ktile(i + 1), vtile(i), c, row.seen(s, (t0 + i) * kAtKeys) & ok);
+                att_tile_masked(r, sc, ktile(i + 1), vtile(i), c, row.seen(s, (t0 + i) * kAtKeys) & in);
                 mx = att_max(sc);
             }
-            commit(i), next();
             ++i;
         }
         const float l = r.l + __shfl_xor(r.l, 32);
@@ -662,43 +697,50 @@ __global__ __launch_bounds__(64 * kTrWaves, (WideShape<DK, DV, X8>::kPerCu)) voi
 #endif
 }
 
-// Joins the cut ends. Block (w, y): if the end of run w - 1 is the first one within its segment, some rows of that
-// segment, four dimensions per thread.
+// Joins the cut ends. Block (w, y): where run w + 1 is the first that begins within its segment, some rows of that
+// segment, DV / 4 threads for a row.
 template <int DV>
 __global__ __launch_bounds__(256) void k_tree_join(TreeParams p)
 {
-    constexpr int TR = DV / 4, RB = 256 / TR;             // threads of a row, rows at a time
-    const int w = (int)blockIdx.x + 1;
-    const TreePlan plan = tree_plan(p, w);
-    // run w begins within a segment, and is the first that does
-    if (plan.last <= 0 || plan.tile == 0 || plan.tile > plan.per) return;
-    const TreeSeq s = plan.s;
-    const int kvh = plan.seg / s.rt, rows0 = (plan.seg - kvh * s.rt) * p.rows;
-    const int w0 = w - 1, w1 = w + (s.kt - plan.tile - 1) / plan.per;
-    const int row = (int)blockIdx.y * RB + (int)threadIdx.x / TR, e = 4 * ((int)threadIdx.x % TR);
-    const int m = rows0 + row;
-    if (row >= p.rows || m >= s.n * p.group) return;
-    auto place = [&](int r) { return (int64_t)(2 * r + (r == w0)) * p.rows + row; };
-    float mx = -INFINITY;
-    for (int r = w0; r <= w1; ++r) mx = fmaxf(mx, p.ml[2 * place(r)]);
-    const float use = mx == -INFINITY ? 0.0f : mx;
-    float l = 0.0f;
+    constexpr int TR = DV / 4, RB = 256 / TR;             // threads of a row, rows of a block
+    const TreeCut cut = p.cut[blockIdx.x + 1];
+    const int row = (int)blockIdx.y * RB + (int)threadIdx.x / TR, part = (int)threadIdx.x % TR;
+    const int m = cut.rows0 + row;
+    if (cut.last < 0 || m >= cut.n * p.group) return;
+    const int base = ((int)threadIdx.x & 63) / TR * TR;   // the row's first lane
+    float mx = -INFINITY, l = 0.0f;
     float4 o = float4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int r = w0; r <= w1; ++r) {
-        const int64_t at = place(r);
-        const float2 x = *reinterpret_cast<const float2 *>(p.ml + 2 * at);
-        const float4 v = *reinterpret_cast<const float4 *>(p.part + at * DV + e);
+    for (int r0 = cut.first; r0 <= cut.last; r0 += TR) {
+        // a thread looks at one run's maximum and sum
+        auto place = [&](int r) { return (int64_t)(2 * r + (r == cut.first)) * p.rows + row; };
+        const int r = r0 + part;
+        const float2 x = r <= cut.last ? *reinterpret_cast<const float2 *>(p.ml + 2 * place(r)) : float2{-INFINITY, 0.0f};
+        float top = x.x;
+#pragma unroll
+        for (int s = 1; s < TR; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
+        top = fmaxf(top, mx);
+        const float use = top == -INFINITY ? 0.0f : top;
+        const float old = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - use);
         const float f = x.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x.x - use);
-        l += x.x == -INFINITY ? x.y : x.y * f;            // without a score above -inf: 0, or NaN
-        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+        mx = top;
+        l = l * old + (x.x == -INFINITY ? x.y : x.y * f);     // without a score above -inf: 0, or NaN
+        o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+        const int n = min(TR, cut.last - r0 + 1);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float4 v = *reinterpret_cast<const float4 *>(p.part + place(r0 + k) * DV + 4 * part);
+            const float g = __shfl(f, base + k);
+            o.x = fmaf(v.x, g, o.x), o.y = fmaf(v.y, g, o.y), o.z = fmaf(v.z, g, o.z), o.w = fmaf(v.w, g, o.w);
+        }
     }
+#pragma unroll
+    for (int s = 1; s < TR; s <<= 1) l += __shfl_xor(l, s);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t t = s.q0 + m / p.group;
-    const int head = kvh * p.group + m % p.group;
-    *reinterpret_cast<uint2 *>(p.out + t * p.os + (int64_t)head * DV + e) =
+    const int64_t t = cut.q0 + m / p.group;
+    const int head = cut.kvh * p.group + m % p.group;
+    *reinterpret_cast<uint2 *>(p.out + t * p.os + (int64_t)head * DV + 4 * part) =
         uint2{at_bf16(o.x * inv) | (at_bf16(o.y * inv) << 16), at_bf16(o.z * inv) | (at_bf16(o.w * inv) << 16)};
-    if (p.lse && e == 0) p.lse[t * p.Hq + head] = l == 0.0f ? -INFINITY : (use + __log2f(l)) * kLn2;
+    if (p.lse && part == 0) p.lse[t * p.Hq + head] = l == 0.0f ? -INFINITY : (mx + __log2f(l)) * kLn2;
 }
 
 template <int DV>
@@ -706,6 +748,7 @@ k3moe_status launch(void (*kernel)(TreeParams), int lds, TreeParams p, int per_c
 {
     p.runs = 256 * per_cu, p.rows = rows;
     p.ml = p.part + (size_t)2 * p.runs * p.rows * DV;
+    p.cut = reinterpret_cast<TreeCut *>(p.ml + (size_t)2 * p.runs * p.rows * 2);
     kernel<<<(unsigned)p.runs, 64 * kTrWaves, lds, s>>>(p);
     k_tree_join<DV><<<dim3((unsigned)p.runs - 1, (unsigned)(p.rows / (1024 / DV))), 256, 0, s>>>(p);
     return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
@@ -721,7 +764,7 @@ k3moe_status launch(const TreeParams &p, hipStream_t s)
         hipFuncSetAttribute(reinterpret_cast<const void *>(k_tree_wide<DK, DV, X8>), hipFuncAttributeMaxDynamicSharedMemorySize, Wide::kLds)};
     if (allowed[0] != hipSuccess || allowed[1] != hipSuccess) return K3MOE_E_HIP;
     return p.maxq * p.group <= kTrFew ? launch<DV>(k_tree_few<DK, DV, X8>, Few::kLds, p, Few::kPerCu, kTrFew, s)
-                                      : launch<DV>(k_tree_wide<DK, DV, X8>, Wide::kLds, p, Wide::kPerCu, kTrMaxRows, s);
+                                      : launch<DV>(k_tree_wide<DK, DV, X8>, Wide::kLds, p, 1, kTrMaxRows, s);
 }
 
 template <int DK, int DV>
@@ -733,7 +776,7 @@ k3moe_status launch(const TreeParams &p, bool x8, hipStream_t s)
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // For the most runs and rows that any variant has.
-size_t ws_bytes(int v_dim) { return (size_t)2 * kTrMaxRuns * kTrMaxRows * (size_t)(v_dim + 2) * 4; }
+size_t ws_bytes(int v_dim) { return (size_t)2 * kTrMaxRuns * kTrMaxRows * (size_t)(v_dim + 2) * 4 + kTrMaxRuns * sizeof(TreeCut); }
 
 }  // namespace
 }  // namespace k3moe
