@@ -368,6 +368,20 @@ __device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, v16f (&s)[2], float
     const float mc = r.m == -INFINITY ? 0.0f : r.m * c;
     uint32_t p[16];
     float l[2] = {r.l, 0.0f};
+    // a pair of scores goes through its operations a step apart each, so that none waits for the one in front of it
+    auto scaled = [&](int w) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) s[w / 8][2 * (w % 8) + x] = fmaf(s[w / 8][2 * (w % 8) + x], c, -mc);
+    };
+    auto raised = [&](int w) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) s[w / 8][2 * (w % 8) + x] = __builtin_amdgcn_exp2f(s[w / 8][2 * (w % 8) + x]);
+    };
+    auto summed = [&](int w) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) l[x] += s[w / 8][2 * (w % 8) + x];
+        p[w] = at_pack(s[w / 8][2 * (w % 8)], s[w / 8][2 * (w % 8) + 1]);
+    };
 #pragma unroll
     for (int i = 0; i < QS; ++i) {
         __builtin_amdgcn_sched_barrier(0);
@@ -380,15 +394,17 @@ __device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, v16f (&s)[2], float
             for (int e = 0; e < 16; ++e) next[t][e] = 0.0f;
         next[t] = mfma32(as_bf8(ka[i]), r.q[k], next[t]);
 #pragma unroll
-        for (int w = QP * i; w < QP * i + QP && w < 16; ++w) {
-            float e[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                e[x] = __builtin_amdgcn_exp2f(fmaf(s[w / 8][2 * (w % 8) + x], c, -mc));
-                l[x] += e[x];
-            }
-            p[w] = at_pack(e[0], e[1]);
+        for (int w = QP * i; w < QP * i + QP; ++w) {
+            if (w - 2 * QP >= 0 && w - 2 * QP < 16) summed(w - 2 * QP);
+            if (w - QP >= 0 && w - QP < 16) raised(w - QP);
+            if (w < 16) scaled(w);
         }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int w = QP * QS; w < 16 + 2 * QP; ++w) {
+        if (w - 2 * QP < 16) summed(w - 2 * QP);
+        if (w - QP < 16) raised(w - QP);
     }
     r.l = l[0] + l[1];
     asm volatile("" : "+v"(r.l));   // or the sum is put off to the next tile, and with it all weights are held

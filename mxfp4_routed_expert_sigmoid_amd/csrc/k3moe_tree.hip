@@ -594,19 +594,20 @@ __global__ __launch_bounds__(64 * kTrWaves, 1) void k_tree_wide(TreeParams p)
             at = ((int64_t)max(id, 0) * p.Hkv + kvh) * page + (pos & (page - 1));
             return id < 0 ? 0 : min(s.keys - pos, 16);
         };
-        auto cached = [&](int i) {                                 // which of a tile's keys are in the cache
-            const uint64_t m = __ballot(ids >= 0) >> (4 * (i - ids_from));
-            uint64_t r16 = 0;
+        // which of a tile's four runs of 16 keys are in the cache, and the same for its keys
+        auto cached = [&](int i) { return (uint32_t)(__ballot(ids >= 0) >> (4 * (i - ids_from))) & 15u; };
+        auto keys_of = [](uint32_t runs) {
+            uint64_t m = 0;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) r16 |= m >> g & 1 ? 0xffffull << (16 * g) : 0ull;
-            return r16;
+            for (int g = 0; g < 4; ++g) m |= runs >> g & 1 ? 0xffffull << (16 * g) : 0ull;
+            return m;
         };
         constexpr int NB = WideShape<DK, DV, X8>::kBufs;
         auto ktile = [&](int i) { return lds + (unsigned)(i + NB) % NB * KB; };
         auto vtile = [&](int i) { return lds + NB * KB + (unsigned)(i + NB) % NB * VB; };
         int64_t kat = 0;
         int krows = 0;                                             // of the keys that were fetched last
-        uint64_t ok = 0, ok1 = 0, ok2 = 0, ok3 = 0;                // cached keys of the next three tiles, and of what is fetched
+        uint32_t ok = 0, ok1 = 0, ok2 = 0, ok3 = 0;                // cached runs of the next three tiles, and of what is fetched
         // Step i's fetches, behind its barrier: keys of tile i + 3, values of tile i + 2. Keys run a tile ahead of the
         // values: step i computes the scores of tile i + 1.
         auto fetch = [&](int i) {
@@ -646,37 +647,37 @@ __global__ __launch_bounds__(64 * kTrWaves, 1) void k_tree_wide(TreeParams p)
         at_barrier();                                              // the last segment's tiles are read
         fetch(-3), fetch(-2), fetch(-1);                           // now ok: tile 0, ok1: tile 1, ok2: tile 2
         at_barrier();
-        v16f sc[2];
-        float mx = 0.0f;
-        if (busy) {
-            att_scores(sc, r, ktile(0));
-            mx = att_max(sc);
-        }
-        int i = 0;
-        auto whole = [&](int i, uint64_t in) { return (t0 + i + 1) * kAtKeys <= s.ctx && in == ~0ull; };
-        while (i < n) {
-            while (i + 1 < n && whole(i, ok) && whole(i + 1, ok1)) {
-                v16f o[2];
+        if (!busy) {       // a wave without rows fetches its share of the tiles
+            for (int i = 0; i < n; ++i) {
                 step_barrier(i);
                 fetch(i);
-                if (busy) att_tile(r, sc, mx, o, ktile(i + 1), vtile(i), c);
-                step_barrier(i + 1);
-                fetch(i + 1);
-                if (busy) att_tile(r, o, mx, sc, ktile(i + 2), vtile(i + 1), c);
-                i += 2;
             }
-            if (i >= n) break;
-            const uint64_t in = ok;
-            step_barrier(i);
-            fetch(i);
-            if (busy) {
-                att_tile_masked(r, sc, ktile(i + 1), vtile(i), c, row.seen(s, (t0 + i) * kAtKeys) & in);
+        } else {
+            v16f sc[2];
+            att_scores(sc, r, ktile(0));
+            float mx = att_max(sc);
+            int i = 0;
+            auto whole = [&](int i, uint32_t in) { return (t0 + i + 1) * kAtKeys <= s.ctx && in == 15u; };
+            while (i < n) {
+                while (i + 1 < n && whole(i, ok) && whole(i + 1, ok1)) {
+                    v16f o[2];
+                    step_barrier(i);
+                    fetch(i);
+                    att_tile(r, sc, mx, o, ktile(i + 1), vtile(i), c);
+                    step_barrier(i + 1);
+                    fetch(i + 1);
+                    att_tile(r, o, mx, sc, ktile(i + 2), vtile(i + 1), c);
+                    i += 2;
+                }
+                if (i >= n) break;
+                const uint32_t in = ok;
+                step_barrier(i);
+                fetch(i);
+                att_tile_masked(r, sc, ktile(i + 1), vtile(i), c, row.seen(s, (t0 + i) * kAtKeys) & keys_of(in));
                 mx = att_max(sc);
+                ++i;
             }
-            ++i;
-        }
-        const float l = r.l + __shfl_xor(r.l, 32);
-        if (busy) {
+            const float l = r.l + __shfl_xor(r.l, 32);
             float v[DV / 2];
 #pragma unroll
             for (int d = 0; d < DV / 32; ++d)
@@ -726,7 +727,6 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p)
         l = l * old + (x.x == -INFINITY ? x.y : x.y * f);     // without a score above -inf: 0, or NaN
         o.x *= old, o.y *= old, o.z *= old, o.w *= old;
         const int n = min(TR, cut.last - r0 + 1);
-#pragma unroll 8
         for (int k = 0; k < n; ++k) {
             const float4 v = *reinterpret_cast<const float4 *>(p.part + place(r0 + k) * DV + 4 * part);
             const float g = __shfl(f, base + k);
