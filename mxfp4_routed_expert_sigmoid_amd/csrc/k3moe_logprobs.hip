@@ -22,7 +22,7 @@ namespace {
 constexpr int kLpThreads = 256, kLpWaves = kLpThreads / 64;
 constexpr int kLpMaxTop = 64, kLpCand = 1024;
 constexpr int kLpMaxVocab = 1 << 24, kLpMaxIds = 4096;
-constexpr int kLpShort = 16, kLpLong = 64;   // elements per thread
+constexpr int kLpShort = 16, kLpLong = 32;   // elements per thread
 
 struct LpStats {
     double rest, dev;   // sum of e^(x - m) but for the maxima, sum of (m - x) e^(x - m)
@@ -50,9 +50,6 @@ __device__ __forceinline__ float lp_logit(const LpParams &p, bool f32, int t, in
     const int64_t o = (int64_t)t * p.stride + i;
     return f32 ? static_cast<const float *>(p.x)[o] : bf16f(static_cast<const uint16_t *>(p.x)[o]);
 }
-
-// e^d for d <= 0: d log2(e) is rounded once, 2^-24 of |d| relative in the result.
-__device__ __forceinline__ float lp_exp(float d) { return __builtin_amdgcn_exp2f(d * 1.44269502f); }
 
 // Wave reductions through DPP, the result in every lane (read back from lane 63).
 template <class T, class F>
@@ -167,7 +164,7 @@ __device__ __forceinline__ void lp_collect(LpTop &L, uint64_t key)
 
 // One chunk of VPT * 256 logits of a row. W: neighbouring elements per load.
 template <int VPT, bool F32, int W>
-__global__ __launch_bounds__(kLpThreads, 4) void k_lp_chunk(LpParams p)
+__global__ __launch_bounds__(kLpThreads, 6) void k_lp_chunk(LpParams p)
 {
     __shared__ LpTop L;
     __shared__ float wmax[kLpWaves];
@@ -181,30 +178,37 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_lp_chunk(LpParams p)
     float v[VPT];
     const int64_t row = (int64_t)t * p.stride;
     const bool whole = base + VPT * kLpThreads <= p.V;
+    auto one = [&](int i) {
+        return F32 ? static_cast<const float *>(p.x)[row + i] : bf16f(static_cast<const uint16_t *>(p.x)[row + i]);
+    };
+    if (whole) {
 #pragma unroll
-    for (int j = 0; j < VPT; j += W) {
-        const int i = whole ? index(j) : min(index(j), p.V - 1) / W * W;
-        if (W > 1 && (whole || i + W <= p.V)) {
-            if constexpr (F32) {
-                const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + row + i);
+        for (int j = 0; j < VPT; j += W) {
+            if constexpr (W == 1) {
+                v[j] = one(index(j));
+            } else if constexpr (F32) {
+                const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + row + index(j));
                 v[j] = a.x, v[j + 1] = a.y, v[j + 2] = a.z, v[j + 3] = a.w;
             } else {
-                const u4 a = *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(p.x) + row + i);
+                const u4 a = *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(p.x) + row + index(j));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[j + 2 * e] = bf16f(a[e] & 0xffffu), v[j + 2 * e + 1] = bf16f(a[e] >> 16);
             }
-        } else {   // single elements, or the row's last ones
+        }
+    } else {   // a row's end, one by one
 #pragma unroll
-            for (int e = 0; e < W; ++e)
-                v[j + e] = F32 ? static_cast<const float *>(p.x)[row + min(i + e, p.V - 1)]
-                               : bf16f(static_cast<const uint16_t *>(p.x)[row + min(i + e, p.V - 1)]);
+        for (int j = 0; j < VPT; ++j) {
+            const float x = one(min(index(j), p.V - 1));
+            v[j] = index(j) < p.V ? x : -INFINITY;
         }
     }
-    float mine = -INFINITY;
+    float group[VPT / 8], mine = -INFINITY;          // maxima of eight elements each; they pass over NaN
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        if (!whole && index(j) >= p.V) v[j] = -INFINITY;
-        mine = fmaxf(mine, v[j]);          // passes over NaN
+    for (int g = 0; g < VPT / 8; ++g) {
+        group[g] = fmaxf(v[8 * g], v[8 * g + 1]);
+#pragma unroll
+        for (int j = 2; j < 8; j += 2) group[g] = fmaxf(fmaxf(group[g], v[8 * g + j]), v[8 * g + j + 1]);
+        mine = fmaxf(mine, group[g]);
     }
     // lanes without an element hold none of the chunk's largest
     const float wm = lp_wave(mine, -INFINITY, LpFmax());
@@ -219,44 +223,53 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_lp_chunk(LpParams p)
     float m = wmax[0];
 #pragma unroll
     for (int w = 1; w < kLpWaves; ++w) m = fmaxf(m, wmax[w]);
-    const float use = m == -INFINITY ? 0.0f : m;
-    float rest = 0.0f, dev = 0.0f;
+    // e^(x - m) = 2^(x L - mh) 2^-ml with mh + ml = m L: one rounding per element, and one factor for all
+    constexpr float L2E = 1.44269502f;
+    const float use = m == -INFINITY ? 0.0f : m, mh = use * L2E, ml = fmaf(use, L2E, -mh);
+    float rest = 0.0f, dev = 0.0f;                   // sums of e and of -(x L - mh) e
     int top = 0;
-    // -inf: e is 0, and so is its term of the deviation; +inf: d is NaN and stays
+    // -inf: e is 0, and so is its term of the deviation; +inf: x L - mh is NaN and stays
     if (wm == m && m < INFINITY) {         // the wave that holds the maximum counts it apart
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const float d = v[j] - use, e = lp_exp(d);
+            const float t = fmaf(v[j], L2E, -mh), e = __builtin_amdgcn_exp2f(t);
             const bool peak = v[j] == m;
             top += peak ? 1 : 0;
             rest += peak ? 0.0f : e;
-            dev = fmaf(-fmaxf(d, -256.0f), e, dev);
+            dev = fmaf(peak ? 0.0f : -fmaxf(t, -512.0f), e, dev);
         }
         if (m == -INFINITY) top = 0, rest = rest != rest ? rest : 0.0f;
     } else {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const float d = v[j] - use, e = lp_exp(d);
+            const float t = fmaf(v[j], L2E, -mh), e = __builtin_amdgcn_exp2f(t);
             rest += e;
-            dev = fmaf(-fmaxf(d, -256.0f), e, dev);
+            dev = fmaf(-fmaxf(t, -512.0f), e, dev);
         }
     }
     {
+        const double f = 1.0 - 0.69314718055994531 * (double)ml;   // 2^-ml: ml is below 2^-24 of |m L|, its square below any digit
         const double R = lp_wave<double>(rest, 0.0, LpAdd()), D = lp_wave<double>(dev, 0.0, LpAdd());
         const int N = lp_wave<int>(top, 0, LpAdd());
-        if (lane == 0) wsum[wave] = LpStats{R, D, m, N};
+        // sum of (m - x) e = (sum of -t e - ml sum of e) / L
+        if (lane == 0) wsum[wave] = LpStats{R * f, (D - (double)ml * R) * f * (1.0 / (double)L2E), m, N};
     }
     if (p.k > 0) {
         uint32_t bound = wbound[0];
 #pragma unroll
         for (int w = 1; w < kLpWaves; ++w) bound = max(bound, wbound[w]);
         if (__ballot(key >= bound && key)) {
+            // -inf and NaN, which rank alike, are among the largest only of a chunk with few others
+            const bool low = bound <= order_key(-INFINITY);
+            const float least = low ? -INFINITY : __uint_as_float(bound & 0x80000000u ? bound ^ 0x80000000u : ~bound);
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const uint32_t x = order_key(v[j] + 0.0f);
-                if (__ballot(x >= bound)) {
-                    const int i = index(j);
-                    if (x >= bound && i < p.V) lp_collect(L, ((uint64_t)x << 32) | (uint32_t)~(uint32_t)i);
+            for (int g = 0; g < VPT / 8; ++g) {
+                if (__ballot(low || group[g] >= least)) {
+#pragma unroll
+                    for (int j = 8 * g; j < 8 * g + 8; ++j) {
+                        const int i = index(j);
+                        if ((low || v[j] >= least) && i < p.V) lp_collect(L, lp_key(v[j], i));
+                    }
                 }
             }
         }
@@ -281,8 +294,9 @@ __global__ __launch_bounds__(kLpThreads, 4) void k_lp_chunk(LpParams p)
                       [&](int rank, uint64_t key) { out[rank] = key; });
 }
 
-// Joins a row's chunks: one block of W waves per row.
-template <bool F32, int W>
+// Joins a row's chunks: one block of W waves per row, whose threads hold the chunks' candidates, up to 64 W CPT of them
+// (CPT 0: any number, read again where they are needed). Everything that does not wait for the sums is loaded first.
+template <bool F32, int W, int CPT>
 __global__ __launch_bounds__(64 * W) void k_lp_join(LpParams p)
 {
     __shared__ LpTop L;
@@ -290,15 +304,31 @@ __global__ __launch_bounds__(64 * W) void k_lp_join(LpParams p)
     const LpStats *st = p.stats + (int64_t)t * p.chunks;
     const uint64_t *cand = p.cand + (int64_t)t * p.chunks * p.k;
     const int n = p.chunks * p.k;
+    const LpStats mine = tid < p.chunks ? st[tid] : LpStats{0.0, 0.0, -INFINITY, 0};
+    const int64_t ids0 = (int64_t)t * p.n_ids;
+    const int id0 = tid < p.n_ids ? p.ids[ids0 + tid] : -1;
+    uint64_t held[CPT > 0 ? CPT : 1];
     uint64_t best = 0ull;
-    for (int i = tid; i < n; i += 64 * W) best = cand[i] > best ? cand[i] : best;
-    float m = -INFINITY;
-    for (int c = tid; c < p.chunks; c += 64 * W) m = fmaxf(m, st[c].m);
+    if constexpr (CPT > 0) {
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) held[i] = tid + 64 * W * i < n ? cand[tid + 64 * W * i] : 0ull;
+    }
+    const float x0 = id0 >= 0 && id0 < p.V ? lp_logit(p, F32, t, id0) : NAN;
+    auto each = [&](auto f) {
+        if constexpr (CPT > 0) {
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) f(held[i]);
+        } else {
+            for (int i = tid; i < n; i += 64 * W) f(cand[i]);
+        }
+    };
+    each([&](uint64_t key) { best = key > best ? key : best; });
+    float m = mine.m;
+    for (int c = tid + 64 * W; c < p.chunks; c += 64 * W) m = fmaxf(m, st[c].m);
     m = lp_block<W, float>(m, -INFINITY, reinterpret_cast<float *>(L.red), LpFmax());
     double s = 0.0, dev = 0.0;
     int top = 0;
-    for (int c = tid; c < p.chunks; c += 64 * W) {
-        const LpStats x = st[c];
+    auto add = [&](const LpStats &x) {
         const double part = x.rest + x.top;
         if (x.m == m) {
             s += x.rest, dev += x.dev, top += x.top;
@@ -306,7 +336,9 @@ __global__ __launch_bounds__(64 * W) void k_lp_join(LpParams p)
             const double f = exp((double)x.m - (double)m);
             s += part * f, dev += f * (x.dev + ((double)m - (double)x.m) * part);
         }
-    }
+    };
+    add(mine);
+    for (int c = tid + 64 * W; c < p.chunks; c += 64 * W) add(st[c]);
     s = lp_block<W, double>(s, 0.0, reinterpret_cast<double *>(L.red), LpAdd());
     dev = lp_block<W, double>(dev, 0.0, reinterpret_cast<double *>(L.red), LpAdd());
     top = lp_block<W, int>(top, 0, reinterpret_cast<int *>(L.red), LpAdd());
@@ -314,28 +346,25 @@ __global__ __launch_bounds__(64 * W) void k_lp_join(LpParams p)
     const double log_s = top > 0 ? log1p(s + (top - 1)) : (double)NAN;
     const double peak = (double)m;
     if (p.ent && tid == 0) p.ent[t] = (float)(log_s + dev / (s + top));
-    for (int j = tid; j < p.n_ids; j += 64 * W) {
-        const int64_t o = (int64_t)t * p.n_ids + j;
-        const int i = p.ids[o];
-        p.lp[o] = i >= 0 && i < p.V ? (float)((double)lp_logit(p, F32, t, i) - peak - log_s) : NAN;
+    if (tid < p.n_ids) p.lp[ids0 + tid] = (float)((double)x0 - peak - log_s);
+    for (int j = tid + 64 * W; j < p.n_ids; j += 64 * W) {
+        const int i = p.ids[ids0 + j];
+        p.lp[ids0 + j] = i >= 0 && i < p.V ? (float)((double)lp_logit(p, F32, t, i) - peak - log_s) : NAN;
     }
     if (p.k == 0) return;
     if (tid == 0) L.count = 0;
     const uint32_t bound = lp_block<W, uint32_t>(lp_bound((uint32_t)(best >> 32), p.k), 0u, reinterpret_cast<uint32_t *>(L.red), LpMax());
     __syncthreads();
-    auto each = [&](auto f) {
-        for (int i = tid; i < n; i += 64 * W) f(cand[i]);
-    };
     if ((uint32_t)(best >> 32) >= bound)
         each([&](uint64_t key) {
             if (key && (uint32_t)(key >> 32) >= bound) lp_collect(L, key);
         });
     __syncthreads();
     lp_rank<W>(L, p.k, each, [&](int rank, uint64_t key) {
-        const int i = (int)~(uint32_t)key;
         const int64_t o = (int64_t)t * p.k + rank;
-        p.top_ids[o] = i;
-        p.top_lp[o] = (float)((double)lp_logit(p, F32, t, i) - peak - log_s);
+        const uint32_t b = (uint32_t)(key >> 32), v = b & 0x80000000u ? b ^ 0x80000000u : ~b;   // the logit of the key
+        p.top_ids[o] = (int)~(uint32_t)key;
+        p.top_lp[o] = (float)((double)__uint_as_float(v) - peak - log_s);
     });
 }
 
@@ -365,8 +394,10 @@ void launch_lp(const LpParams &p, bool vec, hipStream_t s)
         if (vec) k_lp_chunk<kLpShort, F32, W><<<grid, kLpThreads, 0, s>>>(p);
         else k_lp_chunk<kLpShort, F32, 1><<<grid, kLpThreads, 0, s>>>(p);
     }
-    if (p.chunks * (int64_t)p.k <= 4096) k_lp_join<F32, 1><<<(unsigned)p.T, 64, 0, s>>>(p);
-    else k_lp_join<F32, kLpWaves><<<(unsigned)p.T, kLpThreads, 0, s>>>(p);
+    const int64_t cand = p.chunks * (int64_t)p.k;
+    if (cand <= 256) k_lp_join<F32, 1, 4><<<(unsigned)p.T, 64, 0, s>>>(p);
+    else if (cand <= 1024) k_lp_join<F32, kLpWaves, 4><<<(unsigned)p.T, kLpThreads, 0, s>>>(p);
+    else k_lp_join<F32, kLpWaves, 0><<<(unsigned)p.T, kLpThreads, 0, s>>>(p);
 }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
