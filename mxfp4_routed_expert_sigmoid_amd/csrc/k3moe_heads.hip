@@ -16,7 +16,7 @@
 namespace k3moe {
 namespace {
 
-constexpr int kHdThreads = 256, kHdBatch = 4;   // heads in flight per lane
+constexpr int kHdThreads = 256, kHdBatch = 8;   // heads in flight per lane
 constexpr int kHdMaxTokens = 1 << 25;           // a launch's work-items are counted in 32 bits
 
 struct HeadsParams {
@@ -29,16 +29,16 @@ struct HeadsParams {
     int64_t qs, kst, vst, qos, kos, places;
     int T, Hq, Hkv, D, Dv, R, rot, page, lpage, split;
     int qi, ki, vi;   // steps of a token: queries, keys, values
-    float eps;
+    float eps, per_dim;   // 1 / D
 };
 
-__device__ __forceinline__ uint32_t hd_bf16(float f) { return f != f ? 0x7fc0u : bf16_rne_u32(f); }
-
+// Eight fp32 -> bf16, to nearest even; NaN stays NaN.
 __device__ __forceinline__ u4 hd_pack(const float (&y)[8])
 {
+    typedef float f8 __attribute__((ext_vector_type(8)));
+    const bf8 b = __builtin_convertvector((f8{y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]}), bf8);
     u4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = hd_bf16(y[2 * i]) | (hd_bf16(y[2 * i + 1]) << 16);
+    __builtin_memcpy(&r, &b, 16);
     return r;
 }
 
@@ -48,11 +48,38 @@ __device__ __forceinline__ void hd_unpack(u4 w, float (&x)[8])
     for (int i = 0; i < 4; ++i) x[2 * i] = bf16f(w[i] & 0xffffu), x[2 * i + 1] = bf16f(w[i] >> 16);
 }
 
+template <int CTRL>
+__device__ __forceinline__ float hd_dpp(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+
+// Sum over LH lanes, in each of them.
+template <int LH>
+__device__ __forceinline__ float hd_sum(float v)
+{
+    v += hd_dpp<0xb1>(v);                        // neighbours
+    v += hd_dpp<0x4e>(v);                        // pairs
+    v += hd_dpp<0x141>(v);                       // mirrored eights
+    if constexpr (LH > 8) v += hd_dpp<0x140>(v); // mirrored sixteens
+    if constexpr (LH > 16) v += __shfl_xor(v, 16);
+    return v;
+}
+
+// The value of the lane LH / 2 away among LH.
+template <int LH>
+__device__ __forceinline__ float hd_half(float v)
+{
+    if constexpr (LH == 8) return hd_dpp<0x1b>(hd_dpp<0x141>(v));   // 7 - i, then i ^ 3
+    if constexpr (LH == 16) return hd_dpp<0x128>(v);                // turned by eight
+    return __shfl_xor(v, 16);
+}
+
 // Maximum over the four lanes of a quad.
 __device__ __forceinline__ float quad_max(float m)
 {
-    m = fmaxf(m, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m), 0xb1, 0xf, 0xf, false)));
-    return fmaxf(m, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m), 0x4e, 0xf, 0xf, false)));
+    m = fmaxf(m, hd_dpp<0xb1>(m));
+    return fmaxf(m, hd_dpp<0x4e>(m));
 }
 
 // Eight values of row `row` of the cache at dimension e: bf16, or MXFP8 with the quad's lanes holding one group.
@@ -76,6 +103,19 @@ __device__ __forceinline__ void hd_cache(uint8_t *c, uint8_t *s, int64_t row, in
     if (e % 32 == 0) s[row * (dim / 32) + e / 32] = (uint8_t)(x + 127);
 }
 
+// Sine and cosine of t turns, |t| <= 1/2: the angle from the nearest quarter turn, r in [-pi/4, pi/4], and the series of
+// both there (their next terms, r^11 / 11! and r^10 / 10!, are below 2^-28 and 2^-25).
+__device__ __forceinline__ void turn_sincos(float t, float &s, float &c)
+{
+    const float q = rintf(4.0f * t), r = fmaf(q, -0.25f, t) * 6.28318531f, z = r * r;
+    const float a = fmaf(z * r, fmaf(z, fmaf(z, fmaf(z, 2.75573192e-6f, -1.98412698e-4f), 8.33333333e-3f), -0.166666667f), r);
+    const float b = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 2.48015873e-5f, -1.38888889e-3f), 4.16666667e-2f), -0.5f), 1.0f);
+    const int k = (int)q;
+    const float x = k & 1 ? b : a, y = k & 1 ? a : b;
+    s = k & 2 ? -x : x;
+    c = (k + 1) & 2 ? -y : y;
+}
+
 // LH lanes per head (D <= 8 LH). Wave w of token w / split takes the token's steps w % split, + split, ...: first the
 // queries' (64 / LH heads each), then the keys', then the values' (64 pieces of 16 bytes each).
 template <int LH>
@@ -92,24 +132,32 @@ __global__ __launch_bounds__(kHdThreads) void k_heads(HeadsParams p)
     const bool place = slot >= 0 && slot < p.places;
     const int64_t prow = place ? (slot >> p.lpage) * p.Hkv * p.page + (slot & (p.page - 1)) : 0;   // row of head 0
 
-    // sine and cosine for this lane's eight dimensions (0 and 1 behind the rotated ones)
-    float cs[8], sn[8];
+    // Sine and cosine for this lane's eight dimensions (0 and 1 behind the rotated ones), taken behind the first loads.
     const bool turns = e0 < p.R, pairs = p.rot == K3MOE_ROT_PAIRS;
+    const int pos = p.R > 0 ? p.pos[t] : 0;
+    float freq[8], cs[8], sn[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
-    if (turns && part < p.qi + p.ki) {
-        const double at = (double)p.pos[t] * 0.15915494309189535;   // 1 / (2 pi)
+    for (int j = 0; j < 8; ++j) {
+        const int i = pairs ? (e0 + j) / 2 : e0 + j < p.R / 2 ? e0 + j : e0 + j - p.R / 2;
+        freq[j] = turns ? p.freq[i] : 0.0f;
+    }
+    bool ready = false;
+    auto angles = [&]() {
+        if (ready) return;
+        ready = true;
+        const double at = (double)pos * 0.15915494309189535;   // 1 / (2 pi)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if (pairs && (j & 1)) {
-                cs[j] = cs[j - 1], sn[j] = sn[j - 1];
-                continue;
+            if (j & 1) {
+                if (pairs) {
+                    cs[j] = cs[j - 1], sn[j] = sn[j - 1];
+                    continue;
+                }
             }
-            const int i = pairs ? (e0 + j) / 2 : e0 + j < p.R / 2 ? e0 + j : e0 + j - p.R / 2;
-            const double turn = at * (double)p.freq[i];
-            sincospif(2.0f * (float)(turn - rint(turn)), &sn[j], &cs[j]);
+            const double turn = at * (double)freq[j];
+            turn_sincos((float)(turn - rint(turn)), sn[j], cs[j]);
         }
-    }
+    };
     // y1 = n1 c - n2 s, y2 = n2 c + n1 s: the second of a pair takes its sine with the other sign
     const bool first = e0 < p.R / 2;
     const int other = turns ? (lane - sub) + (first ? sub + p.R / 16 : sub - p.R / 16) : lane;
@@ -125,6 +173,7 @@ __global__ __launch_bounds__(kHdThreads) void k_heads(HeadsParams p)
                 const int head = min((s + b * p.split) * HW + lane / LH, H - 1);
                 raw[b] = *reinterpret_cast<const u4 *>(x + head * p.D + ec);
             }
+            angles();
 #pragma unroll
             for (int b = 0; b < kHdBatch; ++b) {
                 if (s + b * p.split >= steps) break;     // the same for the whole wave
@@ -136,10 +185,7 @@ __global__ __launch_bounds__(kHdThreads) void k_heads(HeadsParams p)
                     float ss = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
-                    if (!used) ss = 0.0f;
-#pragma unroll
-                    for (int o = 1; o < LH; o <<= 1) ss += __shfl_xor(ss, o);
-                    const float inv = 1.0f / sqrtf(ss / (float)p.D + p.eps);
+                    const float inv = __builtin_amdgcn_rsqf(fmaf(hd_sum<LH>(used ? ss : 0.0f), p.per_dim, p.eps));   // within an ulp
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] = y[j] * inv * g[j];
                 }
@@ -148,6 +194,9 @@ __global__ __launch_bounds__(kHdThreads) void k_heads(HeadsParams p)
                     if (pairs) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) z[j] = y[j ^ 1];
+                    } else if (p.R == 8 * LH) {      // the whole head: the lane half a head away
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) z[j] = hd_half<LH>(y[j]);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) z[j] = __shfl(y[j], other);
@@ -240,7 +289,7 @@ extern "C" k3moe_status k3moe_qk_norm_rope(const uint16_t *q, int64_t q_stride, 
     p.q = q, p.k = k, p.v = v, p.qo = q_out, p.ko = k_out, p.gq = gamma_q, p.gk = gamma_k, p.freq = inv_freq;
     p.pos = positions, p.slots = slots;
     p.qs = q_stride, p.kst = k_stride, p.vst = v_stride, p.qos = q_out_stride, p.kos = k_out_stride;
-    p.T = T, p.Hq = q_heads, p.Hkv = kv_heads, p.D = dim, p.Dv = v_dim, p.R = rot_dim, p.rot = rot_kind, p.eps = eps;
+    p.T = T, p.Hq = q_heads, p.Hkv = kv_heads, p.D = dim, p.Dv = v_dim, p.R = rot_dim, p.rot = rot_kind, p.eps = eps, p.per_dim = 1.0f / (float)dim;
     if (cache && cache->pages > 0) {
         p.kc = static_cast<uint8_t *>(cache->k), p.vc = static_cast<uint8_t *>(cache->v), p.ks = cache->ks, p.vs = cache->vs;
         p.page = cache->page, p.lpage = __builtin_ctz((unsigned)cache->page), p.places = (int64_t)cache->pages * cache->page;
