@@ -8,6 +8,7 @@ no fallback path.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -60,11 +61,6 @@ class Weights(ctypes.Structure):
 class CacheStats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in ("steps", "requests", "resident_hits", "misses",
                                                 "evictions", "dropped", "bytes_read")]
-
-
-class Pages(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("vs", ctypes.c_void_p),
-                ("pages", ctypes.c_int32), ("page", ctypes.c_int32)]
 
 
 _lib = None
@@ -143,17 +139,16 @@ def lib():
         L.k3moe_glu.restype = st
         L.k3moe_glu.argtypes = [P, P, P, P, i32, i32, P, i64, P, i64, i32, i32, f32, f32, P, i64, P, i64, i32, P]
         size, sz = ctypes.POINTER(ctypes.c_size_t), ctypes.c_size_t
-        pages = ctypes.POINTER(Pages)
         L.k3moe_qk_norm_rope.restype = st
         L.k3moe_qk_norm_rope.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, i32, i32, P, P, f32, P, P, i32, i32,
-                                         P, i64, P, i64, pages, P, P]
+                                         P, i64, P, i64, P, P, P]
         L.k3moe_attention.restype = st
         L.k3moe_attention.argtypes = [P, i64, P, i64, P, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, i32, P,
                                       i64, P, P]
         L.k3moe_tree_attention_workspace_size.restype = st
         L.k3moe_tree_attention_workspace_size.argtypes = [i32, i32, i32, i32, size]
         L.k3moe_tree_attention.restype = st
-        L.k3moe_tree_attention.argtypes = [P, i64, pages, P, i32, P, P, P, i32, i32, i32, i32, i32, i32, i32, f32, P,
+        L.k3moe_tree_attention.argtypes = [P, i64, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32, i32, f32, P,
                                            i64, P, P, sz, P]
         L.k3moe_logprobs_workspace_size.restype = st
         L.k3moe_logprobs_workspace_size.argtypes = [i32, i32, i32, size]
@@ -666,8 +661,8 @@ def glu(gate_packed, gate_scales, up_packed, up_scales, x, out, xs=None, outs=No
 # k3moe_tree_attention, k3moe_logprobs): functions over device tensors with the
 # dense operators' rules. Heads are [T][heads][dim] views, rows possibly part of
 # a wider projection; cache pages are [pages][heads][page][dim].
-_BF16_VALUES = (torch.bfloat16, torch.int16, torch.uint16)
 _I32, _I64 = (torch.int32,), (torch.int64,)
+_PAGES = struct.Struct("PPPPii").pack     # k3moe_pages, as bytes: a third of the time of a ctypes structure
 
 
 def _heads(t, rows, heads, dim, name, dev):
@@ -675,23 +670,27 @@ def _heads(t, rows, heads, dim, name, dev):
     `dev` whose rows are contiguous. Returns its address and row stride."""
     if t.shape != (rows, heads, dim):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, heads, dim)}")
-    if t.dtype not in _BF16_VALUES:
+    if t.dtype not in _BF16:
         raise ValueError(f"{name}: {t.dtype}, expected torch.bfloat16")
-    width = heads * dim
-    if rows >> 31 or width >> 31:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, rows and columns are counted in 32 bits")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{dev}" if dev >= 0 else "a GPU"))
-    if t.is_contiguous():
-        return t.data_ptr(), width
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     st, head, unit = t.stride()
-    if (unit != 1 and dim > 1) or (head != dim and heads > 1):
-        raise ValueError(f"{name}: a row's heads must be contiguous")
-    if rows < 2:
-        return t.data_ptr(), width
-    if st < width:
-        raise ValueError(f"{name}: rows overlap (stride {st}, width {width})")
-    return t.data_ptr(), st
+    width = heads * dim
+    if unit != 1 or head != dim or st < width:     # (strides of single entries are not used)
+        if (unit != 1 and dim > 1) or (head != dim and heads > 1):
+            raise ValueError(f"{name}: a row's heads must be contiguous")
+        if st < width and rows > 1:
+            raise ValueError(f"{name}: rows overlap (stride {st}, width {width})")
+    return t.data_ptr(), st if rows > 1 else width
+
+
+def _counted(dev, *sizes):
+    """Refuse tensors that are not on a GPU, or whose sizes 32 bits do not count."""
+    if dev < 0:
+        raise ValueError("expected tensors on a GPU")
+    for n in sizes:
+        if n >> 31:
+            raise ValueError(f"a size of {n}: sizes are counted in 32 bits")
 
 
 def _flat(t, shape, dtypes, name, dev):
@@ -699,29 +698,28 @@ def _flat(t, shape, dtypes, name, dev):
     if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous "
                          f"{' or '.join(str(d) for d in dtypes)} {tuple(shape)}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{dev}" if dev >= 0 else "a GPU"))
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     return t.data_ptr()
 
 
-def _cache(kc, vc, ks, vs, dim, v_dim, dev):
-    """(Pages, heads) of cache tensors [pages][heads][page][dim], MXFP8 with ks and vs."""
-    if kc.dim() != 4 or vc.dim() != 4:
-        raise ValueError(f"kc, vc: shapes {tuple(kc.shape)} and {tuple(vc.shape)}, expected [pages][heads][page][dim]")
-    n, heads, page = kc.shape[:3]
-    if n >> 31 or page >> 31 or heads >> 31:
+def _cache(kc, vc, ks, vs, heads, dim, v_dim, dev):
+    """k3moe_pages of cache tensors [pages][heads][page][dim], MXFP8 with ks and vs."""
+    if kc.dim() != 4:
+        raise ValueError(f"kc: shape {tuple(kc.shape)}, expected [pages][heads][page][dim]")
+    n, _, page, _ = kc.shape
+    if (n | page) >> 31:
         raise ValueError(f"kc: shape {tuple(kc.shape)}, pages and rows are counted in 32 bits")
-    if (ks is None) != (vs is None):
+    if ks is None and vs is None:
+        return _PAGES(_flat(kc, (n, heads, page, dim), _BF16, "kc", dev), _flat(vc, (n, heads, page, v_dim), _BF16, "vc", dev),
+                      0, 0, n, page)
+    if ks is None or vs is None:
         raise ValueError("ks and vs go together")
-    types = _BF16_VALUES if ks is None else _E4M3
-    k = _flat(kc, (n, heads, page, dim), types, "kc", dev)
-    v = _flat(vc, (n, heads, page, v_dim), types, "vc", dev)
-    if ks is None:
-        return Pages(k, v, None, None, n, page), heads
     if dim % 32 or v_dim % 32:
         raise ValueError(f"kc, vc: head widths {dim} and {v_dim}, an MXFP8 cache takes multiples of 32")
-    return Pages(k, v, _flat(ks, (n, heads, page, dim // 32), _E8M0, "ks", dev),
-                 _flat(vs, (n, heads, page, v_dim // 32), _E8M0, "vs", dev), n, page), heads
+    return _PAGES(_flat(kc, (n, heads, page, dim), _E4M3, "kc", dev), _flat(vc, (n, heads, page, v_dim), _E4M3, "vc", dev),
+                  _flat(ks, (n, heads, page, dim // 32), _E8M0, "ks", dev),
+                  _flat(vs, (n, heads, page, v_dim // 32), _E8M0, "vs", dev), n, page)
 
 
 def _scratch_ok(workspace, dev):
@@ -757,6 +755,7 @@ def qk_norm_rope(q, k, positions, inv_freq, gamma_q=None, gamma_k=None, eps=1e-6
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     dev = q.get_device()
+    _counted(dev, T, Hq, Hkv, D)
     qp, qst = _heads(q, T, Hq, D, "q", dev)
     kp, kst = _heads(k, T, Hkv, D, "k", dev)
     gqp = None if gamma_q is None else _vec(gamma_q, D, "gamma_q", dev)
@@ -766,31 +765,32 @@ def qk_norm_rope(q, k, positions, inv_freq, gamma_q=None, gamma_k=None, eps=1e-6
     if inv_freq is not None:
         if inv_freq.dim() != 1:
             raise ValueError(f"inv_freq: shape {tuple(inv_freq.shape)}, expected [rot_dim / 2]")
-        R = 2 * inv_freq.shape[0]
-        fp = _vec(inv_freq, R // 2, "inv_freq", dev) if R else None
-        pp = _flat(positions, (T,), _I32, "positions", dev) if R else None
+        R = inv_freq.shape[0]
+        if R:
+            _counted(dev, 2 * R)
+            fp = _vec(inv_freq, R, "inv_freq", dev)
+            pp = _flat(positions, (T,), _I32, "positions", dev)
+            R *= 2
     op = kop = None
     ost = kost = 0
     written = ()
     if q_out is not None:
         op, ost = _heads(q_out, T, Hq, D, "q_out", dev)
-        written += (q_out,)
+        written = (q_out,)
     if k_out is not None:
         kop, kost = _heads(k_out, T, Hkv, D, "k_out", dev)
         written += (k_out,)
     vp = sp = cache = None
     vst = Dv = 0
-    given = [x is not None for x in (kc, vc, v, slots)]
-    if any(given) or ks is not None or vs is not None:
-        if not all(given):
+    if kc is not None or vc is not None or v is not None or slots is not None or ks is not None or vs is not None:
+        if kc is None or vc is None or v is None or slots is None:
             raise ValueError("kc, vc, v and slots go together")
         if v.dim() != 3:
             raise ValueError(f"v: shape {tuple(v.shape)}, expected [T][heads][dim]")
         Dv = v.shape[2]
+        _counted(dev, Dv)
         vp, vst = _heads(v, T, Hkv, Dv, "v", dev)
-        cache, heads = _cache(kc, vc, ks, vs, D, Dv, dev)
-        if heads != Hkv:
-            raise ValueError(f"kc: {heads} heads, k has {Hkv}")
+        cache = _cache(kc, vc, ks, vs, Hkv, D, Dv, dev)
         sp = _flat(slots, (T,), _I64, "slots", dev)
         written += (kc, vc) if ks is None else (kc, vc, ks, vs)
     if _grad_enabled():
@@ -821,6 +821,7 @@ def attention(q, k, v, cu_q, out, cu_k=None, scale=None, causal=True, lse=None, 
     Tq, Hq, D = q.shape
     Tk, Hkv, Dv = v.shape
     dev = q.get_device()
+    _counted(dev, Tq, Tk, Hq, Hkv, D, Dv)
     qp, qst = _heads(q, Tq, Hq, D, "q", dev)
     kp, kst = _heads(k, Tk, Hkv, D, "k", dev)
     vp, vst = _heads(v, Tk, Hkv, Dv, "v", dev)
@@ -828,6 +829,7 @@ def attention(q, k, v, cu_q, out, cu_k=None, scale=None, causal=True, lse=None, 
     op, ost = _heads(out, Tq, Hq, Dv, "out", dev)
     if cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError(f"cu_q: shape {tuple(cu_q.shape)}, expected [sequences + 1]")
+    _counted(dev, cu_q.shape[0])
     cqp = _flat(cu_q, cu_q.shape, _I32, "cu_q", dev)
     ckp = None if cu_k is None else _flat(cu_k, cu_q.shape, _I32, "cu_k", dev)
     lp = None if lse is None else _flat(lse, (Tq, Hq), _F32, "lse", dev)
@@ -872,13 +874,13 @@ def tree_attention(q, kc, vc, pages, lens, out, ks=None, vs=None, cu_q=None, max
     Tq, Hq, D = q.shape
     Dv = vc.shape[3]
     B, width = pages.shape
+    Hkv = kc.shape[1]
     dev = q.get_device()
+    _counted(dev, Tq, Hq, D, Dv, B, width, Hkv)
     qp, qst = _heads(q, Tq, Hq, D, "q", dev)
-    cache, Hkv = _cache(kc, vc, ks, vs, D, Dv, dev)
+    cache = _cache(kc, vc, ks, vs, Hkv, D, Dv, dev)
     _group(Hq, Hkv)
     op, ost = _heads(out, Tq, Hq, Dv, "out", dev)
-    if B >> 31 or width >> 31:
-        raise ValueError(f"pages: shape {tuple(pages.shape)}, rows and columns are counted in 32 bits")
     pp = _flat(pages, (B, width), _I32, "pages", dev)
     np_ = _flat(lens, (B,), _I32, "lens", dev)
     cqp = None if cu_q is None else _flat(cu_q, (B + 1,), _I32, "cu_q", dev)
@@ -886,6 +888,7 @@ def tree_attention(q, kc, vc, pages, lens, out, ks=None, vs=None, cu_q=None, max
         if cu_q is not None:
             raise ValueError("max_q: with cu_q the most drafted tokens of a sequence must be given")
         max_q = max(Tq // B, 1) if B else 1
+    _counted(dev, max_q)
     tp = None if tree is None else _flat(tree, (Tq,), _I64, "tree", dev)
     lp = None if lse is None else _flat(lse, (Tq, Hq), _F32, "lse", dev)
     _scratch_ok(workspace, dev)
@@ -934,6 +937,7 @@ def logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=None,
         if ids.dim() != 2:
             raise ValueError(f"ids: shape {tuple(ids.shape)}, expected [T][M]")
         M = ids.shape[1]
+        _counted(dev, M)
         ip, op = _flat(ids, (T, M), _I32, "ids", dev), _flat(lp, (T, M), _F32, "lp", dev)
         written += (lp,)
     if entropy is not None:
@@ -943,6 +947,7 @@ def logprobs(logits, ids=None, lp=None, entropy=None, top_ids=None, top_lp=None,
         if top_ids.dim() != 2:
             raise ValueError(f"top_ids: shape {tuple(top_ids.shape)}, expected [T][k]")
         k = top_ids.shape[1]
+        _counted(dev, k)
         tip, tlp = _flat(top_ids, (T, k), _I32, "top_ids", dev), _flat(top_lp, (T, k), _F32, "top_lp", dev)
         written += (top_ids, top_lp)
     _scratch_ok(workspace, dev)

@@ -17,7 +17,7 @@ BIG = 2 ** 31 - 1
 
 
 def _pages(k=A, v=A, ks=None, vs=None, pages=4, page=16):
-    return ctypes.byref(k3.Pages(k, v, ks, vs, pages, page))
+    return k3._PAGES(k or 0, v or 0, ks or 0, vs or 0, pages, page)
 
 
 def _heads(**kw):
@@ -215,6 +215,21 @@ def test_binding_refuses_wrong_tensors_of_logprobs(monkeypatch):
         dict(ids=_z(3, dtype=I32)), dict(lp=_z(3, 1)), dict(entropy=_z(3, 1)), dict(entropy=_z(3, dtype=BF)),
         dict(top_ids=_z(3, 3, dtype=I32)), dict(top_lp=_z(3, 4, dtype=BF)), dict(logits=torch.zeros(3, 50)),
         dict(workspace=_Dev(torch.zeros(10, dtype=U8), "cuda:1"))])
+
+
+def test_binding_refuses_sizes_past_32_bits(monkeypatch):
+    """A size would be cut to its low 32 bits on its way into the library."""
+    monkeypatch.setattr(k3, "lib", lambda: pytest.fail("the call was made"))
+    wide = _Dev(torch.empty(1, 1, 64, dtype=BF).expand(2 ** 32 + 2, 1, 64))
+    with pytest.raises(ValueError, match="counted in 32 bits"):
+        k3.qk_norm_rope(wide, wide, None, None, q_out=wide)
+    with pytest.raises(ValueError, match="counted in 32 bits"):
+        k3.attention(wide, wide, wide, _z(2, dtype=I32), wide)
+    pool = _Dev(torch.empty(1, 1, 16, 64, dtype=BF).expand(2 ** 32 + 2, 1, 16, 64))
+    with pytest.raises(ValueError, match="counted in 32 bits"):
+        k3.tree_attention(_z(2, 1, 64, dtype=BF), pool, pool, _z(2, 1, dtype=I32), _z(2, dtype=I32), _z(2, 1, 64, dtype=BF))
+    with pytest.raises(ValueError, match="counted in 32 bits"):
+        k3.logprobs(_Dev(torch.empty(1, 8).expand(2 ** 32 + 2, 8)), entropy=_z(3))
 
 
 def _tracked(*shape, dtype=torch.float32):
