@@ -528,12 +528,19 @@ k3moe_status k3moe_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint1
  * (k_dim, v_dim): (64, 64), (128, 128) or (192, 128), others
  * K3MOE_E_UNSUPPORTED_SHAPE; scale > 0 and finite. Rows 16-byte aligned, strides
  * up to 2^24 elements. Scores and sums are fp32; the weights are rounded to bf16
- * for their product with the values. */
+ * for their product with the values.
+ *   workspace  optional: with one of k3moe_attention_workspace_size bytes (which
+ *              may be 0: not used) few queries over many keys are split over
+ *              more of the card; NULL = they are not. The results of the two
+ *              agree to their rounding. */
+k3moe_status k3moe_attention_workspace_size(int32_t seqs, int32_t Tq, int32_t Tk, int32_t q_heads,
+                                            int32_t v_dim, size_t *bytes);
 k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
                              const uint16_t *v, int64_t v_stride, const int32_t *cu_q, const int32_t *cu_k,
                              int32_t seqs, int32_t Tq, int32_t Tk, int32_t q_heads, int32_t kv_heads,
                              int32_t k_dim, int32_t v_dim, float scale, int32_t causal, uint16_t *out,
-                             int64_t out_stride, float *lse, void *stream);
+                             int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                             void *stream);
 
 /* Attention of drafted tokens over the cache. Sequence b has lens[b] tokens of
  * context at positions 0 .. lens[b) and n_b drafted ones whose keys and values

@@ -70,7 +70,7 @@ EXPORTS = ("k3moe_layer_create", "k3moe_workspace_size", "k3moe_route", "k3moe_f
            "k3moe_cache_forward", "k3moe_cache_stats_read", "k3moe_cache_slots", "k3moe_cache_reset", "k3moe_cache_destroy",
            "k3moe_error_count", "k3moe_error_reset", "k3moe_profile_enable",
            "k3moe_profile_read", "k3moe_layer_destroy", "k3moe_status_string",
-           "k3moe_add_norm", "k3moe_linear", "k3moe_glu", "k3moe_qk_norm_rope", "k3moe_attention",
+           "k3moe_add_norm", "k3moe_linear", "k3moe_glu", "k3moe_qk_norm_rope", "k3moe_attention_workspace_size", "k3moe_attention",
            "k3moe_tree_attention_workspace_size", "k3moe_tree_attention", "k3moe_logprobs_workspace_size",
            "k3moe_logprobs")
 STAGES = ("router", "topk", "perm", "gateup", "shared_gateup", "down", "combine",
@@ -144,7 +144,9 @@ def lib():
                                          P, i64, P, i64, P, P, P]
         L.k3moe_attention.restype = st
         L.k3moe_attention.argtypes = [P, i64, P, i64, P, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, i32, P,
-                                      i64, P, P]
+                                      i64, P, P, sz, P]
+        L.k3moe_attention_workspace_size.restype = st
+        L.k3moe_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32, size]
         L.k3moe_tree_attention_workspace_size.restype = st
         L.k3moe_tree_attention_workspace_size.argtypes = [i32, i32, i32, i32, size]
         L.k3moe_tree_attention.restype = st
@@ -811,11 +813,24 @@ def _group(Hq, Hkv):
         raise ValueError(f"{Hq} query heads over {Hkv} key heads")
 
 
-def attention(q, k, v, cu_q, out, cu_k=None, scale=None, causal=True, lse=None, stream=None):
+def _attention_bytes(seqs, Tq, Tk, q_heads, v_dim):
+    n = ctypes.c_size_t()
+    _check(lib().k3moe_attention_workspace_size(seqs, Tq, Tk, q_heads, v_dim, ctypes.byref(n)),
+           "k3moe_attention_workspace_size")
+    return n.value
+
+
+def attention_workspace(seqs, Tq, Tk, q_heads, v_dim, device=None):
+    """A device byte tensor for ``attention``."""
+    return torch.empty(_attention_bytes(seqs, Tq, Tk, q_heads, v_dim) + 256, dtype=torch.uint8, device=device or "cuda")
+
+
+def attention(q, k, v, cu_q, out, cu_k=None, scale=None, causal=True, lse=None, workspace=None, stream=None):
     """k3moe_attention: out bf16 [Tq][Hq][Dv] of packed sequences. q bf16
     [Tq][Hq][D], k bf16 [Tk][Hkv][D], v bf16 [Tk][Hkv][Dv]; cu_q int32 [seqs + 1]
     offsets of the sequences, cu_k those of their keys (None: cu_q); scale None:
-    D ** -0.5; lse fp32 [Tq][Hq] (None: not written)."""
+    D ** -0.5; lse fp32 [Tq][Hq] (None: not written); workspace from
+    ``attention_workspace`` (None: a new one where few queries have many keys)."""
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, v: expected [T][heads][dim]")
     Tq, Hq, D = q.shape
@@ -833,14 +848,22 @@ def attention(q, k, v, cu_q, out, cu_k=None, scale=None, causal=True, lse=None, 
     cqp = _flat(cu_q, cu_q.shape, _I32, "cu_q", dev)
     ckp = None if cu_k is None else _flat(cu_k, cu_q.shape, _I32, "cu_k", dev)
     lp = None if lse is None else _flat(lse, (Tq, Hq), _F32, "lse", dev)
+    _scratch_ok(workspace, dev)
     written = (out,) if lse is None else (out, lse)
     if _grad_enabled():
         _untracked(written)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
-            return attention(q, k, v, cu_q, out, cu_k, scale, causal, lse, stream)
-    status = lib().k3moe_attention(qp, qst, kp, kst, vp, vst, cqp, ckp, cu_q.shape[0] - 1, Tq, Tk, Hq, Hkv, D, Dv,
-                                   D ** -0.5 if scale is None else scale, 1 if causal else 0, op, ost, lp,
+            return attention(q, k, v, cu_q, out, cu_k, scale, causal, lse, workspace, stream)
+    wp, wn = None, 0
+    seqs = cu_q.shape[0] - 1
+    # (a split takes 512 keys or more; its size is asked for only then)
+    if workspace is not None or Tk >= 512 and (Dv == 64 or Dv == 128):
+        size = 1 if workspace is not None else _attention_bytes(seqs, Tq, Tk, Hq, Dv)
+        if size:
+            workspace, wp, wn = _scratch(workspace, lambda: size, q.device, stream)
+    status = lib().k3moe_attention(qp, qst, kp, kst, vp, vst, cqp, ckp, seqs, Tq, Tk, Hq, Hkv, D, Dv,
+                                   D ** -0.5 if scale is None else scale, 1 if causal else 0, op, ost, lp, wp, wn,
                                    _queue(dev, stream))
     if status:
         raise K3MoeError(status, "k3moe_attention")

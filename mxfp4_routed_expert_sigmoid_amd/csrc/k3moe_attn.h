@@ -136,6 +136,18 @@ struct RowStage {
 };
 #endif
 
+// The sum over the lanes up to and with this one.
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // one lane to the right, within a row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row 0 into 1, 2 into 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row 1 into 2 and 3
+    return v;
+}
+
 // Waits for this wave's loads and LDS operations, then for the block.
 __device__ __forceinline__ void at_barrier()
 {
@@ -429,7 +441,7 @@ __device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, v16f (&s)[2], float
 // whatever its key and value hold. The next scores take the place of this tile's.
 template <int DK, int DV>
 __device__ __forceinline__ void att_tile_masked(AttRows<DK, DV> &r, v16f (&s)[2], const uint8_t *nk, const uint8_t *vt, float c,
-                                                uint64_t seen)
+                                                uint64_t seen, bool more)
 {
     att_mask(s, seen);
     att_raise(r, att_max(s), c);
@@ -442,7 +454,7 @@ __device__ __forceinline__ void att_tile_masked(AttRows<DK, DV> &r, v16f (&s)[2]
     } else {
         att_values<false>(r, p, vt);
     }
-    att_scores(s, r, nk);
+    if (more) att_scores(s, r, nk);
 }
 
 }  // namespace k3moe

@@ -73,18 +73,6 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b)
     return s;
 }
 
-// The sum over the lanes up to and with this one.
-__device__ __forceinline__ int wave_scan(int v)
-{
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // one lane to the right, within a row
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row 0 into 1, 2 into 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row 1 into 2 and 3
-    return v;
-}
-
 // The line of units and a block's run of it. Runs of `per` units follow each other regardless of segments (a segment:
 // the units of one sequence, head and block of rows), or, where the runs of segments cut on their own fit the blocks
 // too, begin with the segments: a block then has one segment instead of up to two ends, one after the other.
@@ -673,7 +661,8 @@ __global__ __launch_bounds__(64 * kTrWaves, 1) void k_tree_wide(TreeParams p)
                 const uint32_t in = ok;
                 step_barrier(i);
                 fetch(i);
-                att_tile_masked(r, sc, ktile(i + 1), vtile(i), c, row.seen(s, (t0 + i) * kAtKeys) & keys_of(in));
+                att_tile_masked(r, sc, ktile(i + 1), vtile(i), c, row.seen(s, (t0 + i) * kAtKeys) & keys_of(in),
+                                i + 1 < n);
                 mx = att_max(sc);
                 ++i;
             }

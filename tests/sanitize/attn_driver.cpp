@@ -38,7 +38,7 @@ static k3moe_status heads(int32_t T, int32_t Hq, int32_t D, int64_t st, int32_t 
 static k3moe_status att(int32_t seqs, int32_t T, int32_t Hq, int32_t Hkv, int64_t st, float scale, uintptr_t off)
 {
     return k3moe_attention(at<h16>(off), st, at<h16>(), st, at<h16>(), st, at<int32_t>(), nullptr, seqs, T, T, Hq, Hkv, 128, 128,
-                           scale, 1, at<h16>(), st, nullptr, nullptr);
+                           scale, 1, at<h16>(), st, nullptr, at<void>(128), 0, nullptr);
 }
 
 static k3moe_status tree(int32_t seqs, int32_t T, int32_t Hq, int32_t width, int32_t page, int64_t st, size_t bytes)
@@ -75,8 +75,13 @@ int main()
     EXPECT(att(1, 5, 8, 3, 1024, 1.0f, 0), K3MOE_E_INVALID_ARG);
     EXPECT(att(1, 5, 8, 8, 1024, -INFINITY, 0), K3MOE_E_INVALID_ARG);
     EXPECT(att(1, 5, 8, 8, 1024, 1.0f, 4), K3MOE_E_ALIGNMENT);
+    EXPECT(att(1, 5, 8, 8, 1024, 1.0f, 0), K3MOE_E_WORKSPACE);             // misaligned
 
     size_t n = 0;
+    EXPECT(k3moe_attention_workspace_size(big, big, big, big, 128, &n), K3MOE_OK);
+    EXPECT(k3moe_attention_workspace_size(1, 1, big, 1, 128, &n), K3MOE_OK);
+    EXPECT(k3moe_attention_workspace_size(0, 0, 0, big, 64, &n), K3MOE_OK);
+    EXPECT(k3moe_attention_workspace_size(INT32_MIN, 1, 1, 1, 64, &n), K3MOE_E_INVALID_ARG);
     EXPECT(k3moe_tree_attention_workspace_size(4096, 1, 128, 64, &n), K3MOE_OK);
     EXPECT(k3moe_tree_attention_workspace_size(big, 1, 128, 64, &n), K3MOE_E_UNSUPPORTED_SHAPE);
     EXPECT(k3moe_tree_attention_workspace_size(INT32_MIN, -1, 128, 64, &n), K3MOE_E_INVALID_ARG);

@@ -54,7 +54,7 @@ def test_qk_norm_rope_refusals(kw, status):
 
 def _att(**kw):
     a = dict(q=A, qst=512, k=A, kst=128, v=A, vst=128, cq=A, ck=A, seqs=2, Tq=9, Tk=9, Hq=8, Hkv=2, D=64, Dv=64, scale=0.125,
-             causal=1, out=A, ost=512, lse=A)
+             causal=1, out=A, ost=512, lse=A, ws=None, n=0)
     a.update(kw)
     return k3.lib().k3moe_attention(*a.values(), None)
 
@@ -70,10 +70,26 @@ def _att(**kw):
     (dict(ost=2 ** 24 + 8), SHAPE), (dict(Tq=BIG, seqs=BIG), SHAPE), (dict(Tq=BIG, seqs=1), SHAPE),
     (dict(q=A + 8), ALIGN), (dict(k=A + 2), ALIGN), (dict(v=A + 8), ALIGN), (dict(out=A + 8), ALIGN), (dict(qst=516), ALIGN),
     (dict(kst=132), ALIGN), (dict(vst=132), ALIGN), (dict(ost=516), ALIGN), (dict(cq=A + 2), ALIGN), (dict(ck=A + 2), ALIGN),
-    (dict(lse=A + 2), ALIGN), (dict(seqs=0), OK), (dict(Tq=0, q=None, out=None, cq=None), OK),
+    (dict(lse=A + 2), ALIGN), (dict(ws=A + 128, n=1 << 30), WORKSPACE), (dict(ws=A, Tk=9000, n=100), WORKSPACE),
+    (dict(ws=A, Tk=9000, n="short"), WORKSPACE), (dict(seqs=0), OK), (dict(Tq=0, q=None, out=None, cq=None), OK),
 ])
 def test_attention_refusals(kw, status):
+    if kw.get("n") == "short":
+        kw = dict(kw, n=k3._attention_bytes(2, 9, 9000, 8, 64) - 1)
     assert _att(**kw) == status
+
+
+def test_attention_workspace_refusals():
+    n = ctypes.c_size_t()
+    f = k3.lib().k3moe_attention_workspace_size
+    assert f(1, 100, 9000, 8, 128, ctypes.byref(n)) == OK and n.value > 0
+    assert f(1, 100, 100, 8, 128, ctypes.byref(n)) == OK and n.value == 0        # nothing to split
+    assert f(BIG, BIG, BIG, BIG, 128, ctypes.byref(n)) == OK and n.value == 0
+    assert f(0, 0, 0, 1, 64, ctypes.byref(n)) == OK and n.value == 0
+    for a, want in (((-1, 1, 1, 1, 64), INVALID), ((1, -1, 1, 1, 64), INVALID), ((1, 1, -1, 1, 64), INVALID),
+                    ((1, 1, 1, 0, 64), INVALID), ((1, 1, 1, 1, 96), SHAPE)):
+        assert f(*a, ctypes.byref(n)) == want
+    assert f(1, 1, 1, 1, 64, None) == INVALID
 
 
 def _tree(**kw):

@@ -72,7 +72,7 @@ def test_packed(D, Dv, causal):
 @pytest.mark.parametrize("D,Dv", DIMS)
 @pytest.mark.parametrize("causal", [True, False])
 def test_more_tiles_than_cus(D, Dv, causal):
-    """Whole tiles per block; with few of them, as in most tests here, two halves of a block share a tile's keys."""
+    """Two blocks on most CUs."""
     _case([257, 1, 130, 64], [257, 40, 700, 64], 96, 8, D, Dv, causal, heads=[0, 37, 95], tail=2)
 
 
@@ -147,6 +147,61 @@ def test_scores_that_are_not_finite():
     assert torch.isnan(o[20]).all() and torch.isnan(o[30]).all() and (o[40] == 0).all() and lse[40] == float("-inf")
     rest = [i for i in range(90) if i not in (20, 30, 40)]
     assert torch.isfinite(o[rest]).all()
+
+
+@pytest.mark.parametrize("D,Dv", DIMS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,H", [
+    ([1], [512], 2), ([1], [4097], 1),                  # one token: 4 parts and 16
+    ([100], [1000], 4), ([130], [1024], 8),             # rows behind the sequence's; a last tile that nearly all is
+    ([1, 0, 3, 129], [0, 0, 5000, 700], 2),             # rows without keys, a sequence without rows
+    ([700], [600], 1),                                  # causal: rows that see nothing, tiles without keys
+    ([33, 300], [4000, 20], 3)])                        # parts that only one sequence has
+def test_few_queries_split_their_keys(D, Dv, causal, nq, nk, H):
+    assert k3._attention_bytes(len(nq), sum(nq), sum(nk), 2 * H, Dv) > 0
+    _case(nq, nk, 2 * H, H, D, Dv, causal)
+
+
+def test_split_results_agree_with_whole_ones_and_repeat():
+    q, k, v = _inputs([200], [3001], 8, 2, 128, 128, 8)
+    cq, ck = _cu([200]), _cu([3001])
+    ws = k3.attention_workspace(1, 200, 3001, 8, 128, device=DEV)
+    ws.fill_(255)                                       # what it holds has no influence
+
+    def run(w):
+        out, lse = torch.empty_like(q), torch.empty(200, 8, device=DEV)
+        k3.attention(q, k, v, cq, out, cu_k=ck, lse=lse, workspace=w)
+        return out, lse
+
+    a, b, c = run(ws), run(ws), run(None)
+    assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(a, b, c))
+    out, lse = torch.empty_like(q), torch.empty(200, 8, device=DEV)
+    p = lambda t: t.data_ptr()
+    assert k3.lib().k3moe_attention(p(q), q.stride(0), p(k), k.stride(0), p(v), v.stride(0), p(cq), p(ck), 1, 200, 3001, 8, 2,
+                                    128, 128, 128 ** -0.5, 1, p(out), out.stride(0), p(lse), None, 0,
+                                    torch.cuda.current_stream().cuda_stream) == 0
+    _check(q, k, v, [200], [3001], True, out, lse, 128 ** -0.5)
+    with pytest.raises(k3.K3MoeError):
+        run(ws[:1000])
+    with pytest.raises((ValueError, TypeError)):
+        run(ws.cpu())
+
+
+def test_split_not_finite():
+    """A row all of whose scores are -inf in one part, or in every one; NaN and infinities where they are not seen."""
+    q, k, v = _inputs([2], [2000], 2, 1, 128, 128, 9)
+    k, v = k.contiguous(), v.contiguous()
+    q[0] = 1.0
+    q[1] = torch.where(torch.arange(128, device=DEV) == 0, 1.0, 0.0).to(BF)
+    k[:600, 0, 0] = -float("inf")
+    k[1999], v[1999, 0, :5] = float("nan"), float("inf")    # the last key: only row 1 sees it
+    out, lse = torch.empty(2, 2, 128, dtype=BF, device=DEV), torch.empty(2, 2, device=DEV)
+    k3.attention(q, k, v, _cu([2]), out, cu_k=_cu([2000]), lse=lse)
+    assert out[0].isfinite().all() and lse[0].isfinite().all() and out[1].isnan().all() and lse[1].isnan().all()
+    k[:, 0, 0] = -float("inf")
+    k[1999], v[1999] = k[1998], v[1998]
+    k3.attention(q, k, v, _cu([2]), out, cu_k=_cu([2000]), lse=lse)
+    assert (out == 0).all() and (lse == -float("inf")).all()
 
 
 def test_offsets_are_held_to_the_tensors():
