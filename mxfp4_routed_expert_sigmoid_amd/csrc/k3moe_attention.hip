@@ -34,29 +34,45 @@ struct PromptTile {
     int q0, n, k0, N, tile, keys;     // n: 0: there is no such tile
 };
 
-__device__ __forceinline__ PromptTile prompt_tile(const PromptParams &p, int tile)
+// The tile's place in the order of the most keys first, among 64 sequences at a time: the level, a number of tiles of
+// keys, that the place falls in is found by halving, a lane counting the tiles of its sequence that reach it.
+__device__ __forceinline__ PromptTile prompt_tile(const PromptParams &p, int place)
 {
     const int lane = threadIdx.x & 63;
     const int32_t *cu_k = p.cu_k ? p.cu_k : p.cu_q;
     PromptTile r{};
-    for (int b0 = 0; b0 < p.seqs; b0 += 64) {         // 64 sequences at a time
+    for (int b0 = 0; b0 < p.seqs; b0 += 64) {
         int lo = 0, hi = 0, klo = 0, khi = 0;
         if (b0 + lane < p.seqs) {
             lo = min(max(p.cu_q[b0 + lane], 0), p.Tq), klo = min(max(cu_k[b0 + lane], 0), p.Tk);
             hi = min(max(p.cu_q[b0 + lane + 1], lo), p.Tq), khi = min(max(cu_k[b0 + lane + 1], klo), p.Tk);
         }
-        const int mine = (hi - lo + kPrRows - 1) / kPrRows, upto = wave_scan(mine);
-        const uint64_t past = __ballot(upto > tile);
-        if (past) {
-            const int at = __builtin_ctzll(past);
-            r.q0 = __builtin_amdgcn_readlane(lo, at), r.n = __builtin_amdgcn_readlane(hi, at) - r.q0;
-            r.k0 = __builtin_amdgcn_readlane(klo, at), r.N = __builtin_amdgcn_readlane(khi, at) - r.k0;
-            r.tile = __builtin_amdgcn_readlane(upto, at) - 1 - tile;   // the longest first
-            const int see = p.causal ? min(kPrRows * (r.tile + 1), r.n) + r.N - r.n : r.N;
-            r.keys = (max(see, 0) + kAtKeys - 1) / kAtKeys;
-            return r;
+        const int n = hi - lo, N = khi - klo, mine = (n + kPrRows - 1) / kPrRows;
+        const int all = __builtin_amdgcn_readlane(wave_scan(mine), 63);
+        if (place >= all) {
+            place -= all;
+            continue;
         }
-        tile -= __builtin_amdgcn_readlane(upto, 63);
+        // this sequence's tiles with `level` tiles of keys or more: its last ones
+        auto reach = [&](int level) {
+            const int x = kAtKeys * (level - 1) - (p.causal ? N - n : 0);   // a tile's last row has to see more
+            return level <= 0 ? mine : p.causal ? n <= x ? 0 : mine - max(x, 0) / kPrRows : N > x ? mine : 0;
+        };
+        int level = 0, above = (p.Tk + kAtKeys - 1) / kAtKeys + 1;   // reached by more tiles than `place`; not so
+        int c = mine, next = 0;                                      // this sequence's tiles that reach either
+        while (p.seqs > 1 && above - level > 1) {
+            const int half = (level + above) >> 1, some = reach(half);
+            if (__builtin_amdgcn_readlane(wave_scan(some), 63) > place) level = half, c = some;
+            else above = half, next = some;
+        }
+        const int before = __builtin_amdgcn_readlane(wave_scan(next), 63), upto = wave_scan(c - next);
+        const int at = __builtin_ctzll(__ballot(upto > place - before));
+        r.q0 = __builtin_amdgcn_readlane(lo, at), r.n = __builtin_amdgcn_readlane(n, at);
+        r.k0 = __builtin_amdgcn_readlane(klo, at), r.N = __builtin_amdgcn_readlane(N, at);
+        r.tile = __builtin_amdgcn_readlane(mine - next - 1 - (place - before - (upto - (c - next))), at);
+        const int see = p.causal ? min(kPrRows * (r.tile + 1), r.n) + r.N - r.n : r.N;
+        r.keys = (max(see, 0) + kAtKeys - 1) / kAtKeys;
+        return r;
     }
     return r;
 }
