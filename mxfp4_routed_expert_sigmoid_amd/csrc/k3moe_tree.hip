@@ -700,11 +700,15 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p)
     const int base = ((int)threadIdx.x & 63) / TR * TR;   // the row's first lane
     float mx = -INFINITY, l = 0.0f;
     float4 o = float4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int r0 = cut.first; r0 <= cut.last; r0 += TR) {
-        // a thread looks at one run's maximum and sum
+    constexpr int G = 16;                                 // runs whose sums are read at a time
+    for (int r0 = cut.first; r0 <= cut.last; r0 += G) {
         auto place = [&](int r) { return (int64_t)(2 * r + (r == cut.first)) * p.rows + row; };
-        const int r = r0 + part;
-        const float2 x = r <= cut.last ? *reinterpret_cast<const float2 *>(p.ml + 2 * place(r)) : float2{-INFINITY, 0.0f};
+        // a thread looks at one run's maximum and sum
+        const int r = r0 + part, n = min(G, cut.last - r0 + 1);
+        const float2 x = part < n ? *reinterpret_cast<const float2 *>(p.ml + 2 * place(r)) : float2{-INFINITY, 0.0f};
+        float4 v[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) v[k] = *reinterpret_cast<const float4 *>(p.part + place(r0 + min(k, n - 1)) * DV + 4 * part);
         float top = x.x;
 #pragma unroll
         for (int s = 1; s < TR; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
@@ -715,11 +719,11 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p)
         mx = top;
         l = l * old + (x.x == -INFINITY ? x.y : x.y * f);     // without a score above -inf: 0, or NaN
         o.x *= old, o.y *= old, o.z *= old, o.w *= old;
-        const int n = min(TR, cut.last - r0 + 1);
-        for (int k = 0; k < n; ++k) {
-            const float4 v = *reinterpret_cast<const float4 *>(p.part + place(r0 + k) * DV + 4 * part);
-            const float g = __shfl(f, base + k);
-            o.x = fmaf(v.x, g, o.x), o.y = fmaf(v.y, g, o.y), o.z = fmaf(v.z, g, o.z), o.w = fmaf(v.w, g, o.w);
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            const float g = __shfl(f, base + k);              // 0 where there is no such run: its sums count as zeros
+            const float4 w = k < n ? v[k] : float4{0.0f, 0.0f, 0.0f, 0.0f};
+            o.x = fmaf(w.x, g, o.x), o.y = fmaf(w.y, g, o.y), o.z = fmaf(w.z, g, o.z), o.w = fmaf(w.w, g, o.w);
         }
     }
 #pragma unroll
