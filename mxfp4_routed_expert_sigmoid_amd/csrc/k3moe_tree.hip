@@ -320,12 +320,6 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
         const int j1 = min(2 * t1, (s.keys + kTrTile - 1) / kTrTile);   // tiles of 32 keys
 
         const TreeRow row(p, s, kvh, rows0 + l32);
-        bf8 q[DK / 16];
-        {
-            const uint16_t *qp = p.q + row.token * p.qs + (int64_t)row.head * DK + 8 * h;
-#pragma unroll
-            for (int k = 0; k < DK / 16; ++k) q[k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
-        }
         v16f o[DV / 32];
         float mx = -INFINITY, l = 0.0f;
 #pragma unroll
@@ -398,7 +392,7 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
             whole = (j + 1) * kTrTile <= s.ctx && ok == ~0u;
         };
         v16f sc;
-        bf8 pw[2];
+        bf8 q[DK / 16], pw[2];
         auto scores = [&]() {
             const uint32_t at = fresh(krow), x = fresh(kx);
 #pragma unroll
@@ -449,6 +443,9 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
         if (j < j1) {
             look(j);
             load(j, 0);
+            const uint16_t *qp = p.q + row.token * p.qs + (int64_t)row.head * DK + 8 * h;
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) q[k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
         }
         while (j < j1) {
             ready();
@@ -559,14 +556,6 @@ __global__ __launch_bounds__(64 * kTrWaves, 1) void k_tree_wide(TreeParams p)
         const int n = min(s.kt - t0, left);                        // tiles of this segment here
         const TreeRow row(p, s, kvh, rows0 + kAtRows * wave + l32);
         const bool busy = rows0 + kAtRows * wave < s.n * p.group;
-        AttRows<DK, DV> r;
-        {
-            const uint16_t *qp = p.q + row.token * p.qs + (int64_t)row.head * DK + 8 * h;
-#pragma unroll
-            for (int k = 0; k < DK / 16; ++k) r.q[k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
-        }
-        r.clear();
-
         // Page numbers of 16 tiles, four (of 16 keys) each, a lane holds one; -1: no such key or page. i counts tiles from t0.
         const int32_t *table = p.pages + (int64_t)b * p.width;
         int ids = -1, ids_from = 0;
@@ -633,7 +622,39 @@ __global__ __launch_bounds__(64 * kTrWaves, 1) void k_tree_wide(TreeParams p)
         };
         look(0);
         at_barrier();                                              // the last segment's tiles are read
-        fetch(-3), fetch(-2), fetch(-1);                           // now ok: tile 0, ok1: tile 1, ok2: tile 2
+        AttRows<DK, DV> r;
+        auto queries = [&]() {
+            const uint16_t *qp = p.q + row.token * p.qs + (int64_t)row.head * DK + 8 * h;
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) r.q[k] = as_bf8(*reinterpret_cast<const u4 *>(qp + 16 * k));
+        };
+        if constexpr (X8) {                                        // as fetch does it, a wait less
+            auto keys = [&](int i) {
+                krows = rows_of(i, kat);
+                bk.load(p.kc + kat * DK, p.ks + kat * (DK / 32), krows);
+            };
+            auto values = [&]() { bv.load(p.vc + kat * DV, p.vs + kat * (DV / 32), krows); };
+            auto drop = [&]() {
+                if (__ballot(max(bk.top(), bv.top()) == 255u)) bk.drop(), bv.drop();
+            };
+            ok = cached(0), ok1 = n > 1 ? cached(1) : 0u, ok2 = n > 2 ? cached(2) : 0u;
+            keys(0), values();
+            queries();
+            drop();
+            bk.store(ktile(0), 16 * wave, k_slot<DK>);
+            bv.store(vtile(0), 16 * wave, v_slot<DV>);
+            if (n > 1) {
+                keys(1), values();
+                drop();
+                bk.store(ktile(1), 16 * wave, k_slot<DK>);
+                if (n > 2) keys(2);
+            }
+        } else {
+            fetch(-3);
+            queries();
+            fetch(-2), fetch(-1);                                  // now ok: tile 0, ok1: tile 1, ok2: tile 2
+        }
+        r.clear();
         at_barrier();
         if (!busy) {       // a wave without rows fetches its share of the tiles
             for (int i = 0; i < n; ++i) {
