@@ -498,7 +498,7 @@ typedef enum {
  *   cache  pages out (optional): token t's keys y and values v go to place
  *          slots[t] = page number * page + row of the page; a token whose place
  *          is outside the cache (negative: a padding row) is not written there.
- *          Two tokens with one place: either's.
+ *          A place that two tokens have holds pieces of either.
  *   slots  int64 [T], NULL iff no cache
  * dim and v_dim multiples of 8 up to 256 (of 32 with an MXFP8 cache), rot_dim a
  * multiple of 16 up to dim, heads up to 4096 each, T up to 2^25. Rows 16-byte
@@ -526,13 +526,15 @@ k3moe_status k3moe_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint1
  *   q bf16 [Tq][q_heads][k_dim], k bf16 [Tk][kv_heads][k_dim], v bf16 [Tk][kv_heads][v_dim]
  *   out bf16 [Tq][q_heads][v_dim], lse fp32 [Tq][q_heads] (optional, NULL = not written)
  * (k_dim, v_dim): (64, 64), (128, 128) or (192, 128), others
- * K3MOE_E_UNSUPPORTED_SHAPE; scale > 0 and finite. Rows 16-byte aligned, strides
- * up to 2^24 elements. Scores and sums are fp32; the weights are rounded to bf16
- * for their product with the values.
- *   workspace  optional: with one of k3moe_attention_workspace_size bytes (which
- *              may be 0: not used) few queries over many keys are split over
- *              more of the card; NULL = they are not. The results of the two
- *              agree to their rounding. */
+ * K3MOE_E_UNSUPPORTED_SHAPE; 0 < scale <= 2^64. Rows 16-byte aligned, strides
+ * up to 2^24 elements, seqs up to 2^30. out and lse overlap none of the inputs.
+ * Scores and sums are fp32, a weight below 2^-126 of the row's largest counts as
+ * 0; the weights are rounded to bf16 for their product with the values.
+ *   workspace  optional: with one of k3moe_attention_workspace_size bytes few
+ *              queries over many keys are split over more of the card; NULL =
+ *              they are not. The results of the two agree to their rounding. The
+ *              size is 0 for calls that are not split (the workspace is not
+ *              used) and else depends on v_dim alone (34 MB for 128). */
 k3moe_status k3moe_attention_workspace_size(int32_t seqs, int32_t Tq, int32_t Tk, int32_t q_heads,
                                             int32_t v_dim, size_t *bytes);
 k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
@@ -560,7 +562,7 @@ k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, const uint16_t
  *          max_q of a sequence, and rows of no sequence, are left as they were.
  *   tree   uint64 [Tq] (optional)
  *   q bf16 [Tq][q_heads][k_dim], out bf16 [Tq][q_heads][v_dim], lse fp32 [Tq][q_heads] (optional)
- * (k_dim, v_dim) and alignment as in k3moe_attention; page * pages_width up to
+ * (k_dim, v_dim), scale, weights, alignment and overlap as in k3moe_attention; page * pages_width up to
  * 2^30, and the tiles of 64 keys of all heads, blocks of 32 rows and sequences up
  * to 2^30 if every table were full (K3MOE_E_UNSUPPORTED_SHAPE above). The
  * workspace's size depends on neither lens nor the number of sequences. */

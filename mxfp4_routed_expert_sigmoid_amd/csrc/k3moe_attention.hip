@@ -58,7 +58,7 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptParams &p, int pla
             const int x = kAtKeys * (level - 1) - (p.causal ? N - n : 0);   // a tile's last row has to see more
             return level <= 0 ? mine : p.causal ? n <= x ? 0 : mine - max(x, 0) / kPrRows : N > x ? mine : 0;
         };
-        int level = 0, above = (p.Tk + kAtKeys - 1) / kAtKeys + 1;   // reached by more tiles than `place`; not so
+        int level = 0, above = p.Tk / kAtKeys + 2;   // reached by more tiles than `place`; not so
         int c = mine, next = 0;                                      // this sequence's tiles that reach either
         while (p.seqs > 1 && above - level > 1) {
             const int half = (level + above) >> 1, some = reach(half);
@@ -237,9 +237,8 @@ template <int DK, int DV>
 k3moe_status launch(const PromptParams &p, unsigned tiles, hipStream_t s)
 {
     constexpr int lds = 2 * kAtKeys * (DK + DV) * 2;
-    static const hipError_t allowed =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(k_attention<DK, DV>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (allowed != hipSuccess) return K3MOE_E_HIP;
+    static std::atomic<uint64_t> allowed{0};
+    if (!allow_lds(reinterpret_cast<const void *>(k_attention<DK, DV>), lds, allowed)) return K3MOE_E_HIP;
     k_attention<DK, DV><<<tiles * (unsigned)(p.Hq * p.split), 64 * kPrWaves, lds, s>>>(p);
     if (p.split > 1) k_attention_join<DV><<<dim3(tiles * (unsigned)p.Hq, kPrRows * DV / 1024), 256, 0, s>>>(p);
     return hipGetLastError() == hipSuccess ? K3MOE_OK : K3MOE_E_HIP;
@@ -268,10 +267,10 @@ int prompt_split(int64_t seqs, int64_t Tq, int64_t Tk, int64_t Hq)
     return s;
 }
 
+// The same for every split, so that one workspace serves calls of all sizes.
 size_t prompt_bytes(int64_t seqs, int64_t Tq, int64_t Tk, int64_t Hq, int64_t v_dim)
 {
-    const int split = prompt_split(seqs, Tq, Tk, Hq);
-    return split < 2 ? 0 : (size_t)(prompt_tiles(seqs, Tq) * Hq * split) * kPrRows * (size_t)(v_dim + 2) * 4;
+    return prompt_split(seqs, Tq, Tk, Hq) < 2 ? 0 : (size_t)kPrBlocks * kPrRows * (size_t)(v_dim + 2) * 4;
 }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -289,9 +288,10 @@ extern "C" k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, con
                                         void *stream)
 {
     if (seqs < 0 || Tq < 0 || Tk < 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads || causal < 0 || causal > 1 ||
-        !(scale > 0.0f && scale < INFINITY))
+        !(scale > 0.0f && scale <= 0x1p64f))
         return K3MOE_E_INVALID_ARG;
-    if (!((k_dim == v_dim && (k_dim == 64 || k_dim == 128)) || (k_dim == 192 && v_dim == 128))) return K3MOE_E_UNSUPPORTED_SHAPE;
+    if (!((k_dim == v_dim && (k_dim == 64 || k_dim == 128)) || (k_dim == 192 && v_dim == 128)))
+        return K3MOE_E_UNSUPPORTED_SHAPE;
     if (seqs == 0 || Tq == 0) return K3MOE_OK;
     if (!q || !cu_q || !out || (Tk > 0 && (!k || !v))) return K3MOE_E_INVALID_ARG;
     const int64_t qw = (int64_t)q_heads * k_dim, kw = (int64_t)kv_heads * k_dim, vw = (int64_t)kv_heads * v_dim,
@@ -306,7 +306,7 @@ extern "C" k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, con
         !at(cu_q, 4) || !at(cu_k, 4) || !at(lse, 4))
         return K3MOE_E_ALIGNMENT;
     const int64_t tiles = prompt_tiles(seqs, Tq);
-    if (tiles * q_heads >= (int64_t)1 << 24) return K3MOE_E_UNSUPPORTED_SHAPE;   // work-items are counted in 32 bits
+    if (tiles * q_heads >= (int64_t)1 << 24 || seqs > 1 << 30) return K3MOE_E_UNSUPPORTED_SHAPE;   // work-items are counted in 32 bits
     if (workspace && (!at(workspace, 256) || workspace_bytes < prompt_bytes(seqs, Tq, Tk, q_heads, v_dim))) return K3MOE_E_WORKSPACE;
     PromptParams p{};
     p.q = q, p.k = k, p.v = v, p.cu_q = cu_q, p.cu_k = cu_k, p.out = out, p.lse = lse;

@@ -12,12 +12,34 @@
 //
 // P is rounded to bf16 for the second product (2^-9 of each weight, whose
 // errors average out over the keys); the sums l are taken of the fp32 values.
+//
+// What bounds it: per tile of 64 keys and heads of 128 a wave has 32 products
+// (1024 cycles of the matrix unit) and 32 scores a lane, each with one
+// exponential, at a quarter of the other operations' rate, and four operations
+// more. att_tile interleaves the two by hand, a pair of scores to a step: 8192
+// causal tokens of 32 heads take 560 us (0.98 PFLOP/s) where the compiler's
+// order took 619, 4096 tokens that see every key 275 (1.0). On runs as long as
+// these the card's power sets the pace: its clock goes to 1.5 - 2.0 GHz.
 #pragma once
+
+#include <atomic>
 
 #include "k3moe_device.h"
 #include "k3moe_internal.h"
 
 namespace k3moe {
+
+// Lets a kernel have `bytes` of LDS on the current device; done: the kernel's own, a bit per device.
+inline bool allow_lds(const void *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short s4 __attribute__((ext_vector_type(4)));

@@ -517,7 +517,8 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
         if (++seg == p.Hkv * s.rt) {
             seg = 0;
             do s = tree_seq(p, ++b);
-            while (s.units == 0);
+            while (s.units == 0 && b < p.seqs);
+            if (b >= p.seqs) return;                       // the lengths have changed meanwhile
         }
     }
 #endif
@@ -702,7 +703,8 @@ __global__ __launch_bounds__(64 * kTrWaves, 1) void k_tree_wide(TreeParams p)
         if (++seg == p.Hkv * s.rt) {
             seg = 0;
             do s = tree_seq(p, ++b);
-            while (s.units == 0);
+            while (s.units == 0 && b < p.seqs);
+            if (b >= p.seqs) return;                       // the lengths have changed meanwhile
         }
     }
 #endif
@@ -773,12 +775,13 @@ k3moe_status launch(const TreeParams &p, hipStream_t s)
 {
     typedef TreeShape<DK, DV, X8> Few;
     typedef WideShape<DK, DV, X8> Wide;
-    static const hipError_t allowed[2] = {
-        hipFuncSetAttribute(reinterpret_cast<const void *>(k_tree_few<DK, DV, X8>), hipFuncAttributeMaxDynamicSharedMemorySize, Few::kLds),
-        hipFuncSetAttribute(reinterpret_cast<const void *>(k_tree_wide<DK, DV, X8>), hipFuncAttributeMaxDynamicSharedMemorySize, Wide::kLds)};
-    if (allowed[0] != hipSuccess || allowed[1] != hipSuccess) return K3MOE_E_HIP;
-    return p.maxq * p.group <= kTrFew ? launch<DV>(k_tree_few<DK, DV, X8>, Few::kLds, p, Few::kPerCu, kTrFew, s)
-                                      : launch<DV>(k_tree_wide<DK, DV, X8>, Wide::kLds, p, 1, kTrMaxRows, s);
+    static std::atomic<uint64_t> few{0}, wide{0};
+    if (p.maxq * p.group <= kTrFew) {
+        if (!allow_lds(reinterpret_cast<const void *>(k_tree_few<DK, DV, X8>), Few::kLds, few)) return K3MOE_E_HIP;
+        return launch<DV>(k_tree_few<DK, DV, X8>, Few::kLds, p, Few::kPerCu, kTrFew, s);
+    }
+    if (!allow_lds(reinterpret_cast<const void *>(k_tree_wide<DK, DV, X8>), Wide::kLds, wide)) return K3MOE_E_HIP;
+    return launch<DV>(k_tree_wide<DK, DV, X8>, Wide::kLds, p, 1, kTrMaxRows, s);
 }
 
 template <int DK, int DV>
@@ -814,7 +817,7 @@ extern "C" k3moe_status k3moe_tree_attention(const uint16_t *q, int64_t q_stride
                                              void *stream)
 {
     if (!cache || seqs < 0 || Tq < 0 || max_q < 1 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads || pages_width < 0 ||
-        cache->pages < 0 || cache->page <= 0 || !(scale > 0.0f && scale < INFINITY))
+        cache->pages < 0 || cache->page <= 0 || !(scale > 0.0f && scale <= 0x1p64f))
         return K3MOE_E_INVALID_ARG;
     const int page = cache->page;
     if (!((k_dim == v_dim && (k_dim == 64 || k_dim == 128)) || (k_dim == 192 && v_dim == 128)) || max_q > kTrMaxDraft ||

@@ -70,6 +70,7 @@ def _att(**kw):
     (dict(ost=2 ** 24 + 8), SHAPE), (dict(Tq=BIG, seqs=BIG), SHAPE), (dict(Tq=BIG, seqs=1), SHAPE),
     (dict(q=A + 8), ALIGN), (dict(k=A + 2), ALIGN), (dict(v=A + 8), ALIGN), (dict(out=A + 8), ALIGN), (dict(qst=516), ALIGN),
     (dict(kst=132), ALIGN), (dict(vst=132), ALIGN), (dict(ost=516), ALIGN), (dict(cq=A + 2), ALIGN), (dict(ck=A + 2), ALIGN),
+    (dict(scale=3e19), INVALID), (dict(seqs=2 ** 30 + 1), SHAPE),
     (dict(lse=A + 2), ALIGN), (dict(ws=A + 128, n=1 << 30), WORKSPACE), (dict(ws=A, Tk=9000, n=100), WORKSPACE),
     (dict(ws=A, Tk=9000, n="short"), WORKSPACE), (dict(seqs=0), OK), (dict(Tq=0, q=None, out=None, cq=None), OK),
 ])
@@ -80,9 +81,11 @@ def test_attention_refusals(kw, status):
 
 
 def test_attention_workspace_refusals():
-    n = ctypes.c_size_t()
+    n, m = ctypes.c_size_t(), ctypes.c_size_t()
     f = k3.lib().k3moe_attention_workspace_size
     assert f(1, 100, 9000, 8, 128, ctypes.byref(n)) == OK and n.value > 0
+    assert f(2, 9, 800, 64, 128, ctypes.byref(m)) == OK and m.value in (0, n.value)   # one size serves every call
+    assert f(1, 1, 40000, 1, 128, ctypes.byref(m)) == OK and m.value == n.value
     assert f(1, 100, 100, 8, 128, ctypes.byref(n)) == OK and n.value == 0        # nothing to split
     assert f(BIG, BIG, BIG, BIG, 128, ctypes.byref(n)) == OK and n.value == 0
     assert f(0, 0, 0, 1, 64, ctypes.byref(n)) == OK and n.value == 0
@@ -104,6 +107,7 @@ def _tree(**kw):
     (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID), (dict(Hq=7), INVALID), (dict(width=-1), INVALID),
     (dict(cache=_pages(pages=-1)), INVALID), (dict(cache=_pages(page=0)), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(cq=None, Tq=5), INVALID),
+    (dict(scale=3e19), INVALID),
     (dict(cq=None, maxq=1), INVALID), (dict(q=None), INVALID), (dict(lens=None), INVALID), (dict(out=None), INVALID),
     (dict(pages=None), INVALID), (dict(cache=_pages(ks=A)), INVALID), (dict(cache=_pages(vs=A)), INVALID),
     (dict(cache=_pages(k=None)), INVALID), (dict(cache=_pages(v=None)), INVALID), (dict(qst=504), INVALID),
