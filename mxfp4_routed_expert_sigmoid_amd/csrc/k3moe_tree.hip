@@ -11,11 +11,24 @@
 // workspace as unnormalised sums with their maximum, and a second kernel joins
 // them in their order.
 //
-// Up to 32 rows (k_tree_few) are bound by the cache's bytes: every wave holds all
-// rows of its block and reads tiles of 32 keys of its own, every fourth of the
-// run, through its own part of the LDS, so nothing waits for another wave until a
-// segment ends and the four waves' sums are added. More rows (k_tree_wide) are
-// split over the waves, which share tiles of 64 keys as the prompts' kernel does.
+// Up to 32 rows (k_tree_few; 64, in two blocks, over 8 bits) are bound by the
+// cache's bytes: every wave holds all rows of its block and reads tiles of 32
+// keys of its own, every fourth of the run, through its own part of the LDS, so
+// nothing waits for another wave until a segment ends and the four waves' sums
+// are added. 32 sequences of up to 32768 tokens, 8 heads of 128: 395 us in bf16
+// (2.3 GB, 5.9 TB/s), 222 over 8 bits (5.4 TB/s; there the expansion, two
+// operations per value with its LDS write, is as long as the loads). One
+// sequence of 4000: 8.7 us and the join's 4.5, the ends of two short kernels.
+//
+// More rows (k_tree_wide) are split over the waves, which share tiles of 64 keys
+// as the prompts' kernel does. 64 keys of 128 rows take 1.5 us, the time of one
+// wave's products and exponentials, which no second wave on its SIMD fills: three
+// tiles take the LDS, the accumulators the registers. Plan, first tiles and the
+// stores of cut ends are another 10 us. 6 sequences of 16 drafted tokens over up
+// to 5000 keys: 34 us and the join's 4.5.
+//
+// Two launches, no counters: a workspace need not hold anything in front of a
+// call, and no block waits for another.
 #include "k3moe_attn.h"
 
 namespace k3moe {
@@ -776,7 +789,10 @@ k3moe_status launch(const TreeParams &p, hipStream_t s)
     typedef TreeShape<DK, DV, X8> Few;
     typedef WideShape<DK, DV, X8> Wide;
     static std::atomic<uint64_t> few{0}, wide{0};
-    if (p.maxq * p.group <= kTrFew) {
+    // Up to 32 rows a wave that holds them all wins (8 sequences x 4000 keys x 8 heads, 32 rows: 30 us and 35, over 8 bits
+    // 27 and 36); behind that two blocks of 32 rows read a bf16 cache twice (40 rows: 47 and 37), but expand an 8-bit one
+    // faster than one block of 128, alone on its CU, does (64 rows: 35 and 39; 32 x 8000: 171 and 220; 96 rows: 49 and 42).
+    if (p.maxq * p.group <= (X8 ? 2 * kTrFew : kTrFew)) {
         if (!allow_lds(reinterpret_cast<const void *>(k_tree_few<DK, DV, X8>), Few::kLds, few)) return K3MOE_E_HIP;
         return launch<DV>(k_tree_few<DK, DV, X8>, Few::kLds, p, Few::kPerCu, kTrFew, s);
     }

@@ -152,6 +152,16 @@ def test_empty_words_and_bits_behind_the_last_token():
     assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
 
 
+@pytest.mark.parametrize("D,Dv", DIMS)
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("group,n", [(2, 16), (2, 17), (2, 32), (2, 33), (2, 64), (5, 12), (5, 13), (5, 27)])
+def test_rows_of_a_block(D, Dv, x8, group, n):
+    """Rows around 32, 64 and 128: one block or two of 32, one of 128 or two; a second, shorter sequence leaves some idle."""
+    ns = [n, 1, max(n - 9, 2)]
+    c = Case([333, 5, 130], ns, 2 * group, 2, D, Dv, page=32, x8=x8, words=_tree(ns))
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("x8", [False, True])
 @pytest.mark.parametrize("n", [1, 20])
 def test_bad_pages_are_seen_by_nobody(x8, n):
