@@ -35,6 +35,7 @@ struct PromptParams {
     const int32_t *cu_q, *cu_k;
     uint16_t *out;
     float *lse, *part, *ml;   // part [tiles][heads][split][128][DV], ml the same of pairs
+    int4 *joins;              // [tiles]: first query, queries, tile, tiles of keys, for the join
     int64_t qs, ks, vs, os;   // row strides, elements
     int seqs, Tq, Tk, Hq, group, causal, split;
     float scale;
@@ -106,6 +107,7 @@ __global__ __launch_bounds__(64 * kPrWaves, 2) void k_attention(PromptParams p)
     const PromptTile x = prompt_tile(p, unit / p.split);
     const int n = x.n, N = x.N, per = prompt_part(p, x.keys);
     const int t0 = split * per, t1 = min(t0 + per, x.keys), tiles = t1 - t0;   // this part's tiles
+    if (p.split > 1 && head == 0 && split == 0 && threadIdx.x == 0) p.joins[unit / p.split] = int4{x.q0, n, x.tile, x.keys};
     if (n == 0 || (split > 0 && tiles <= 0)) return;
 
     const int row = kPrRows * x.tile + kAtRows * wave + l32;   // this lane's query of the sequence
@@ -199,7 +201,8 @@ __global__ __launch_bounds__(256) void k_attention_join(PromptParams p)
 {
     constexpr int TR = DV / 4, RB = 256 / TR;
     const int head = blockIdx.x % p.Hq, tile = blockIdx.x / p.Hq;
-    const PromptTile x = prompt_tile(p, tile);
+    const int4 d = p.joins[tile];
+    const struct { int q0, n, tile, keys; } x = {d.x, d.y, d.z, d.w};
     const int per = prompt_part(p, x.keys), in = (int)blockIdx.y * RB + (int)threadIdx.x / TR, e = 4 * ((int)threadIdx.x % TR);
     const int row = kPrRows * x.tile + in;
     if (per >= x.keys || row >= x.n) return;              // one part, or no such tile or row
@@ -282,7 +285,7 @@ int prompt_split(int64_t seqs, int64_t Tq, int64_t Tk, int64_t Hq)
 // The same for every split, so that one workspace serves calls of all sizes.
 size_t prompt_bytes(int64_t seqs, int64_t Tq, int64_t Tk, int64_t Hq, int64_t v_dim)
 {
-    return prompt_split(seqs, Tq, Tk, Hq) < 2 ? 0 : (size_t)kPrBlocks * kPrRows * (size_t)(v_dim + 2) * 4;
+    return prompt_split(seqs, Tq, Tk, Hq) < 2 ? 0 : (size_t)kPrBlocks * (kPrRows * (size_t)(v_dim + 2) * 4 + sizeof(int4));
 }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -325,8 +328,11 @@ extern "C" k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, con
     p.qs = q_stride, p.ks = k_stride, p.vs = v_stride, p.os = out_stride;
     p.seqs = seqs, p.Tq = Tq, p.Tk = Tk, p.Hq = q_heads, p.group = q_heads / kv_heads, p.causal = causal, p.scale = scale;
     p.split = workspace ? prompt_split(seqs, Tq, Tk, q_heads) : 1;
-    p.part = static_cast<float *>(workspace);
-    p.ml = p.part + (size_t)(tiles * q_heads * p.split) * kPrRows * (size_t)v_dim;
+    if (p.split > 1) {
+        p.joins = static_cast<int4 *>(workspace);
+        p.part = reinterpret_cast<float *>(p.joins + kPrBlocks);
+        p.ml = p.part + (size_t)(tiles * q_heads * p.split) * kPrRows * (size_t)v_dim;
+    }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const unsigned t = (unsigned)tiles;
     return k_dim == 64 ? launch<64, 64>(p, t, s) : k_dim == 128 ? launch<128, 128>(p, t, s) : launch<192, 128>(p, t, s);

@@ -15,7 +15,7 @@
 // logits) it takes the elements one by one instead.
 //
 // Bound by the logits' bytes: 509 x 163840 in fp32 without a list 56 us (6.0
-// TB/s), with the 20 largest 63 to 70: the list's steps, ballots and a barrier, stand
+// TB/s), with the 8 largest 63 to 70, the 20 largest 80: the list's steps, ballots and a barrier, stand
 // between a block's loads and its end, and the join takes 5. A thread holds 16
 // or 32 elements (64 were slower: fewer blocks on a CU, loads behind each other),
 // read by loads of 16 bytes where a row allows it; each element costs one
