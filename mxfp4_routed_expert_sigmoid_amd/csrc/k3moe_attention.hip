@@ -18,7 +18,7 @@
 // 1.0 PFLOP/s), heads of 64, 4096 tokens, 93 (0.74: the same exponentials for half
 // the products), of 192 / 128, 16 heads, 115 (0.75: its registers spill a little
 // outside the loop of whole tiles). Short prompts packed together (7 of 1 to 2047
-// tokens, 32 heads) 77 to 87 us, 0.65 PFLOP/s: 1184 blocks of 1 to 32 tiles, of
+// tokens, 32 heads) 76 to 88 us, 0.65 PFLOP/s: 1184 blocks of 1 to 32 tiles, of
 // whose time first loads, masked tiles and last stores take a larger part.
 #include "k3moe_attn.h"
 
