@@ -238,6 +238,46 @@ def test_same_bits_streams_and_graphs():
         assert torch.equal(a, b)
 
 
+def test_split_calls_share_a_workspace_in_two_graphs():
+    cases = []
+    for D, Dv, nq, nk, H in ((128, 128, [200], [3001], 4), (192, 128, [5, 90], [2000, 800], 2), (128, 128, [1], [9000], 8)):
+        q, k, v = _inputs(nq, nk, 2 * H, H, D, Dv, seed=len(cases))
+        cases.append((q, k, v, _cu(nq), _cu(nk), torch.zeros((sum(nq), 2 * H, Dv), dtype=BF, device=DEV)))
+    ws = k3.attention_workspace(1, 1, 9000, 16, 128, device=DEV)      # one size for all
+    ws.fill_(255)
+
+    def run(c, out, w=None, stream=None):
+        k3.attention(c[0], c[1], c[2], c[3], out, cu_k=c[4], workspace=w, stream=stream)
+
+    graphs = []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(c, c[5], ws)
+        graphs.append(g)
+    for step in range(3):
+        for c in cases:
+            c[0].normal_()
+            c[5].zero_()
+        cases[0][3][1] -= step                                        # other lengths in the same graph
+        for g in graphs:
+            g.replay()
+        want = [torch.empty_like(c[5]).copy_(c[5]) for c in cases]
+        eager = [torch.zeros_like(c[5]) for c in cases]
+        for c, o in zip(cases, eager):
+            run(c, o, ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, eager))
+    s = torch.cuda.Stream()
+    other = [torch.zeros_like(c[5]) for c in cases]
+    s.wait_stream(torch.cuda.current_stream())
+    for c, o in zip(cases, other):                                    # two streams at once, a workspace each
+        run(c, o, None, s)
+        run(c, c[5].zero_(), None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) and torch.equal(a, c[5]) for a, b, c in zip(other, eager, cases))
+
+
 def test_rows_beyond_32_bits():
     """Keys more than 2^32 bytes behind the first ones."""
     T, W = 40000, 65536
