@@ -259,8 +259,8 @@ __global__ __launch_bounds__(kLpThreads, 6) void k_lp_chunk(LpParams p)
         const double f = 1.0 - 0.69314718055994531 * (double)ml;   // 2^-ml: ml is below 2^-24 of |m L|, its square below any digit
         const double R = lp_wave<double>(rest, 0.0, LpAdd()), D = lp_wave<double>(dev, 0.0, LpAdd());
         const int N = lp_wave<int>(top, 0, LpAdd());
-        // sum of (m - x) e = (sum of -t e - ml sum of e) / L
-        if (lane == 0) wsum[wave] = LpStats{R * f, (D - (double)ml * R) * f * (1.0 / (double)L2E), m, N};
+        // t = x L - mh = (x - m) L + ml: sum of (m - x) e = (sum of -t e + ml sum of e) / L
+        if (lane == 0) wsum[wave] = LpStats{R * f, (D + (double)ml * R) * f * (1.0 / (double)L2E), m, N};
     }
     if (p.k > 0) {
         uint32_t bound = wbound[0];
