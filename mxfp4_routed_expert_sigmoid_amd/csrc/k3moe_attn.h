@@ -279,15 +279,15 @@ __device__ __forceinline__ float att_max(const v16f (&s)[2])
     return swap_max(mx);
 }
 
-// Raises the running maximum where a score exceeds it by the slack.
+// Raises the running maximum of the rows where a score exceeds it by the slack; the others keep theirs, so that a row's
+// bits do not depend on what other rows see.
 template <int DK, int DV>
 __device__ __forceinline__ void att_raise(AttRows<DK, DV> &r, float mx, float c)
 {
-    // (mx - m) is NaN where both are -inf: nothing to raise
-    if (__ballot((mx - r.m) * c > kAtSlack)) {
-        const float mn = fmaxf(r.m, mx);
-        const float a = r.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.m - mn) * c);
-        r.m = mn, r.l *= a;
+    const bool up = (mx - r.m) * c > kAtSlack;   // NaN where both are -inf: nothing to raise
+    if (__ballot(up)) {
+        const float a = up ? __builtin_amdgcn_exp2f((r.m - mx) * c) : 1.0f;   // 0 from -inf on
+        r.m = up ? mx : r.m, r.l *= a;
 #pragma unroll
         for (int d = 0; d < DV / 32; ++d)
 #pragma unroll

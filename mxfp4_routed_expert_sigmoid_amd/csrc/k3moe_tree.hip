@@ -419,10 +419,10 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
 #pragma unroll
             for (int i = 1; i < 16; ++i) m = fmaxf(m, sc[i]);
             m = swap_max(m);
-            if (__ballot((m - mx) * c > kAtSlack)) {
-                const float mn = fmaxf(mx, m);
-                const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx - mn) * c);
-                mx = mn, l *= f;
+            const bool up = (m - mx) * c > kAtSlack;       // as att_raise: the other rows keep theirs
+            if (__ballot(up)) {
+                const float f = up ? __builtin_amdgcn_exp2f((mx - m) * c) : 1.0f;
+                mx = up ? m : mx, l *= f;
 #pragma unroll
                 for (int d = 0; d < DV / 32; ++d)
 #pragma unroll
