@@ -6,6 +6,7 @@ The C ABI is declared in ``include/k3moe.h``; the names here mirror it.
 If the library has not been built this module raises ImportError: there is
 no fallback path.
 """
+import contextlib
 import ctypes
 import os
 import struct
@@ -284,16 +285,16 @@ class Layer:
         return ctypes.c_void_p(base + off), ws.numel() - off
 
     def _call_ws(self, workspace, T, stream):
-        """The caller's workspace, or a new one for T tokens. A new one is
-        allocated on the current stream; when the call runs on another
-        stream it is marked as used there, so the caching allocator does not
-        hand its memory out again while the queued kernels still use it."""
+        """The caller's workspace, or a new one for T tokens. A new one belongs
+        to the stream that the call runs on: freed when the call returns, its
+        memory is given out again in that stream's order only, behind the
+        queued kernels that still use it."""
         if workspace is not None:
             return workspace
-        ws = self.workspace(T)
-        if stream is not None and stream != torch.cuda.current_stream(self.device):
-            ws.record_stream(stream)
-        return ws
+        if stream is None:
+            return self.workspace(T)
+        with torch.cuda.stream(stream):
+            return self.workspace(T)
 
     def _check_tokens(self, T, **t):
         H, K, E = self.cfg.hidden, self.cfg.topk, self.cfg.n_experts
@@ -435,11 +436,7 @@ class Cache:
         T = _rows(x, self.layer.cfg.hidden)
         self.layer._check_tokens(T, idx=idx, w=w, out=out)
         _dev(x, (2,), "x"), _dev(idx, (4,), "idx"), _dev(w, (4,), "w"), _dev(out, (4,), "out")
-        ws = workspace
-        if ws is None:
-            ws = self.workspace(T)
-            if stream is not None and stream != torch.cuda.current_stream(self.device):
-                ws.record_stream(stream)
+        ws = Layer._call_ws(self, workspace, T, stream)
         p, n = Layer._ws(ws)
         _check(lib().k3moe_cache_forward(self.handle, x.data_ptr(), T, idx.data_ptr(), w.data_ptr(),
                                          out.data_ptr(), p, n, _stream(stream, self.device)),
@@ -731,13 +728,15 @@ def _scratch_ok(workspace, dev):
         raise ValueError(f"workspace: {workspace.dtype} on {workspace.device}, expected contiguous torch.uint8 on cuda:{dev}")
 
 
+_NO_STREAM = contextlib.nullcontext()
+
+
 def _scratch(workspace, size, device, stream):
-    """The caller's workspace or a new one (marked as used on `stream`), with its address and bytes from the first
-    256-byte boundary on. The caller holds it until its call is queued: freed before, it could be given out again."""
+    """The caller's workspace or a new one, with its address and bytes from the first 256-byte boundary on. A new one
+    belongs to the stream that uses it (see Layer._call_ws), and the caller holds it until its call is queued."""
     if workspace is None:
-        workspace = torch.empty(size() + 256, dtype=torch.uint8, device=device)
-        if stream is not None and stream != torch.cuda.current_stream(device):
-            workspace.record_stream(stream)
+        with _NO_STREAM if stream is None else torch.cuda.stream(stream):
+            workspace = torch.empty(size() + 256, dtype=torch.uint8, device=device)
     base = workspace.data_ptr()
     off = -base % 256
     return workspace, base + off, max(workspace.numel() - off, 0)

@@ -308,3 +308,20 @@ def test_a_cache_beyond_32_bits():
     c.pages += (pages - c.k.shape[0]) * (c.pages >= 0)
     out, lse = c.run()
     c.check(out, lse)
+
+
+def test_two_streams_without_a_workspace():
+    """Calls on the current stream and on another in turn, each with a workspace of its own making: the first one's is
+    freed while its kernels run, and must not be the second one's."""
+    a = Case([9000] * 12, [1] * 12, 16, 8, 64, 64, page=64, seed=1)
+    b = Case([4000], [1], 16, 8, 64, 64, page=64, seed=2)
+    wa, wb = a.run(uniform=True, lse=False)[0], b.run(uniform=True, lse=False)[0]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = [(torch.zeros_like(wa), torch.zeros_like(wb)) for _ in range(6)]
+    torch.cuda.synchronize()
+    for oa, ob in outs:
+        a.run(uniform=True, lse=False, out=oa)
+        b.run(uniform=True, lse=False, out=ob, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(oa, wa) and torch.equal(ob, wb) for oa, ob in outs)
