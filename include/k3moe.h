@@ -590,7 +590,9 @@ k3moe_status k3moe_tree_attention(const uint16_t *q, int64_t q_stride, const k3m
  * A row that is no distribution (a NaN, +inf, or every logit -inf) gives NaN in
  * lp, entropy and top_lp; its top_ids go by the logits all the same (NaN lowest,
  * with -inf). V up to 2^24, n_ids up to 4096. A term e^(x - max) is an
- * fp32 number (below 2^-126: 0), sums are joined in 64 bits. T == 0 does nothing. */
+ * fp32 number (below 2^-126: 0), sums are joined in 64 bits. T == 0 does nothing.
+ * A workspace of k3moe_logprobs_workspace_size bytes serves every call of up to T
+ * rows of V logits and up to k alternatives. */
 k3moe_status k3moe_logprobs_workspace_size(int32_t T, int32_t V, int32_t k, size_t *bytes);
 k3moe_status k3moe_logprobs(const void *logits, int32_t logits_f32, int64_t stride, int32_t T, int32_t V,
                             const int32_t *ids, int32_t n_ids, float *lp, float *entropy, int32_t *top_ids,

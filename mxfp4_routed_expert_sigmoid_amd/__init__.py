@@ -935,7 +935,7 @@ def _logprobs_bytes(T, V, k):
 
 
 def logprobs_workspace(T, V, k=0, device=None):
-    """A device byte tensor for ``logprobs`` on T rows of V logits with k alternatives."""
+    """A device byte tensor for ``logprobs`` on up to T rows of V logits with up to k alternatives."""
     return torch.empty(_logprobs_bytes(T, V, k) + 256, dtype=torch.uint8, device=device or "cuda")
 
 

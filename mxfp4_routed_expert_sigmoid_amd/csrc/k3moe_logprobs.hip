@@ -380,10 +380,9 @@ __global__ __launch_bounds__(64 * W) void k_lp_join(LpParams p)
 // Chunks of a row: long ones where they still give every CU some blocks (a chunk's ends, the top list first of all,
 // cost the same for both). Short and long, rows x 163840, k = 20: 1: 11.9 and 13.5 us, 16: 13.7 and 14.7, 32 (640 long
 // chunks): 15.8 and 15.6, 64: 23.2 and 21.8, 509: 96 and 80; 128 x 32000 (512): 12.4 and 13.4.
-int lp_per_thread(int64_t T, int64_t V)
-{
-    return T * ((V + kLpLong * kLpThreads - 1) / (kLpLong * kLpThreads)) >= 640 ? kLpLong : kLpShort;
-}
+constexpr int64_t kLpLongFrom = 640;
+int64_t lp_long_chunks(int64_t V) { return (V + kLpLong * kLpThreads - 1) / (kLpLong * kLpThreads); }
+int lp_per_thread(int64_t T, int64_t V) { return T * lp_long_chunks(V) >= kLpLongFrom ? kLpLong : kLpShort; }
 int lp_chunks(int64_t T, int64_t V)
 {
     const int64_t per = (int64_t)lp_per_thread(T, V) * kLpThreads;
@@ -391,6 +390,12 @@ int lp_chunks(int64_t T, int64_t V)
 }
 size_t lp_stat_bytes(int64_t T, int64_t V) { return ((size_t)(T * lp_chunks(T, V)) * sizeof(LpStats) + 255) / 256 * 256; }
 size_t lp_bytes(int64_t T, int64_t V, int k) { return lp_stat_bytes(T, V) + (size_t)(T * lp_chunks(T, V)) * (size_t)k * 8; }
+// The most that T rows or fewer take: the largest number of rows in short chunks may take more than T in long ones.
+size_t lp_most_bytes(int64_t T, int64_t V, int k)
+{
+    const int64_t shorts = min(T, (kLpLongFrom - 1) / lp_long_chunks(V));
+    return max(lp_bytes(T, V, k), lp_bytes(shorts, V, k));
+}
 
 template <bool F32>
 void launch_lp(const LpParams &p, bool vec, hipStream_t s)
@@ -429,7 +434,7 @@ extern "C" k3moe_status k3moe_logprobs_workspace_size(int32_t T, int32_t V, int3
 {
     if (!bytes) return K3MOE_E_INVALID_ARG;
     const k3moe_status st = lp_sizes(T, V, k);
-    if (st == K3MOE_OK) *bytes = lp_bytes(T, V, k);
+    if (st == K3MOE_OK) *bytes = lp_most_bytes(T, V, k);
     return st;
 }
 

@@ -184,3 +184,16 @@ def test_rows_beyond_32_bits():
     a, _, order, top, tol, _ = ref.logprobs(x[T - 1].cpu().numpy(), [5], 1)
     assert abs(float(lp[T - 1, 0]) - a[0]) <= tol + ref.U32 * abs(a[0]) and int(ti[T - 1, 0]) == order[0]
     assert int(ti[T - 2, 0]) == 0 and abs(float(lp[0, 0]) + np.log(V)) < 1e-5
+
+
+def test_a_workspace_serves_fewer_rows():
+    """160 rows of 32000 take half the chunks that 159 take."""
+    V = 32000
+    ws = k3.logprobs_workspace(160, V, 5, device=DEV)
+    for T in (160, 159, 81, 80, 1):
+        x, ids = _x(T, V, seed=T), _ids(T, V, 1)
+        ws.fill_(0xff)
+        for w, g in zip(_run(x, ids, 5), _run(x, ids, 5, ws=ws)):
+            assert np.array_equal(w, g)
+        for w, g in zip(_run(x, ids, 2), _run(x, ids, 2, ws=ws)):
+            assert np.array_equal(w, g)
