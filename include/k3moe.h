@@ -533,8 +533,10 @@ k3moe_status k3moe_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint1
  *   workspace  optional: with one of k3moe_attention_workspace_size bytes few
  *              queries over many keys are split over more of the card; NULL =
  *              they are not. The results of the two agree to their rounding. The
- *              size is 0 for calls that are not split (the workspace is not
- *              used) and else depends on v_dim alone (34 MB for 128). */
+ *              size serves every call of up to these sequences, queries and keys
+ *              with these heads. It is 0 where none of them is split (the
+ *              workspace is not used) and else depends on v_dim alone (34 MB for
+ *              128). */
 k3moe_status k3moe_attention_workspace_size(int32_t seqs, int32_t Tq, int32_t Tk, int32_t q_heads,
                                             int32_t v_dim, size_t *bytes);
 k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,

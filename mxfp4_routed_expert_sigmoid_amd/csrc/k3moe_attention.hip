@@ -283,10 +283,7 @@ int prompt_split(int64_t seqs, int64_t Tq, int64_t Tk, int64_t Hq)
 }
 
 // The same for every split, so that one workspace serves calls of all sizes.
-size_t prompt_bytes(int64_t seqs, int64_t Tq, int64_t Tk, int64_t Hq, int64_t v_dim)
-{
-    return prompt_split(seqs, Tq, Tk, Hq) < 2 ? 0 : (size_t)kPrBlocks * (kPrRows * (size_t)(v_dim + 2) * 4 + sizeof(int4));
-}
+size_t prompt_bytes(int64_t v_dim) { return (size_t)kPrBlocks * (kPrRows * (size_t)(v_dim + 2) * 4 + sizeof(int4)); }
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -322,12 +319,13 @@ extern "C" k3moe_status k3moe_attention(const uint16_t *q, int64_t q_stride, con
         return K3MOE_E_ALIGNMENT;
     const int64_t tiles = prompt_tiles(seqs, Tq);
     if (tiles * q_heads >= (int64_t)1 << 24 || seqs > 1 << 30) return K3MOE_E_UNSUPPORTED_SHAPE;   // work-items are counted in 32 bits
-    if (workspace && (!at(workspace, 256) || workspace_bytes < prompt_bytes(seqs, Tq, Tk, q_heads, v_dim))) return K3MOE_E_WORKSPACE;
+    const int split = workspace ? prompt_split(seqs, Tq, Tk, q_heads) : 1;
+    if (workspace && (!at(workspace, 256) || (split > 1 && workspace_bytes < prompt_bytes(v_dim)))) return K3MOE_E_WORKSPACE;
     PromptParams p{};
     p.q = q, p.k = k, p.v = v, p.cu_q = cu_q, p.cu_k = cu_k, p.out = out, p.lse = lse;
     p.qs = q_stride, p.ks = k_stride, p.vs = v_stride, p.os = out_stride;
     p.seqs = seqs, p.Tq = Tq, p.Tk = Tk, p.Hq = q_heads, p.group = q_heads / kv_heads, p.causal = causal, p.scale = scale;
-    p.split = workspace ? prompt_split(seqs, Tq, Tk, q_heads) : 1;
+    p.split = split;
     if (p.split > 1) {
         p.joins = static_cast<int4 *>(workspace);
         p.part = reinterpret_cast<float *>(p.joins + kPrBlocks);
@@ -343,6 +341,7 @@ extern "C" k3moe_status k3moe_attention_workspace_size(int32_t seqs, int32_t Tq,
 {
     if (!bytes || seqs < 0 || Tq < 0 || Tk < 0 || q_heads <= 0) return K3MOE_E_INVALID_ARG;
     if (v_dim != 64 && v_dim != 128) return K3MOE_E_UNSUPPORTED_SHAPE;
-    *bytes = prompt_bytes(seqs, Tq, Tk, q_heads, v_dim);
+    // one query over all keys is split if any call of up to these sizes is: fewer blocks and longer sequences split first
+    *bytes = prompt_split(seqs < 1 ? seqs : 1, Tq < 1 ? Tq : 1, Tk, q_heads) < 2 ? 0 : prompt_bytes(v_dim);
     return K3MOE_OK;
 }

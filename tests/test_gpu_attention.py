@@ -296,3 +296,15 @@ def test_rows_beyond_32_bits():
     see = np.arange(T)[None, :] <= np.array(rows)[:, None] + T - n
     want = ref.attend(qn, kn, vn, see, 128 ** -0.5)
     ref.check_rows(_np(out[T - n:])[rows, 0], _np(lse[T - n:])[rows, 0], *want, "far rows")
+
+
+def test_a_workspace_serves_smaller_calls():
+    """Made for a call that is not split, used by smaller ones that are."""
+    ws = k3.attention_workspace(1, 3000, 3000, 32, 128, device=DEV)
+    for nq, nk in ((3000, 3000), (64, 2999), (1, 600), (64, 100)):
+        q, k, v = _inputs([nq], [nk], 32, 4, 128, 128, seed=nq)
+        ws.fill_(0xff)
+        a, b = torch.zeros_like(q), torch.zeros_like(q)
+        k3.attention(q, k, v, _cu([nq]), a, cu_k=_cu([nk]), workspace=ws)
+        k3.attention(q, k, v, _cu([nq]), b, cu_k=_cu([nk]))
+        assert torch.equal(a, b) and a.float().abs().sum() > 0

@@ -20,3 +20,18 @@ def test_logprobs_sizes_do_not_fall(V, k):
             assert n.value >= last[i], T
             last[i] = n.value
         assert last[0] >= last[1] >= last[2]
+
+
+@pytest.mark.parametrize("heads", [1, 8, 32, 96, 255, 256, 257])
+@pytest.mark.parametrize("v_dim", [64, 128])
+def test_an_attention_size_serves_every_smaller_call(heads, v_dim):
+    """A call that is not split by itself may be larger than one that is."""
+    sizes = [(1, 8192, 8192), (7, 4264, 4264), (64, 64, 70000), (3, 1024, 4096), (1, 1, 300)]
+    for seqs, Tq, Tk in sizes:
+        most = k3._attention_bytes(seqs, Tq, Tk, heads, v_dim)
+        for s in {1, 2, seqs}:
+            for q in {1, 64, 129, Tq}:
+                for k in {1, 255, 512, 4096, Tk}:
+                    if s <= seqs and q <= Tq and k <= Tk:
+                        assert k3._attention_bytes(s, q, k, heads, v_dim) <= most, (seqs, Tq, Tk, s, q, k)
+    assert k3._attention_bytes(1, 8192, 8192, 32, v_dim) >= k3._attention_bytes(1, 64, 4096, 32, v_dim) > 0
