@@ -856,8 +856,8 @@ def attention(q, k, v, cu_q, out, cu_k=None, scale=None, causal=True, lse=None, 
             return attention(q, k, v, cu_q, out, cu_k, scale, causal, lse, workspace, stream)
     wp, wn = None, 0
     seqs = cu_q.shape[0] - 1
-    # (a split takes 512 keys or more and makes two of at most 256 blocks of 128 queries; its size is asked for only then)
-    if workspace is not None or Tk >= 512 and Hq * -(-Tq // 128) <= 256 and (Dv == 64 or Dv == 128):
+    # (a split takes 384 keys or more and makes two of at most 256 blocks of 128 queries; its size is asked for only then)
+    if workspace is not None or Tk >= 384 and Hq * -(-Tq // 128) <= 256 and (Dv == 64 or Dv == 128):
         size = 1 if workspace is not None else _attention_bytes(seqs, Tq, Tk, Hq, Dv)
         if size:
             workspace, wp, wn = _scratch(workspace, lambda: size, q.device, stream)

@@ -28,6 +28,7 @@ namespace {
 constexpr int kPrWaves = 4, kPrRows = kPrWaves * kAtRows;
 constexpr int kPrBlocks = 512;        // blocks that a split makes at most: two per CU
 constexpr int kPrMaxSplit = 16, kPrLeast = 2;  // parts of a tile's keys, tiles of keys of a part at least
+constexpr int kPrFrom = 6;            // tiles of keys that are split at least
 constexpr int kPrGain = 28;           // what a tile of keys costs a block over what a part costs the launch, two per CU
 
 struct PromptParams {
@@ -271,12 +272,14 @@ int64_t prompt_tiles(int64_t seqs, int64_t Tq)
 // 1.2 K / s + b s / 50 + 4 is least at s * s = 60 K / b, and half of that fits the measurements where more than 256
 // blocks share CUs. Queries x keys x heads of width 128, one part and what the rule takes: 1 x 512 x 8: 11.3 and
 // 8.2 us, 64 x 4096 x 32: 71 and 23, 256 x 16384 x 8: 272 and 36, 1024 x 4096 x 32: 84 and 80. Where it takes one part:
-// 1024 x 2048 x 32: 43, in three 58.
+// 1024 x 2048 x 32: 43, in three 58. Below 384 keys the parts do not pay for the join (1 x 256 x 8: 7.9 and 8.3, 320: 9.6
+// and 10.0; 384: 9.8 and 8.3, 511: 13.5 and 10.0).
 int prompt_split(int64_t seqs, int64_t Tq, int64_t Tk, int64_t Hq)
 {
     if (seqs <= 0 || Tq <= 0) return 1;
     const int64_t blocks = prompt_tiles(seqs, Tq) * Hq, keys = Tk / seqs / kAtKeys;
     int s = 1;
+    if (keys < kPrFrom) return s;
     for (int n = 2; n <= kPrMaxSplit && n * blocks <= kPrBlocks && n * kPrLeast <= keys; ++n)
         if (n * n * blocks <= kPrGain * keys * (n * blocks <= kPrBlocks / 2 ? 2 : 1)) s = n;
     return s;

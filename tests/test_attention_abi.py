@@ -284,3 +284,27 @@ def test_numbers_agree_with_the_header():
     src = open(os.path.join(ROOT, "include", "k3moe.h")).read()
     for name in ("ROT_HALVES", "ROT_PAIRS"):
         assert int(re.search(rf"K3MOE_{name} = (\d)", src).group(1)) == getattr(k3, name)
+
+
+@pytest.mark.parametrize("Tq,Tk,H", [(1, 255, 8), (1, 256, 8), (1, 383, 8), (1, 384, 8), (1, 511, 8), (128, 511, 32), (1, 512, 8),
+                                     (64, 4096, 32), (1, 8192, 256), (1, 8192, 257), (129, 4096, 128)])
+def test_attention_makes_a_workspace_wherever_one_is_used(monkeypatch, Tq, Tk, H):
+    """With none given the binding makes one for every call that the library would split with one."""
+    made, real = [], k3.lib()
+
+    class Lib:
+        k3moe_attention_workspace_size = real.k3moe_attention_workspace_size
+
+        @staticmethod
+        def k3moe_attention(*a):
+            made.append(a[-3] is not None)
+            return OK
+
+    monkeypatch.setattr(k3, "lib", lambda: Lib)
+    monkeypatch.setattr(k3, "_elsewhere", lambda dev: False)
+    monkeypatch.setattr(k3, "_changed", lambda t: None)
+    monkeypatch.setattr(k3, "_queue", lambda dev, stream: 0)
+    monkeypatch.setattr(k3, "_scratch", lambda ws, size, device, stream: (ws, A, size()))
+    q, kv = _z(Tq, H, 64, dtype=BF), _z(Tk, 1, 64, dtype=BF)
+    k3.attention(q, kv, kv, _z(2, dtype=I32), q, cu_k=_z(2, dtype=I32))
+    assert made == [k3._attention_bytes(1, Tq, Tk, H, 64) > 0]

@@ -308,3 +308,16 @@ def test_a_workspace_serves_smaller_calls():
         k3.attention(q, k, v, _cu([nq]), a, cu_k=_cu([nk]), workspace=ws)
         k3.attention(q, k, v, _cu([nq]), b, cu_k=_cu([nk]))
         assert torch.equal(a, b) and a.float().abs().sum() > 0
+
+
+@pytest.mark.parametrize("D,Dv", DIMS)
+@pytest.mark.parametrize("nq,nk,H", [(1, 256, 8), (1, 320, 8), (1, 383, 8), (1, 384, 8), (1, 511, 8), (128, 511, 32)])
+def test_a_given_workspace_changes_nothing(D, Dv, nq, nk, H):
+    """Around the fewest keys that are split: the same bits with a workspace given and without."""
+    _case([nq], [nk], H, H // 4, D, Dv, heads=[0, H - 1])
+    q, k, v = _inputs([nq], [nk], H, H // 4, D, Dv)
+    ws = k3.attention_workspace(1, 128, 5000, H, Dv, device=DEV)
+    a, b = (torch.zeros((nq, H, Dv), dtype=BF, device=DEV) for _ in range(2))
+    k3.attention(q, k, v, _cu([nq]), a, cu_k=_cu([nk]))
+    k3.attention(q, k, v, _cu([nq]), b, cu_k=_cu([nk]), workspace=ws)
+    assert torch.equal(a, b)
