@@ -38,6 +38,8 @@ constexpr int kTrWaves = 4, kTrTile = 32;   // keys of a wave's tile
 constexpr int kTrLeast = 2;                 // units of a run at least: a tile for each wave
 constexpr int kTrMaxDraft = 64;             // bits of a word
 constexpr int kTrMaxRuns = 512, kTrMaxRows = 128, kTrFew = 32;
+constexpr int kTrCus = 256, kTrMaxRunRows = kTrCus * kTrMaxRows;   // 512 runs have 32 rows each, 256 have up to 128
+static_assert(kTrMaxRuns * kTrFew <= kTrMaxRunRows, "rows of all runs");
 
 // A segment whose runs k_tree_join joins, left by the first run that begins within it (last < 0: no such run).
 struct TreeCut {
@@ -297,6 +299,7 @@ struct TreeShape {
     static constexpr int kTiles = kTrWaves * kBufs * (KB + VB), kSums = kTrWaves * (DV / 2 + 1) * 64 * 4;
     static constexpr int kLds = kTiles > kSums ? kTiles : kSums;          // the waves' sums take the tiles' place
     static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;             // blocks that fit a CU
+    static_assert(kTrCus * kPerCu <= kTrMaxRuns, "runs");
 };
 
 template <int DK, int DV, bool X8>
@@ -775,7 +778,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p)
 template <int DV>
 k3moe_status launch(void (*kernel)(TreeParams), int lds, TreeParams p, int per_cu, int rows, hipStream_t s)
 {
-    p.runs = 256 * per_cu, p.rows = rows;
+    p.runs = kTrCus * per_cu, p.rows = rows;
     p.ml = p.part + (size_t)2 * p.runs * p.rows * DV;
     p.cut = reinterpret_cast<TreeCut *>(p.ml + (size_t)2 * p.runs * p.rows * 2);
     kernel<<<(unsigned)p.runs, 64 * kTrWaves, lds, s>>>(p);
@@ -808,8 +811,11 @@ k3moe_status launch(const TreeParams &p, bool x8, hipStream_t s)
 
 bool at(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-// For the most runs and rows that any variant has.
-size_t ws_bytes(int v_dim) { return (size_t)2 * kTrMaxRuns * kTrMaxRows * (size_t)(v_dim + 2) * 4 + kTrMaxRuns * sizeof(TreeCut); }
+// For the most runs, and the most rows of all runs, that any variant has.
+size_t ws_bytes(int v_dim)
+{
+    return (size_t)2 * kTrMaxRunRows * (size_t)(v_dim + 2) * 4 + kTrMaxRuns * sizeof(TreeCut);
+}
 
 }  // namespace
 }  // namespace k3moe

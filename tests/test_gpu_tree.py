@@ -325,3 +325,17 @@ def test_two_streams_without_a_workspace():
         b.run(uniform=True, lse=False, out=ob, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(oa, wa) and torch.equal(ob, wb) for oa, ob in outs)
+
+
+@pytest.mark.parametrize("D,Dv", DIMS)
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("n", [1, 8, 16, 64])
+def test_a_workspace_of_the_stated_size_is_enough(D, Dv, x8, n):
+    """Cut ends in every run: nothing behind the workspace is written."""
+    c = Case([40000, 9000, 3], [n, n, 1], 8, 2, D, Dv, page=64, x8=x8)
+    want = c.run(lse=False)[0]
+    size = k3._tree_bytes(8, 2, Dv, n)
+    buf = torch.full((size + 2 ** 20,), 0xab, dtype=torch.uint8, device=DEV)
+    assert buf.data_ptr() % 256 == 0
+    out = c.run(lse=False, ws=buf[:size])[0]
+    assert torch.equal(out, want) and (buf[size:] == 0xab).all()

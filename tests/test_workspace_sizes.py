@@ -35,3 +35,9 @@ def test_an_attention_size_serves_every_smaller_call(heads, v_dim):
                     if s <= seqs and q <= Tq and k <= Tk:
                         assert k3._attention_bytes(s, q, k, heads, v_dim) <= most, (seqs, Tq, Tk, s, q, k)
     assert k3._attention_bytes(1, 8192, 8192, 32, v_dim) >= k3._attention_bytes(1, 64, 4096, 32, v_dim) > 0
+
+
+@pytest.mark.parametrize("v_dim,most", [(64, 18e6), (128, 35e6)])
+def test_a_tree_workspace_is_what_its_variants_use(v_dim, most):
+    """Two ends of 256 runs of 128 rows, or of 512 of 32, each of v_dim + 2 numbers."""
+    assert 2 * 256 * 128 * (v_dim + 2) * 4 <= k3._tree_bytes(8, 2, v_dim, 64) <= most
