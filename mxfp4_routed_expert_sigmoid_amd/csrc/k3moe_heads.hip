@@ -191,7 +191,16 @@ __global__ __launch_bounds__(kHdThreads) void k_heads(HeadsParams p)
                     float ss = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
-                    const float inv = __builtin_amdgcn_rsqf(fmaf(hd_sum<LH>(used ? ss : 0.0f), p.per_dim, p.eps));   // within an ulp
+                    const float mean = fmaf(hd_sum<LH>(used ? ss : 0.0f), p.per_dim, p.eps);
+                    float inv = __builtin_amdgcn_rsqf(mean);   // within an ulp
+                    // squares that fp32 does not hold (or digits of theirs): those heads once more, scaled
+                    if (__ballot(!(mean >= 0x1p-100f && mean < INFINITY))) {
+                        const float by = mean < INFINITY ? mean >= 0x1p-100f ? 1.0f : 0x1p70f : 0x1p-70f;
+                        ss = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) ss = fmaf(y[j] * by, y[j] * by, ss);
+                        inv = __builtin_amdgcn_rsqf(fmaf(hd_sum<LH>(used ? ss : 0.0f), p.per_dim, p.eps * by * by)) * by;
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] = y[j] * inv * g[j];
                 }

@@ -165,3 +165,20 @@ def test_a_cache_beyond_32_bits():
         n, r = int(at[t]) // page, int(at[t]) % page
         assert torch.equal(kc[n, :, r], k[t]) and torch.equal(vc[n, :, r], v[t])
     assert int(torch.count_nonzero(kc[:pages - 7])) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 72])
+@pytest.mark.parametrize("eps", [1e-5, 1e-40])
+def test_heads_of_any_magnitude(D, eps):
+    """Squares beyond fp32, squares below it, and heads of zeros, beside ordinary ones in the same wave."""
+    g = torch.Generator().manual_seed(D)
+    size = torch.tensor([1.0, 1e25, 3e37, 1e-18, 1e-25, 1e-37, 0.0, 1e18, 1e20, 1.0])
+    k = (torch.randn((3, 10, D), generator=g).clamp(-4, 4) * size[None, :, None]).to(BF).to(DEV)
+    gamma = (1 + 0.2 * torch.randn(D, generator=g)).to(DEV)
+    out = torch.full_like(k, 5.0)
+    k3.qk_norm_rope(k, k, None, None, gamma_q=gamma, gamma_k=gamma, eps=eps, q_out=out)
+    torch.cuda.synchronize()
+    eps = float(np.float32(eps))
+    y, tol = ref.heads(ref.unbf16(_bits(k)), gamma.cpu().numpy().astype(float), eps, np.zeros(3), np.zeros(0), False)
+    got = ref.unbf16(_bits(out))
+    assert (np.abs(got - y) <= ref.U16 * (np.abs(y) + tol) + tol + 2.0 ** -133).all(), np.isfinite(got).all((0, 2))
