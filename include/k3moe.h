@@ -528,8 +528,9 @@ k3moe_status k3moe_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint1
  * (k_dim, v_dim): (64, 64), (128, 128) or (192, 128), others
  * K3MOE_E_UNSUPPORTED_SHAPE; 0 < scale <= 2^64. Rows 16-byte aligned, strides
  * up to 2^24 elements, seqs up to 2^30. out and lse overlap none of the inputs.
- * Scores and sums are fp32, a weight below 2^-126 of the row's largest counts as
- * 0; the weights are rounded to bf16 for their product with the values.
+ * Scores and sums are fp32 (a score whose 1.45-fold is beyond fp32 counts as an
+ * infinity: a row with +inf is NaN), a weight below 2^-126 of the row's largest
+ * counts as 0; the weights are rounded to bf16 for their product with the values.
  *   workspace  optional: with one of k3moe_attention_workspace_size bytes few
  *              queries over many keys are split over more of the card; NULL =
  *              they are not. The results of the two agree to their rounding. The

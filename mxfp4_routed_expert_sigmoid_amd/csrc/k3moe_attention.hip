@@ -175,7 +175,7 @@ __global__ __launch_bounds__(64 * kPrWaves, 2) void k_attention(PromptParams p)
     if (per >= x.keys) {          // one part
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         if (p.lse && h == 0)
-            p.lse[(int64_t)(x.q0 + row) * p.Hq + head] = l == 0.0f ? -INFINITY : fmaf(r.m, c, __log2f(l)) * kLn2;
+            p.lse[(int64_t)(x.q0 + row) * p.Hq + head] = l == 0.0f ? -INFINITY : (r.m + __log2f(l)) * kLn2;
         uint16_t *op = p.out + (int64_t)(x.q0 + row) * p.os + (int64_t)head * DV + 4 * h;
 #pragma unroll
         for (int d = 0; d < DV / 32; ++d)
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(64 * kPrWaves, 2) void k_attention(PromptParams p)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<float4 *>(op + 32 * d + 2 * i) = float4{r.o[d][i], r.o[d][i + 1], r.o[d][i + 2], r.o[d][i + 3]};
-        if (h == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = float2{r.m * c, l};   // c > 0: -inf stays
+        if (h == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = float2{r.m, l};
     }
 #endif
 }

@@ -178,7 +178,7 @@ __device__ __forceinline__ void at_barrier()
     asm volatile("" ::: "memory");
 }
 
-// A wave's 32 rows: the queries as B operands, running maximum (of the raw scores) and sum, O^T.
+// A wave's 32 rows: the queries as B operands, running maximum (in powers of two) and sum, O^T.
 template <int DK, int DV>
 struct AttRows {
     bf8 q[DK / 16];
@@ -279,14 +279,27 @@ __device__ __forceinline__ float att_max(const v16f (&s)[2])
     return swap_max(mx);
 }
 
+// Running maxima are held in powers of two, score * c, so that a score beyond fp32 is an infinity there: -inf is no
+// maximum to start from (mx - m is NaN where both are), and +inf makes the row's sums NaN. The product is rounded by
+// itself: contracted with the difference behind it, it would not overflow.
+__device__ __forceinline__ float in_powers(float score, float c)
+{
+#pragma clang fp contract(off)
+    return score * c;
+}
+__device__ __forceinline__ bool raises(float mx, float m) { return mx - m > kAtSlack; }
+// What raising m to mx turns the sums by: 0 from -inf on.
+__device__ __forceinline__ float raised_by(float m, float mx) { return mx == INFINITY ? NAN : __builtin_amdgcn_exp2f(m - mx); }
+
 // Raises the running maximum of the rows where a score exceeds it by the slack; the others keep theirs, so that a row's
-// bits do not depend on what other rows see.
+// bits do not depend on what other rows see. mx: the largest raw score.
 template <int DK, int DV>
 __device__ __forceinline__ void att_raise(AttRows<DK, DV> &r, float mx, float c)
 {
-    const bool up = (mx - r.m) * c > kAtSlack;   // NaN where both are -inf: nothing to raise
+    mx = in_powers(mx, c);
+    const bool up = raises(mx, r.m);
     if (__ballot(up)) {
-        const float a = up ? __builtin_amdgcn_exp2f((r.m - mx) * c) : 1.0f;   // 0 from -inf on
+        const float a = up ? raised_by(r.m, mx) : 1.0f;
         r.m = up ? mx : r.m, r.l *= a;
 #pragma unroll
         for (int d = 0; d < DV / 32; ++d)
@@ -299,7 +312,7 @@ __device__ __forceinline__ void att_raise(AttRows<DK, DV> &r, float mx, float c)
 template <int DK, int DV>
 __device__ __forceinline__ void att_weights(bf8 (&p)[4], AttRows<DK, DV> &r, v16f (&s)[2], float c)
 {
-    const float mc = r.m == -INFINITY ? 0.0f : r.m * c;
+    const float mc = r.m == -INFINITY ? 0.0f : r.m;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -399,7 +412,7 @@ __device__ __forceinline__ void att_tile(AttRows<DK, DV> &r, v16f (&s)[2], float
 #pragma unroll
     for (int i = 0; i < QA; ++i) kread(i);
     att_raise(r, mx, c);
-    const float mc = r.m == -INFINITY ? 0.0f : r.m * c;
+    const float mc = r.m == -INFINITY ? 0.0f : r.m;
     uint32_t p[16];
     float l[2] = {r.l, 0.0f};
     // a pair of scores goes through its operations a step apart each, so that none waits for the one in front of it

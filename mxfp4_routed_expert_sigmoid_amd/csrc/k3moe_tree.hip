@@ -421,17 +421,17 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
             float m = sc[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) m = fmaxf(m, sc[i]);
-            m = swap_max(m);
-            const bool up = (m - mx) * c > kAtSlack;       // as att_raise: the other rows keep theirs
+            m = in_powers(swap_max(m), c);
+            const bool up = raises(m, mx);                 // as att_raise: the other rows keep theirs
             if (__ballot(up)) {
-                const float f = up ? __builtin_amdgcn_exp2f((mx - m) * c) : 1.0f;
+                const float f = up ? raised_by(mx, m) : 1.0f;
                 mx = up ? m : mx, l *= f;
 #pragma unroll
                 for (int d = 0; d < DV / 32; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[d][i] *= f;
             }
-            const float mc = mx == -INFINITY ? 0.0f : mx * c;
+            const float mc = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 sc[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], c, -mc));
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
 #pragma unroll
         for (int w = 0; w < kTrWaves; ++w) {
             const float m = ml[w * 64 + l32], x = ml[w * 64 + 32 + l32];
-            const float g = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - M) * c);
+            const float g = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
             L += m == -INFINITY ? x : x * g;               // without a score above -inf: 0, or NaN
             f = w == wave ? g : f;
         }
@@ -524,7 +524,7 @@ __global__ __launch_bounds__(64 * kTrWaves, (TreeShape<DK, DV, X8>::kPerCu)) voi
 #pragma unroll
             for (int w = 0; w < kTrWaves; ++w) v[i] += sums[(w * R + RW * wave + i) * 64 + lane];
         }
-        row.store<DV, RW>(p, s, v, RW * wave, M * c, L, t0, t1, l32);
+        row.store<DV, RW>(p, s, v, RW * wave, M, L, t0, t1, l32);
 
         left -= t1 - t0;
         if (left <= 0) return;
@@ -710,7 +710,7 @@ __global__ __launch_bounds__(64 * kTrWaves, 1) void k_tree_wide(TreeParams p)
             for (int d = 0; d < DV / 32; ++d)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[16 * d + e] = r.o[d][e];
-            row.store<DV, DV / 2>(p, s, v, 0, r.m * c, l, t0, t0 + n, kAtRows * wave + l32);   // c > 0: -inf stays
+            row.store<DV, DV / 2>(p, s, v, 0, r.m, l, t0, t0 + n, kAtRows * wave + l32);
         }
 
         left -= n;
