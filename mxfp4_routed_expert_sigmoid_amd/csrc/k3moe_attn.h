@@ -10,8 +10,12 @@
 // operands agree; it is the score layout's: slot 8h + j of lane half h is key
 // 4h + j for j < 4 and key 8 + 4h + j - 4 behind that.
 //
-// P is rounded to bf16 for the second product (2^-9 of each weight, whose
-// errors average out over the keys); the sums l are taken of the fp32 values.
+// P is rounded to bf16 for the second product: at most 2^-8 of each weight, as
+// much again as the result's own rounding where one key has all of it, less where
+// the errors of many keys average out (2.2e-3 of the whole against 64 bits where
+// exact weights leave 1.6e-3). The matrix unit takes nothing wider at its rate,
+// and two halves of each weight would double the second product. The sums l are
+// taken of the fp32 values.
 //
 // What bounds it: per tile of 64 keys and heads of 128 a wave has 32 products
 // (1024 cycles of the matrix unit) and 32 scores a lane, each with one

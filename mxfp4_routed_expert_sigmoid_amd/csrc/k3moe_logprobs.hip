@@ -14,14 +14,17 @@
 // its elements reach, and ranks what reaches it. Where too much does (many equal
 // logits) it takes the elements one by one instead.
 //
-// Bound by the logits' bytes: 509 x 163840 in fp32 without a list 56 us (6.0
-// TB/s), with the 8 largest 63 to 70, the 20 largest 80: the list's steps, ballots and a barrier, stand
+// Bound by the logits' bytes: 509 x 163840 in fp32 without a list 60 us (5.6
+// TB/s), with the 8 largest 63 to 67, the 20 largest 79: the list's steps, ballots and a barrier, stand
 // between a block's loads and its end, and the join takes 5. A thread holds 16
 // or 32 elements (64 were slower: fewer blocks on a CU, loads behind each other),
 // read by loads of 16 bytes where a row allows it; each element costs a
 // difference, a product, an exponential, a clamp, two sums and half an operation
-// for the maximum, which half the bytes do not hide: 509 x 163840 in bf16 44 us
-// without a list (3.8 TB/s), with the 8 largest 61.
+// for the maximum, which half the bytes do not hide: 509 x 163840 in bf16 37 us
+// without a list (4.5 TB/s; vector operations issue in every cycle), with the 8
+// largest 59. Rows that are equal in most places, as a grammar's mask leaves them,
+// reach the bound everywhere and are taken one by one: 173 us with 163000 of the
+// 163840 banned.
 // One row: 7.5 us and the join's 4.6, the latencies of two short kernels.
 #include "k3moe_internal.h"
 #include "k3moe_device.h"

@@ -19,6 +19,10 @@
 // (2.3 GB, 5.9 TB/s), 222 over 8 bits (5.4 TB/s; there the expansion, two
 // operations per value with its LDS write, is as long as the loads). One
 // sequence of 4000: 8.7 us and the join's 4.5, the ends of two short kernels.
+// Heads of 64, 32 sequences: 207 us (1.16 GB, 5.6 TB/s). Heads of 192 / 128 over 8
+// bits do not fit the 256 registers that two blocks on a CU leave a lane: 42 spill
+// (156 bytes a lane), and 16 sequences of up to 8000 tokens take 30 us and the
+// join's 5 (bf16, one block per CU and no spill, 48 in all for twice the bytes).
 //
 // More rows (k_tree_wide) are split over the waves, which share tiles of 64 keys
 // as the prompts' kernel does. 64 keys of 128 rows take 1.5 us, the time of one
