@@ -531,6 +531,8 @@ k3moe_status k3moe_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint1
  * Scores and sums are fp32 (a score whose 1.45-fold is beyond fp32 counts as an
  * infinity: a row with +inf is NaN), a weight below 2^-126 of the row's largest
  * counts as 0; the weights are rounded to bf16 for their product with the values.
+ * The sums are divided at the end: values whose sum over the keys, times 2^8, is
+ * beyond fp32 may give infinities.
  *   workspace  optional: with one of k3moe_attention_workspace_size bytes few
  *              queries over many keys are split over more of the card; NULL =
  *              they are not. The results of the two agree to their rounding. The
